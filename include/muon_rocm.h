@@ -111,7 +111,10 @@ typedef struct muon_matrix {
 #define MUON_KCLASS_SPEC_REDUCE 16     /* SVD entropy: matrix-vector product from the partials */
 #define MUON_KCLASS_SPEC_BISECT 17     /* SVD entropy: eigenvalues by Sturm bisection */
 #define MUON_KCLASS_SPEC_ENTROPY 18    /* SVD entropy: normalisation and entropy */
-#define MUON_KCLASS_COUNT 19
+#define MUON_KCLASS_NORM_FORWARD 19    /* normalisation layer: rows normalised, scaled and shifted */
+#define MUON_KCLASS_NORM_BACKWARD 20   /* its input gradient, with the blocks' weight-gradient sums */
+#define MUON_KCLASS_NORM_WGRAD 21      /* the weight and bias gradients from those sums */
+#define MUON_KCLASS_COUNT 22
 
 /* Returns MUON_ABI_VERSION. Host only. */
 int muon_abi_version(void);
@@ -303,6 +306,77 @@ void adamw_default_hparams(adamw_hparams* hp);
  * w, m, v, g ranges overlap), TOO_LARGE (numel above 2^40), HIP. */
 int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step,
                void* stream);
+
+/* ---- Normalisation layers and their gradients ---------------------------------------
+ * The layers whose parameters the hybrid optimizer keeps on AdamW (affine layer norm, the
+ * query and key RMS norms), and the modulated norm whose scale and shift the blocks'
+ * [6H, H] adaLN matrices produce for every sample. Rows of `cols` elements, split evenly
+ * into `groups` of consecutive rows; row r in group g = r / (rows / groups):
+ *   mean = (1/cols) sum x              (0 under MUON_NORM_RMS)
+ *   rstd = 1 / sqrt((1/cols) sum (x - mean)^2 + eps)
+ *   h = (x - mean) rstd,   y = h (weight_offset + w[g]) + b[g]
+ * One group is an affine norm, one group a sample is adaLN (there weight_offset 1: the
+ * projection gives 1 + scale). Backward, from dy with a = dy (weight_offset + w[g]):
+ *   dx = rstd (a - (1/cols) sum a - h (1/cols) sum a h)   (RMS: without the first sum)
+ *   dw[g] = sum over the group's rows of dy h,   db[g] = sum of dy
+ * Arithmetic and statistics are fp32 whatever the types; each output is rounded once.
+ * Sums run in a fixed order: identical calls give identical bits. */
+#define MUON_DTYPE_F32 0
+#define MUON_DTYPE_BF16 1
+#define MUON_DTYPE_F16 2
+#define MUON_NORM_LAYER 0
+#define MUON_NORM_RMS 1
+#define MUON_NORM_MAX_COLS 16384
+
+typedef struct norm_desc {
+    int64_t rows, cols, groups; /* groups >= 1 divides rows */
+    int64_t inner;              /* >= 1, divides rows: see norm_rows */
+    int32_t kind;               /* MUON_NORM_* */
+    int32_t dtype;              /* of x, y, dy, dx */
+    int32_t wdtype;             /* of w, b, dw, db: MUON_DTYPE_F32 or dtype */
+    float eps;                  /* finite, > 0 */
+    float weight_offset;        /* finite; without effect where w is NULL */
+} norm_desc;
+
+/* A [rows, cols] tensor whose row r starts at data + (r / inner) stride0 +
+ * (r % inner) stride1 elements (a query view [tokens, heads, cols] of a fused
+ * projection: inner = heads). Elements of a row are adjacent. Strides are >= 0; rows that
+ * are written must not overlap each other. data: aligned to its element. */
+typedef struct norm_rows {
+    void* data;
+    int64_t stride0, stride1;
+} norm_rows;
+
+/* A [groups, cols] parameter tensor, group g at data + g stride elements; data NULL =
+ * absent. data: aligned to its element. */
+typedef struct norm_param {
+    void* data;
+    int64_t stride;
+} norm_param;
+
+/* y from x. w and b may be absent (factor 1, shift 0). mean and rstd: DEVICE arrays of
+ * `rows` floats that receive the rows' statistics for the backward pass, each NULL when
+ * not wanted; mean is not written under MUON_NORM_RMS. y may be x itself (same pointer
+ * and strides). One launch.
+ * Errors: INVALID_ARG, ALIGN, ALIAS (y, mean or rstd overlaps another buffer, by the
+ * span from its first to its last element), TOO_LARGE (cols above MUON_NORM_MAX_COLS,
+ * rows or groups of 2^31 or more, a span above 2^46 elements), HIP. rows == 0 or cols == 0 is a
+ * no-op. */
+int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_param* w, const norm_param* b,
+                 const norm_rows* y, float* mean, float* rstd, void* stream);
+
+/* Workspace in bytes of norm_backward with dw or db. Host only. Errors: as norm_forward's
+ * for desc, INVALID_ARG for NULL bytes. */
+int norm_backward_workspace_bytes(const norm_desc* desc, size_t* bytes);
+
+/* dx, dw and db from dy and the forward pass's x, mean (LAYER) and rstd. dw and db are
+ * overwritten, zeros where rows == 0; absent ones are not computed, and without both no
+ * workspace is needed. dw without w is INVALID_ARG. dx may be dy or x itself. One launch,
+ * and a second that adds the blocks' sums where a group spans several blocks.
+ * desc->eps is not used. Errors: as norm_forward, and WORKSPACE. */
+int norm_backward(const norm_desc* desc, const norm_rows* dy, const norm_rows* x, const norm_param* w,
+                  const float* mean, const float* rstd, const norm_rows* dx, const norm_param* dw,
+                  const norm_param* db, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- Singular-spectrum diagnostic ----------------------------------------------------
  * SVD entropy of "Muon is Scalable for LLM Training", Sec. 3.4 (Dynamics of Singular

@@ -34,3 +34,10 @@ from .binding import (  # noqa: F401
     timing_read,
     workspace_bytes,
 )
+from .norms import (  # noqa: F401
+    layer_norm,
+    norm_backward,
+    norm_backward_workspace_bytes,
+    norm_forward,
+    rms_norm,
+)

@@ -6,6 +6,7 @@ library is not built, or no GPU is present, calls raise; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -28,13 +29,14 @@ SCALE_RMS = 2       # 0.2 / RMS(O), Eq. 6
 KCLASS_NAMES = ("cast", "frob", "gram", "poly", "apply", "apply_final", "rownorm_rows",
                 "colnorm_partial", "colnorm_finalize", "colnorm_apply", "rms_finalize",
                 "scaled_update", "adamw", "spec_gram", "spec_house", "spec_pass", "spec_reduce",
-                "spec_bisect", "spec_entropy")
+                "spec_bisect", "spec_entropy", "norm_forward", "norm_backward", "norm_wgrad")
 
 EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_default_hparams",
             "muon_workspace_bytes", "ns5_plan", "muon_step", "ns5_batched", "rownorm_update",
             "rownorm_update_noalloc",
             "adamw_default_hparams", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy",
             "rownorm_shard_workspace_bytes", "rownorm_shard_colsq", "rownorm_shard_apply",
+            "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
 
@@ -66,6 +68,20 @@ class AdamWParam(ctypes.Structure):
 class MuonShard(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("full_rows", ctypes.c_int64),
                 ("w", ctypes.c_void_p), ("m", ctypes.c_void_p), ("g", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("inner", ctypes.c_int64), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class NormRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride0", ctypes.c_int64), ("stride1", ctypes.c_int64)]
+
+
+class NormParam(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 class MuonError(RuntimeError):
@@ -119,13 +135,18 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                         ctypes.POINTER(vp), vp, sz, vp]
     lib.rownorm_shard_apply.argtypes = [ctypes.POINTER(MuonShard), i32, ctypes.POINTER(MuonHParams),
                                         ctypes.POINTER(vp), vp, sz, vp]
+    desc, rows, param = ctypes.POINTER(NormDesc), ctypes.POINTER(NormRows), ctypes.POINTER(NormParam)
+    lib.norm_forward.argtypes = [desc, rows, param, param, rows, vp, vp, vp]
+    lib.norm_backward_workspace_bytes.argtypes = [desc, ctypes.POINTER(ctypes.c_size_t)]
+    lib.norm_backward.argtypes = [desc, rows, rows, param, vp, vp, rows, param, param, vp, sz, vp]
     lib.muon_ceiling_copy.argtypes = [vp, vp, i64, vp]
     lib.muon_ceiling_mfma.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
     lib.muon_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
     for name in ("muon_step", "ns5_batched", "rownorm_update", "rownorm_update_noalloc", "muon_workspace_bytes",
                  "ns5_plan", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
-                 "rownorm_shard_colsq", "rownorm_shard_apply", "muon_ceiling_copy", "muon_ceiling_mfma",
+                 "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
+                 "norm_backward", "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
@@ -230,6 +251,32 @@ def _torch_stream(stream, device):
     if isinstance(stream, torch.cuda.Stream):
         return stream
     return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
+_dtype_codes = None
+
+
+def dtype_codes():
+    """{torch dtype: MUON_DTYPE_* code} of the element types the operators take."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _dtype_codes
+
+
+_same_place = contextlib.nullcontext()
+
+
+def device_and_stream(device, stream):
+    """Context in which `device` is current and allocations belong to `stream` (None: the
+    device's current stream), for calls that allocate outputs or workspaces."""
+    torch = _torch()
+    if stream is not None:
+        return torch.cuda.stream(_torch_stream(stream, device))
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _same_place
 
 
 def _scratch(nbytes, device, stream):

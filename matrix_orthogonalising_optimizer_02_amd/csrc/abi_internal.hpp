@@ -1,10 +1,13 @@
 // Host-side entry points shared between the C-ABI source files of libmuon_rocm.so.
 #pragma once
 
+#include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
+#include <functional>
 #include <string>
+#include <vector>
 
 #include "../../include/muon_rocm.h"
 
@@ -12,6 +15,20 @@ namespace muon {
 
 // Sets this thread's muon_last_error() text and returns `code`; an empty text clears it.
 int set_last_error(int code, const std::string& what);
+
+// Byte range of a buffer of a call, for the overlap check.
+struct Range {
+    uintptr_t lo, hi;
+    bool write;
+};
+
+// MUON_ERR_ALIAS (with the error text set) when a written range overlaps another one.
+// Sorts the ranges.
+int check_overlaps(std::vector<Range>& ranges);
+
+// Runs `launch`, bracketed by events of kernel class `cls` while timing is enabled;
+// MUON_ERR_HIP (with the error text set) when it fails.
+int run_timed(int cls, hipStream_t stream, const char* name, const std::function<hipError_t()>& launch);
 
 // rownorm_update on a scratch buffer of scratch_cap bytes that get_scratch returns for
 // the current device (NULL with *error set on failure). Validates and plans on the host

@@ -541,23 +541,6 @@ double dir_scale(const muon_hparams& hp, int64_t n) {
     return double(hp.rms_scale) * std::sqrt(h);
 }
 
-struct Range {
-    uintptr_t lo, hi;
-    bool write;
-};
-
-int check_overlaps(std::vector<Range>& rs) {
-    std::sort(rs.begin(), rs.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
-    uintptr_t hi_any = 0, hi_write = 0;
-    for (const Range& r : rs) {
-        if (r.hi <= r.lo) continue;
-        if (r.lo < (r.write ? hi_any : hi_write)) return fail(MUON_ERR_ALIAS, "buffers overlap");
-        hi_any = std::max(hi_any, r.hi);
-        if (r.write) hi_write = std::max(hi_write, r.hi);
-    }
-    return MUON_OK;
-}
-
 int check_monitor(const float* update_rms, int32_t count, std::vector<Range>& ranges) {
     if (!update_rms || count == 0) return MUON_OK;
     if (reinterpret_cast<uintptr_t>(update_rms) & 3) return fail(MUON_ERR_ALIGN, "update_rms not 4-byte aligned");
@@ -1177,6 +1160,22 @@ int run_spectrum(const std::vector<SpMat>& g, const float* const* w, char* ws, d
 }  // namespace
 
 int set_last_error(int code, const std::string& what) { return fail(code, what); }
+
+int check_overlaps(std::vector<Range>& rs) {
+    std::sort(rs.begin(), rs.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    uintptr_t hi_any = 0, hi_write = 0;
+    for (const Range& r : rs) {
+        if (r.hi <= r.lo) continue;
+        if (r.lo < (r.write ? hi_any : hi_write)) return fail(MUON_ERR_ALIAS, "buffers overlap");
+        hi_any = std::max(hi_any, r.hi);
+        if (r.write) hi_write = std::max(hi_write, r.hi);
+    }
+    return MUON_OK;
+}
+
+int run_timed(int cls, hipStream_t stream, const char* name, const std::function<hipError_t()>& launch) {
+    return run_kernel(cls, stream, name, launch);
+}
 
 // The RowNorm step on a scratch buffer the library holds (the allocation-free entry
 // point, csrc/noalloc.hip). Every argument is validated and the step planned on the

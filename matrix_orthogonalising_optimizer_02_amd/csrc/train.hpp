@@ -1,0 +1,69 @@
+// Kernel descriptors and host-side launchers of the training-step operators beside the
+// optimizer's own kernels: normalisation layers, many-tensor AdamW and the gradient norm.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace muon {
+
+enum ElemType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };  // MUON_DTYPE_*
+
+inline int elem_size(int t) { return t == kF32 ? 4 : 2; }
+
+// ---- normalisation layers --------------------------------------------------------
+// Row r of a strided [rows, cols] tensor starts at data + (r / inner) s0 + (r % inner) s1
+// elements.
+struct RowsPtr {
+    void* data;
+    int64_t s0, s1;
+};
+
+struct NormArgs {
+    RowsPtr x, y;              // backward: y is dx
+    RowsPtr dy;                // backward only
+    const void* w;             // [groups, cols] with stride w_stride; null = no weight (factor 1)
+    const void* b;             // forward only; null = no bias
+    int64_t w_stride, b_stride;
+    float* mean;               // written by the forward pass, read by the backward pass; null for rms
+    float* rstd;
+    void* dw;                  // backward: gradients in wdtype, null = not wanted
+    void* db;
+    int64_t dw_stride, db_stride;
+    float* partial;            // backward: [2][groups * chunks][cols] when chunks > 1
+    int32_t rows_per_group;
+    int32_t groups;
+    int32_t cols;
+    int32_t inner;             // >= 1
+    uint32_t inner_mul;        // r / inner = (mulhi(r, inner_mul) + r) >> inner_shift, 33-bit sum, for inner > 1
+    int32_t inner_shift;
+    int32_t chunks;            // blocks of a group
+    int32_t chunk_rows;        // rows of a block: ceil(rows_per_group / chunks)
+    int32_t wdtype;
+    float eps, offset;
+    float inv_cols;
+};
+
+// Columns up to this fit the registers of one 1024-thread block, 16 a thread.
+constexpr int kNormMaxCols = 16 * 1024;
+
+// How the kernels split a norm's rows: `lanes` threads share a row (a power of two up to
+// 64, or whole waves), each holding `vecs` 16-byte vectors of it.
+struct NormPlan {
+    int lanes;
+    int vecs;
+    int threads;       // of a block
+    int rows_at_once;  // rows that a block holds at a time
+    int chunks;
+    int chunk_rows;
+};
+NormPlan plan_norm_forward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);
+NormPlan plan_norm_backward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);
+
+hipError_t launch_norm_forward(bool rms, int dtype, const NormPlan& p, const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_backward(bool rms, int dtype, const NormPlan& p, const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_wgrad(const NormArgs& a, hipStream_t s);
+
+}  // namespace muon

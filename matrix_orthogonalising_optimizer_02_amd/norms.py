@@ -1,0 +1,247 @@
+"""Normalisation layers with their gradients, over torch tensors.
+
+The layers beside the block matrices of a transformer: the affine layer norm and the
+query and key RMS norms, whose weights the hybrid optimizer keeps on AdamW, and the
+modulated norm (adaLN) that takes a scale and a shift per sample from a [6H, H]
+projection. `norm_forward` and `norm_backward` are the library's two calls; `layer_norm`
+and `rms_norm` are the same for torch.autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+from . import binding as B
+
+NORM_LAYER, NORM_RMS = 0, 1
+MAX_COLS = 16384
+_KINDS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+
+
+def _row_levels(t, name):
+    """The leading dimensions of t as at most two (size, stride) levels, innermost first."""
+    if t.is_contiguous():
+        n = t.numel() // t.shape[-1] if t.shape[-1] else 0
+        return [(n, t.shape[-1])] if n > 1 else []
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    levels = []
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if levels and stride == levels[-1][0] * levels[-1][1]:
+            levels[-1] = (levels[-1][0] * size, levels[-1][1])
+        else:
+            levels.append((size, stride))
+    if len(levels) > 2:
+        raise ValueError(f"{name} has rows at more than two strides; make it contiguous")
+    return levels
+
+
+def _layout(tensors):
+    """(inner, row structs) for [(tensor, name)] of one shape."""
+    levels = [_row_levels(t, name) for t, name in tensors]
+    inner = 1
+    for lv, (_, name) in zip(levels, tensors):
+        if len(lv) == 2:
+            if inner not in (1, lv[0][0]):
+                raise ValueError(f"{name} splits its rows unlike another tensor of the call; make it contiguous")
+            inner = lv[0][0]
+    rows = []
+    for lv, (t, _) in zip(levels, tensors):
+        if len(lv) == 2:
+            s0, s1 = lv[1][1], lv[0][1]
+        else:
+            s1 = lv[0][1] if lv else 0
+            s0 = s1 * inner
+        rows.append(B.NormRows(t.data_ptr() or None, s0, s1))
+    return inner, rows
+
+
+def _check(t, name, device=None, dtype=None, shape=None):
+    torch = B._torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on a GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must live on {device}")
+
+
+def _param(t, name, cols, groups, device, dtypes):
+    """(groups, struct) of a weight or bias whose last dimension is the row's."""
+    _check(t, name, device)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dict.fromkeys(dtypes))}")
+    if t.dim() < 1 or t.shape[-1] != cols:
+        raise ValueError(f"{name} must have {cols} elements in its last dimension")
+    n = t.numel() // cols if cols else 1
+    if groups is not None and n != groups:
+        raise ValueError(f"{name} must have {groups} rows, as the weight")
+    levels = _row_levels(t, name)
+    if len(levels) > 1:
+        raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
+    return n, B.NormParam(t.data_ptr() or None, levels[0][1] if levels else cols)
+
+
+def _desc(x, weight, bias, kind, eps, weight_offset, inner):
+    """(descriptor, weight struct, bias struct) of a call on x."""
+    torch = B._torch()
+    if kind not in _KINDS:
+        raise ValueError("kind must be 'layer' or 'rms'")
+    codes = B.dtype_codes()
+    if x.dtype not in codes:
+        raise ValueError("x must be float32, bfloat16 or float16")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    groups, w, b, wdtype = None, None, None, torch.float32
+    if weight is not None:
+        groups, w = _param(weight, "weight", cols, None, x.device, (torch.float32, x.dtype))
+        wdtype = weight.dtype
+    if bias is not None:
+        allowed = (wdtype,) if weight is not None else (torch.float32, x.dtype)
+        groups, b = _param(bias, "bias", cols, groups, x.device, allowed)
+        wdtype = bias.dtype
+    d = B.NormDesc(rows, cols, 1 if groups is None else groups, inner, _KINDS[kind], codes[x.dtype], codes[wdtype],
+                   eps, weight_offset)
+    return d, w, b
+
+
+def norm_forward(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1e-6,
+                 weight_offset: float = 0.0, out=None, stats: bool = True, stream=None):
+    """(y, mean, rstd) of y = (x - mean) rstd (weight_offset + weight) + bias over x's last dimension.
+
+    kind "rms" takes no mean away (mean is None). weight and bias: float32 or x's dtype,
+    [cols] for all rows, or one row for each of `groups` equal runs of x's rows (adaLN's
+    scale and shift of each sample, e.g. [samples, cols], with weight_offset 1). x's rows
+    may be strided (a slice of a fused projection). mean and rstd: float32 [rows], for
+    norm_backward; neither is computed into memory with stats=False (both None then). out:
+    receives y, and may be x.
+    """
+    torch = B._torch()
+    _check(x, "x")
+    with B.device_and_stream(x.device, stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        if out is not None:
+            _check(out, "out", x.device, x.dtype, x.shape)
+        inner, (rx, ry) = _layout(((x, "x"), (y, "out")))
+        d, w, b = _desc(x, weight, bias, kind, eps, weight_offset, inner)
+        mean = rstd = None
+        if stats:
+            rstd = torch.empty(d.rows, dtype=torch.float32, device=x.device)
+            if kind == "layer":
+                mean = torch.empty(d.rows, dtype=torch.float32, device=x.device)
+        rc = B.load_library().norm_forward(d, rx, w, b, ry, mean.data_ptr() or None if mean is not None else None,
+                                           rstd.data_ptr() or None if rstd is not None else None,
+                                           B._stream_handle(stream, x.device))
+    B._check(rc, "norm_forward")
+    return y, mean, rstd
+
+
+def norm_backward_workspace_bytes(desc: "B.NormDesc") -> int:
+    out = ctypes.c_size_t(0)
+    B._check(B.load_library().norm_backward_workspace_bytes(desc, out), "norm_backward_workspace_bytes")
+    return int(out.value)
+
+
+def norm_backward(dy, x, weight, mean, rstd, *, kind: str = "layer", weight_offset: float = 0.0,
+                  weight_grad: bool = True, bias_grad: bool = True, out=None, workspace=None, stream=None,
+                  grad_shape=None, grad_dtype=None):
+    """(dx, dweight, dbias) from dy and the forward pass's x, mean and rstd.
+
+    dweight and dbias have weight's shape and dtype; each is None when not asked for (and
+    dweight without a weight). A norm with a bias and no weight names its bias's shape and
+    dtype as grad_shape and grad_dtype. out: receives dx, and may be dy or x. workspace:
+    optional uint8 device buffer of norm_backward_workspace_bytes().
+    """
+    torch = B._torch()
+    _check(x, "x")
+    _check(dy, "dy", x.device, x.dtype, x.shape)
+    with B.device_and_stream(x.device, stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        if out is not None:
+            _check(out, "out", x.device, x.dtype, x.shape)
+        inner, (rdy, rx, rdx) = _layout(((dy, "dy"), (x, "x"), (dx, "out")))
+        dbias = None
+        if bias_grad:
+            if weight is None and grad_shape is None:
+                grad_shape = x.shape[-1:]
+            shape = weight.shape if weight is not None else tuple(grad_shape)
+            dtype = weight.dtype if weight is not None else (grad_dtype or torch.float32)
+            dbias = torch.empty(shape, dtype=dtype, device=x.device)
+        d, w, db = _desc(x, weight, dbias, kind, 1.0, weight_offset, inner)
+        dweight = dw = None
+        if weight_grad and weight is not None:
+            dweight = torch.empty(weight.shape, dtype=weight.dtype, device=x.device)
+            dw = B.NormParam(dweight.data_ptr() or None, d.cols)
+        for t, nm in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _check(t, nm, x.device, torch.float32)
+                if t.numel() != d.rows or not t.is_contiguous():
+                    raise ValueError(f"{nm} must be a contiguous float32 tensor with one entry per row")
+        ws, wsb = None, 0
+        if workspace is not None:
+            ws, wsb = workspace.data_ptr(), workspace.numel()
+        elif dw is not None or db is not None:
+            wsb = norm_backward_workspace_bytes(d)
+            if wsb:
+                workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+                ws = workspace.data_ptr()
+        rc = B.load_library().norm_backward(d, rdy, rx, w, mean.data_ptr() or None if mean is not None else None,
+                                            rstd.data_ptr() or None if rstd is not None else None, rdx, dw, db, ws, wsb,
+                                            B._stream_handle(stream, x.device))
+    B._check(rc, "norm_backward")
+    return dx, dweight, dbias
+
+
+_function = None
+
+
+def _autograd_function():
+    """The autograd function, made at its first use: torch is imported lazily."""
+    global _function
+    if _function is not None:
+        return _function
+    torch = B._torch()
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, kind, eps, weight_offset):
+            y, mean, rstd = norm_forward(x, weight, bias, kind=kind, eps=eps, weight_offset=weight_offset)
+            ctx.save_for_backward(x, weight, mean, rstd)
+            ctx.kind, ctx.weight_offset = kind, weight_offset
+            ctx.bias = None if bias is None else (bias.shape, bias.dtype)
+            return y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            x, weight, mean, rstd = ctx.saved_tensors
+            bias_grad = ctx.bias is not None and ctx.needs_input_grad[2]
+            shape, dtype = ctx.bias or (None, None)
+            try:
+                _layout(((dy, "dy"), (x, "x")))
+            except ValueError:  # an expanded or transposed gradient
+                dy = dy.contiguous()
+            dx, dw, db = norm_backward(dy, x, weight, mean, rstd, kind=ctx.kind, weight_offset=ctx.weight_offset,
+                                       weight_grad=ctx.needs_input_grad[1], bias_grad=bias_grad,
+                                       grad_shape=shape, grad_dtype=dtype)
+            return dx if ctx.needs_input_grad[0] else None, dw, None if db is None else db.view(shape), None, None, None
+
+    _function = Norm
+    return Norm
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
+    """norm_forward's y for torch.autograd: affine with weight and bias of [cols], adaLN
+    with one row a sample and weight_offset 1, plain without either."""
+    return _autograd_function().apply(x, weight, bias, "layer", eps, weight_offset)
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, weight_offset: float = 0.0):
+    """x / sqrt(mean(x^2) + eps) (weight_offset + weight) for torch.autograd."""
+    return _autograd_function().apply(x, weight, None, "rms", eps, weight_offset)
