@@ -114,7 +114,12 @@ typedef struct muon_matrix {
 #define MUON_KCLASS_NORM_FORWARD 19    /* normalisation layer: rows normalised, scaled and shifted */
 #define MUON_KCLASS_NORM_BACKWARD 20   /* its input gradient, with the blocks' weight-gradient sums */
 #define MUON_KCLASS_NORM_WGRAD 21      /* the weight and bias gradients from those sums */
-#define MUON_KCLASS_COUNT 22
+#define MUON_KCLASS_TENSOR_PLAN 22     /* descriptor tables of many-tensor calls (set-up) */
+#define MUON_KCLASS_ADAMW_MULTI 23     /* AdamW over many tensors, 32- or 8-bit states */
+#define MUON_KCLASS_GRAD_NORM 24       /* sums of squares of the gradients, block by block */
+#define MUON_KCLASS_GRAD_TOTAL 25      /* the tensors' norms, their total and the clip factor */
+#define MUON_KCLASS_GRAD_SCALE 26      /* gradients scaled in place */
+#define MUON_KCLASS_COUNT 27
 
 /* Returns MUON_ABI_VERSION. Host only. */
 int muon_abi_version(void);
@@ -307,6 +312,125 @@ void adamw_default_hparams(adamw_hparams* hp);
 int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step,
                void* stream);
 
+/* ---- Many tensors in one launch ------------------------------------------------------
+ * The hybrid optimizer's AdamW side has hundreds of small tensors (238 in the 15B-scale
+ * model). The calls below read their descriptors from a table in device memory that a
+ * plan call writes once, so that a step is one launch whatever the count. */
+
+/* Element types of the operators from here on. */
+#define MUON_DTYPE_F32 0
+#define MUON_DTYPE_BF16 1
+#define MUON_DTYPE_F16 2
+
+/* A written table. Filled by a plan call, read-only to the caller; valid while `device`
+ * and the tensors that it describes live. */
+typedef struct tensor_plan {
+    void* device;    /* the caller's buffer */
+    size_t bytes;    /* the part of it in use */
+    int32_t kind;    /* which plan call filled it */
+    int32_t count;   /* tensors, empty ones included */
+    int32_t blocks;  /* thread blocks of a launch */
+    int32_t reserved;
+} tensor_plan;
+
+/* ---- AdamW with 32-bit or 8-bit states ------------------------------------------------
+ * adamw_step()'s formula with g' = grad_scale g, for each tensor on its own:
+ *   m <- b1 m + (1 - b1) g',  v <- b2 v + (1 - b2) g'^2,  t = step + 1
+ *   W <- (1 - lr wd) W - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * with lr and wd times the tensor's lr_scale and wd_scale. W is fp32; copy, if given,
+ * receives the new W rounded to 16 bits (the weights of the next forward pass). g is
+ * fp32, bf16 or fp16.
+ * state_bits 32: m and v are numel floats.
+ * state_bits 8: m and u = sqrt(v) are numel bytes of e4m3 (1 sign, 4 exponent, 3 mantissa
+ * bits, largest value 448) and a float of scale for every 256 consecutive elements (the
+ * last block may be shorter): m = m_scale code, v = (v_scale code)^2. The step runs in
+ * fp32 on these values; W is updated from the unrounded new m and v. Then each block's
+ * scale becomes its largest magnitude / 448 (0, with all codes 0, where that magnitude is
+ * below 1e-30) and its values are rounded stochastically: with b2 = 0.999 a u moves by at
+ * most 0.05% a step where its gradient shrinks, far below the 6% to 12% between codes, so
+ * that rounding to nearest would hold it for good. A u above 0 is never rounded to 0 (the
+ * update would lose its denominator). A block with a non-finite new m or v gets NaN as
+ * that state's scale, and so NaN in all its 256 elements from the next step on.
+ * The rounding bits are a function of (seed, step, position of the tensor in the list,
+ * index of the element) alone: all 32-bit arithmetic, with
+ *   mix(x): x = (x ^ x >> 16) 0x6A09E667; x = (x ^ x >> 15) 0xBB67AE85; x ^ x >> 16
+ *   key = mix(mix(mix(mix(seed_lo) + seed_hi) + step_lo) + 0x510E527F tensor)
+ *   bits = mix(0x9E3779B9 i_lo + 0x510E527F i_hi + key)
+ * the low 16 round m, the high 16 u. A magnitude a (of 448) between two codes goes up
+ * where its fraction, cut to 20 bits, plus bits / 2^16 reaches 1. */
+typedef struct adamw_tensor {
+    int64_t numel;
+    float* w;
+    void* copy;       /* numel 16-bit elements of copy_dtype, NULL = not wanted */
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;   /* state_bits 8: ceil(numel / 256) floats each; else ignored */
+    float* v_scale;
+    int32_t g_dtype;    /* MUON_DTYPE_* */
+    int32_t copy_dtype; /* MUON_DTYPE_BF16 or _F16 where copy is given */
+    int32_t state_bits; /* 8 or 32 */
+    float lr_scale;     /* finite */
+    float wd_scale;     /* finite */
+} adamw_tensor;
+
+/* Bytes of the device buffer for adamw_multi_plan. Host only; reads numel and state_bits.
+ * Errors: INVALID_ARG, TOO_LARGE. */
+int adamw_multi_plan_bytes(const adamw_tensor* tensors, int32_t count, size_t* bytes);
+
+/* Checks `count` tensors (host array), enqueues the table's writing into `device` (256-byte
+ * aligned, `bytes` of adamw_multi_plan_bytes) on `stream` and fills *plan. Steps with this
+ * plan come after it on the stream. A gradient at another address needs a new plan call
+ * (into the same buffer, if it follows the last step on the stream).
+ * Errors: INVALID_ARG (NULL pointers, negative numel, unknown type or bits, non-finite
+ * scale), ALIGN (w, m, v, g, copy not 16-byte aligned, scales not 4-byte), ALIAS (any two
+ * of all w, copy, m, v, m_scale, v_scale, g ranges or the table overlap, gradients with each
+ * other excepted), WORKSPACE (device
+ * NULL or too small), TOO_LARGE (2^40 elements in a tensor, 2^31 blocks), HIP. */
+int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* device, size_t bytes, tensor_plan* plan,
+                     void* stream);
+
+/* One step at 0-based step `step` over the plan's tensors: one launch.
+ * grad_scale: DEVICE float (the clip factor of grad_norm, or one over a loss scale), NULL = 1.
+ * seed: of the stochastic rounding; without effect on 32-bit states. Two calls on one plan
+ * at the same time race, as on the states themselves.
+ * Errors: INVALID_ARG (as adamw_step, eps below 2^-126, a plan of another kind), ALIGN,
+ * HIP. */
+int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t step, uint64_t seed,
+                     const float* grad_scale, void* stream);
+
+/* ---- Gradient norm and clipping --------------------------------------------------------
+ * n_i = l2 norm of tensor i, total = sqrt(sum n_i^2), factor = min(1, max_norm / (total +
+ * 1e-6)): on the device, for adamw_multi_step's grad_scale and grad_scale() below. Squares
+ * and sums are fp64, in a fixed order. */
+typedef struct grad_tensor {
+    void* g;        /* DEVICE, aligned to its element; only grad_scale writes it */
+    int64_t numel;  /* 0: skipped, its norm is 0 */
+    int32_t dtype;  /* MUON_DTYPE_* */
+    int32_t reserved;
+} grad_tensor;
+
+/* Bytes of the device buffer (table and partial sums) for grad_norm_plan. Host only. */
+int grad_norm_plan_bytes(const grad_tensor* grads, int32_t count, size_t* bytes);
+
+/* As adamw_multi_plan. The buffer also holds the sums of a running grad_norm: calls on one
+ * plan must not overlap in time.
+ * Errors: INVALID_ARG, ALIGN (g not aligned to its element), ALIAS (two tensors, or one and
+ * the table, overlap), WORKSPACE, TOO_LARGE, HIP. */
+int grad_norm_plan(const grad_tensor* grads, int32_t count, void* device, size_t bytes, tensor_plan* plan,
+                   void* stream);
+
+/* total[0] = the norm over all of the plan's tensors, total[1] = the clip factor; norms[i] =
+ * tensor i's norm, NULL = not wanted. DEVICE arrays of 2 and `count` floats. A NaN gradient
+ * gives NaN for both, an infinite one an infinite norm and the factor 0. Two launches.
+ * Errors: INVALID_ARG (NULL plan or total, another plan's kind, max_norm not > 0 and
+ * finite), ALIGN, ALIAS (total and norms overlap each other or the table), HIP. */
+int grad_norm(const tensor_plan* plan, float max_norm, float* total, float* norms, void* stream);
+
+/* g <- factor g in place, rounded to g's type, for the plan's tensors; factor: DEVICE float.
+ * Nothing is read or written where factor is 1. One launch. Errors: INVALID_ARG, ALIGN, HIP. */
+int grad_scale(const tensor_plan* plan, const float* factor, void* stream);
+
 /* ---- Normalisation layers and their gradients ---------------------------------------
  * The layers whose parameters the hybrid optimizer keeps on AdamW (affine layer norm, the
  * query and key RMS norms), and the modulated norm whose scale and shift the blocks'
@@ -321,9 +445,6 @@ int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp
  *   dw[g] = sum over the group's rows of dy h,   db[g] = sum of dy
  * Arithmetic and statistics are fp32 whatever the types; each output is rounded once.
  * Sums run in a fixed order: identical calls give identical bits. */
-#define MUON_DTYPE_F32 0
-#define MUON_DTYPE_BF16 1
-#define MUON_DTYPE_F16 2
 #define MUON_NORM_LAYER 0
 #define MUON_NORM_RMS 1
 #define MUON_NORM_MAX_COLS 16384

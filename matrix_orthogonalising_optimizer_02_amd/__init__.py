@@ -34,6 +34,10 @@ from .binding import (  # noqa: F401
     timing_read,
     workspace_bytes,
 )
+from .multi import (  # noqa: F401
+    AdamWMulti,
+    GradNorm,
+)
 from .norms import (  # noqa: F401
     layer_norm,
     norm_backward,

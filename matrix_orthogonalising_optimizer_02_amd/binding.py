@@ -29,7 +29,8 @@ SCALE_RMS = 2       # 0.2 / RMS(O), Eq. 6
 KCLASS_NAMES = ("cast", "frob", "gram", "poly", "apply", "apply_final", "rownorm_rows",
                 "colnorm_partial", "colnorm_finalize", "colnorm_apply", "rms_finalize",
                 "scaled_update", "adamw", "spec_gram", "spec_house", "spec_pass", "spec_reduce",
-                "spec_bisect", "spec_entropy", "norm_forward", "norm_backward", "norm_wgrad")
+                "spec_bisect", "spec_entropy", "norm_forward", "norm_backward", "norm_wgrad",
+                "tensor_plan", "adamw_multi", "grad_norm", "grad_total", "grad_scale")
 
 EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_default_hparams",
             "muon_workspace_bytes", "ns5_plan", "muon_step", "ns5_batched", "rownorm_update",
@@ -37,6 +38,8 @@ EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_defa
             "adamw_default_hparams", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy",
             "rownorm_shard_workspace_bytes", "rownorm_shard_colsq", "rownorm_shard_apply",
             "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
+            "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
+            "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
 
@@ -82,6 +85,24 @@ class NormRows(ctypes.Structure):
 
 class NormParam(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class TensorPlan(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_void_p), ("bytes", ctypes.c_size_t), ("kind", ctypes.c_int32),
+                ("count", ctypes.c_int32), ("blocks", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("w", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("g_dtype", ctypes.c_int32),
+                ("copy_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("lr_scale", ctypes.c_float),
+                ("wd_scale", ctypes.c_float)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -139,6 +160,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.norm_forward.argtypes = [desc, rows, param, param, rows, vp, vp, vp]
     lib.norm_backward_workspace_bytes.argtypes = [desc, ctypes.POINTER(ctypes.c_size_t)]
     lib.norm_backward.argtypes = [desc, rows, rows, param, vp, vp, rows, param, param, vp, sz, vp]
+    plan, size = ctypes.POINTER(TensorPlan), ctypes.POINTER(ctypes.c_size_t)
+    lib.adamw_multi_plan_bytes.argtypes = [ctypes.POINTER(AdamWTensor), i32, size]
+    lib.adamw_multi_plan.argtypes = [ctypes.POINTER(AdamWTensor), i32, vp, sz, plan, vp]
+    lib.adamw_multi_step.argtypes = [plan, ctypes.POINTER(AdamWHParams), i64, ctypes.c_uint64, vp, vp]
+    lib.grad_norm_plan_bytes.argtypes = [ctypes.POINTER(GradTensor), i32, size]
+    lib.grad_norm_plan.argtypes = [ctypes.POINTER(GradTensor), i32, vp, sz, plan, vp]
+    lib.grad_norm.argtypes = [plan, ctypes.c_float, vp, vp, vp]
+    lib.grad_scale.argtypes = [plan, vp, vp]
     lib.muon_ceiling_copy.argtypes = [vp, vp, i64, vp]
     lib.muon_ceiling_mfma.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
@@ -146,7 +175,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("muon_step", "ns5_batched", "rownorm_update", "rownorm_update_noalloc", "muon_workspace_bytes",
                  "ns5_plan", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
-                 "norm_backward", "muon_ceiling_copy", "muon_ceiling_mfma",
+                 "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
+                 "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale", "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:

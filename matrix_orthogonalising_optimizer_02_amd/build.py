@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["k_elementwise.hip", "k_gemm.hip", "k_adamw.hip", "k_spectrum.hip", "noalloc.hip", "k_ceiling.hip",
-           "k_norm.hip", "muon_abi.cpp", "abi_norm.cpp"]
+           "k_norm.hip", "k_adamw_multi.hip", "k_grad_norm.hip", "muon_abi.cpp", "abi_norm.cpp", "abi_multi.cpp"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

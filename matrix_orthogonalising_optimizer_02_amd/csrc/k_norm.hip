@@ -12,6 +12,7 @@
 // with that group's weights in registers, and asks for the next row before it reduces the
 // present one. Statistics are two-pass over the registers (the mean first, then the
 // squares of the differences), all sums in fp32 in a fixed order.
+#include "lanes.hpp"
 #include "train.hpp"
 
 #include <algorithm>
@@ -22,13 +23,6 @@ namespace {
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf162_t __attribute__((ext_vector_type(2)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
-
-// 16 bytes at any element alignment (global memory takes unaligned dword accesses).
-struct __attribute__((packed, aligned(2))) Raw16Packed {
-    u32x4 v;
-};
-__device__ __forceinline__ u32x4 load16(const void* p) { return reinterpret_cast<const Raw16Packed*>(p)->v; }
-__device__ __forceinline__ void store16(void* p, u32x4 v) { reinterpret_cast<Raw16Packed*>(p)->v = v; }
 
 template <int T>
 struct Elem;
@@ -155,32 +149,6 @@ __device__ __forceinline__ void store_param(void* base, int64_t at, int wdtype, 
     if (wdtype == kF32) reinterpret_cast<float*>(base)[at] = f;
     else if (wdtype == kBF16) reinterpret_cast<unsigned short*>(base)[at] = f2bf(f);
     else reinterpret_cast<_Float16*>(base)[at] = (_Float16)f;
-}
-
-template <int kCtrl>
-__device__ __forceinline__ float dpp_add(float v) {
-    const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true);
-    return v + __int_as_float(o);
-}
-
-// Sum over aligned groups of kLanes lanes, the same bits in every lane of the group.
-// Steps 1 to 8 exchange through DPP (pairs, quads, mirrored halves of a 16-lane row),
-// 16 and 32 through the row and half-wave swaps.
-template <int kLanes>
-__device__ __forceinline__ float lanes_sum(float v) {
-    if constexpr (kLanes >= 2) v = dpp_add<0xB1>(v);    // quad_perm [1, 0, 3, 2]
-    if constexpr (kLanes >= 4) v = dpp_add<0x4E>(v);    // quad_perm [2, 3, 0, 1]
-    if constexpr (kLanes >= 8) v = dpp_add<0x141>(v);   // row_half_mirror
-    if constexpr (kLanes >= 16) v = dpp_add<0x140>(v);  // row_mirror
-    if constexpr (kLanes >= 32) {
-        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-    if constexpr (kLanes >= 64) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-    return v;
 }
 
 __device__ __forceinline__ int64_t row_offset(const NormArgs& a, const RowsPtr& p, unsigned r) {

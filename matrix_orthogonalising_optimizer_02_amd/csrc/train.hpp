@@ -66,4 +66,90 @@ hipError_t launch_norm_forward(bool rms, int dtype, const NormPlan& p, const Nor
 hipError_t launch_norm_backward(bool rms, int dtype, const NormPlan& p, const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_wgrad(const NormArgs& a, hipStream_t s);
 
+// ---- many tensors in one launch ----------------------------------------------------
+// A table in device memory holds the descriptors and, for every block, its tensor. Both
+// are written by kernels whose arguments carry the descriptors: no copy from host memory,
+// so nothing of the caller's has to outlive the call.
+constexpr int kQBlock = 256;             // elements of 8-bit state that share a scale
+constexpr int kMultiBlockElems = 4096;   // elements of a block of the AdamW step
+
+struct MultiDesc {
+    float* w;
+    void* copy;            // null = not wanted
+    const void* g;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    int64_t n;
+    int32_t blk_begin;
+    int32_t index;         // position in the caller's list
+    float lr_scale, wd_scale;
+    int8_t g_type, copy_type, bits, pad_;
+    int32_t pad2_;
+};
+
+constexpr int kMultiPerLaunch = 32;
+struct MultiDescArgs {
+    MultiDesc d[kMultiPerLaunch];
+    MultiDesc* table;
+    int32_t first, n;
+};
+
+struct MultiArgs {
+    const MultiDesc* table;
+    const int32_t* tensor_of_block;
+    int32_t blocks;
+    uint32_t key;          // of (seed, step)
+    float beta1, beta2, one_minus_beta1, one_minus_beta2;
+    float eps;
+    float lr_bc1;          // lr / (1 - beta1^t)
+    float inv_sqrt_bc2;    // 1 / sqrt(1 - beta2^t)
+    double lr_wd;          // lr * weight_decay
+    const float* grad_scale;
+};
+
+struct GradDesc {
+    void* g;
+    int64_t n;
+    int32_t blk_begin;
+    int32_t blk_end;
+    int32_t type;
+    int32_t pad_;
+};
+
+constexpr int kGradPerLaunch = 96;
+struct GradDescArgs {
+    GradDesc d[kGradPerLaunch];
+    GradDesc* table;
+    int32_t first, n;
+};
+
+struct GradArgs {
+    const GradDesc* table;
+    const int32_t* tensor_of_block;
+    double* partial;       // one a block
+    int64_t block_elems;   // of every tensor
+    int32_t count, blocks;
+    float max_norm;
+    float* total;
+    float* norms;          // null = not wanted
+    const float* factor;   // grad_scale
+};
+
+__host__ __device__ inline uint32_t mix32(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0x6A09E667u;
+    x = (x ^ (x >> 15)) * 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+hipError_t launch_multi_table(const MultiDescArgs& a, hipStream_t s);
+hipError_t launch_multi_map(const MultiDesc* table, int count, int32_t* map, int blocks, hipStream_t s);
+hipError_t launch_multi_step(const MultiArgs& a, hipStream_t s);
+hipError_t launch_grad_table(const GradDescArgs& a, hipStream_t s);
+hipError_t launch_grad_map(const GradDesc* table, int count, int32_t* map, int blocks, hipStream_t s);
+hipError_t launch_grad_norm(const GradArgs& a, hipStream_t s);
+hipError_t launch_grad_total(const GradArgs& a, hipStream_t s);
+hipError_t launch_grad_scale(const GradArgs& a, hipStream_t s);
+
 }  // namespace muon

@@ -1,0 +1,275 @@
+"""AdamW and gradient clipping over many tensors, one launch a step whatever their count.
+
+`AdamWMulti` is the AdamW side of the hybrid optimizer for large parameter lists: fp32
+weights, gradients in any type, states in 32 bits or in 8, an optional 16-bit copy of the
+weights, and a gradient factor that stays on the device. `GradNorm` measures the
+gradients' norms and the clip factor that feeds it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+from . import binding as B
+
+STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
+
+
+def _check_list(tensors, name, device=None, dtypes=None, numels=None):
+    torch = B._torch()
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch.Tensor")
+        if dtypes is not None and t.dtype not in dtypes:
+            raise ValueError(f"{name}[{i}] must have dtype {' or '.join(str(d) for d in dtypes)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if numels is not None and t.numel() != numels[i]:
+            raise ValueError(f"{name}[{i}] must have {numels[i]} elements")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}[{i}] must live on a GPU")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name}[{i}] must live on {device}")
+
+
+def _device_of(tensors, name):
+    """The first tensor's device; the current one of an empty list."""
+    torch = B._torch()
+    if not tensors:
+        return torch.device("cuda", torch.cuda.current_device())
+    if not isinstance(tensors[0], torch.Tensor):
+        raise TypeError(f"{name}[0] must be a torch.Tensor")
+    return tensors[0].device
+
+
+def _per_tensor(values, n, name):
+    if values is None:
+        return [1.0] * n
+    values = [float(v) for v in values]
+    if len(values) != n:
+        raise ValueError(f"one {name} per parameter")
+    return values
+
+
+def _scalar_ptr(t, name, device):
+    """Device pointer of an optional one-element float32 tensor."""
+    if t is None:
+        return None
+    torch = B._torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != 1:
+        raise ValueError(f"{name} must be a float32 tensor of one element")
+    if t.device != device:
+        raise ValueError(f"{name} must live on {device}")
+    return t.data_ptr()
+
+
+class AdamWMulti:
+    """AdamW over a list of fp32 parameters of any shapes, in one launch a step.
+
+    The gradient tensors given here (float32, bfloat16 or float16) are read at every step,
+    unless step() or set_grads() is passed new ones.
+    state_bits: 32, or 8 for moments in e4m3 with one scale for every 256 elements (a
+    quarter of the memory), rounded stochastically from `seed`, the step and the position.
+    copies: optional 16-bit tensors that receive the updated weights.
+    lr_scales, wd_scales: optional factors per parameter on lr and on weight decay.
+    states: optional dict of existing states as state_dict() names them, used in place:
+    lists `exp_avg` and `exp_avg_sq` (32 bits: float32; 8 bits: float8_e4m3fn, where
+    exp_avg_sq holds square roots) and for 8 bits `exp_avg_scale`, `exp_avg_sq_scale`
+    (float32, ceil(numel / 256) entries). Otherwise the states start at zero.
+    """
+
+    def __init__(self, params, grads, hp: Optional[B.AdamWHParams] = None, state_bits: int = 32, copies=None,
+                 lr_scales=None, wd_scales=None, seed: int = 0, states=None, stream=None):
+        torch = B._torch()
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if not 0 <= seed < 1 << 64:
+            raise ValueError("seed must be in [0, 2^64)")
+        self.params, self.hp, self.state_bits, self.seed = list(params), hp or B.adamw_default_hparams(), state_bits, seed
+        n = self.n = len(self.params)
+        self.device = _device_of(self.params, "params")
+        _check_list(self.params, "params", self.device, (torch.float32,))
+        self._numels = [p.numel() for p in self.params]
+        self.copies = None if copies is None else list(copies)
+        if self.copies is not None:
+            if len(self.copies) != n:
+                raise ValueError("one copy per parameter")
+            _check_list(self.copies, "copies", self.device, (torch.bfloat16, torch.float16), self._numels)
+        lr_scales, wd_scales = _per_tensor(lr_scales, n, "lr_scale"), _per_tensor(wd_scales, n, "wd_scale")
+        with B.device_and_stream(self.device, stream):
+            self._make_states(states)
+        codes = B.dtype_codes()
+        self._arr = (B.AdamWTensor * max(n, 1))()
+        small = state_bits == 8
+        for i, p in enumerate(self.params):
+            c = self.copies[i] if self.copies is not None else None
+            self._arr[i] = B.AdamWTensor(
+                self._numels[i], p.data_ptr() or None, c.data_ptr() or None if c is not None else None, None,
+                self.exp_avg[i].data_ptr() or None, self.exp_avg_sq[i].data_ptr() or None,
+                self.exp_avg_scale[i].data_ptr() or None if small else None,
+                self.exp_avg_sq_scale[i].data_ptr() or None if small else None, 0,
+                codes[c.dtype] if c is not None else 0, state_bits, lr_scales[i], wd_scales[i])
+        self._plan = B.TensorPlan()
+        self._table = None
+        self.grads = None
+        self.set_grads(grads, stream)
+
+    def _make_states(self, states):
+        torch = B._torch()
+        small = self.state_bits == 8
+        dtype = torch.float8_e4m3fn if small else torch.float32
+        scales = [-(-k // STATE_BLOCK) for k in self._numels]
+        names = {"exp_avg": self._numels, "exp_avg_sq": self._numels}
+        if small:
+            names.update(exp_avg_scale=scales, exp_avg_sq_scale=scales)
+        for name, sizes in names.items():
+            kind = torch.float32 if name.endswith("scale") else dtype
+            if states is not None:
+                tensors = list(states[name])
+                if len(tensors) != self.n:
+                    raise ValueError(f"one {name} per parameter")
+                _check_list(tensors, name, self.device, (kind,), sizes)
+            else:
+                # one zeroed buffer, every tensor at a multiple of 256 bytes
+                size = torch.empty(0, dtype=kind).element_size()
+                starts, at = [], 0
+                for k in sizes:
+                    starts.append(at)
+                    at += -(-k * size // 256) * 256
+                flat = torch.zeros(at, dtype=torch.uint8, device=self.device)
+                tensors = [flat[a:a + k * size].view(kind) for a, k in zip(starts, sizes)]
+            setattr(self, name, tensors)
+        self._state_names = tuple(names)
+
+    def set_grads(self, grads, stream=None):
+        """New gradient tensors. Their addresses are written to the table on `stream` where
+        one differs from before; steps that follow on the stream read them."""
+        torch = B._torch()
+        grads = list(grads)
+        if len(grads) != self.n:
+            raise ValueError("one gradient per parameter")
+        _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
+        codes = B.dtype_codes()
+        same = self._table is not None
+        for d, g in zip(self._arr, grads):
+            ptr, code = g.data_ptr() or None, codes[g.dtype]
+            same = same and d.g == ptr and d.g_dtype == code
+            d.g, d.g_dtype = ptr, code
+        self.grads = grads
+        if same:
+            return
+        lib = B.load_library()
+        self._plan.kind = 0  # no step with a table that was not written
+        with B.device_and_stream(self.device, stream):
+            if self._table is None:
+                need = ctypes.c_size_t(0)
+                B._check(lib.adamw_multi_plan_bytes(self._arr, self.n, need), "adamw_multi_plan_bytes")
+                self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+            rc = lib.adamw_multi_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
+                                      B._stream_handle(stream, self.device))
+        B._check(rc, "adamw_multi_plan")
+
+    def step(self, step: int, grad_scale=None, stream=None, grads=None):
+        """One step at 0-based `step`. grad_scale: optional one-element float32 device tensor."""
+        if grads is not None:
+            self.set_grads(grads, stream)
+        scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
+        with B.device_and_stream(self.device, stream):
+            rc = B.load_library().adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale,
+                                                   B._stream_handle(stream, self.device))
+        B._check(rc, "adamw_multi_step")
+
+    def moments(self, i: int):
+        """The fp32 values of parameter i's first and second moment, in its shape."""
+        p = self.params[i]
+        if self.state_bits == 32:
+            return self.exp_avg[i].view(p.shape).clone(), self.exp_avg_sq[i].view(p.shape).clone()
+        out = []
+        for codes, scale in ((self.exp_avg[i], self.exp_avg_scale[i]), (self.exp_avg_sq[i], self.exp_avg_sq_scale[i])):
+            out.append((codes.float() * scale.repeat_interleave(STATE_BLOCK)[:p.numel()]).view(p.shape))
+        return out[0], out[1].square()
+
+    def state_dict(self):
+        return {"state_bits": self.state_bits, "seed": self.seed,
+                **{name: [t.clone() for t in getattr(self, name)] for name in self._state_names}}
+
+    def load_state_dict(self, state):
+        if state["state_bits"] != self.state_bits:
+            raise ValueError(f"the saved states have {state['state_bits']} bits, these {self.state_bits}")
+        for name in self._state_names:
+            if len(state[name]) != self.n:
+                raise ValueError(f"one {name} per parameter")
+            for dst, src in zip(getattr(self, name), state[name]):
+                if dst.shape != src.shape or dst.dtype != src.dtype:
+                    raise ValueError(f"{name} does not fit the parameters")
+        self.seed = int(state["seed"])
+        for name in self._state_names:
+            for dst, src in zip(getattr(self, name), state[name]):
+                dst.copy_(src)
+
+
+class GradNorm:
+    """l2 norms of a list of gradients, their total and the clip factor, on the device.
+
+    `total` (float32 [2]: the norm, the factor) and `norms` (float32 [count]) belong to the
+    object and are overwritten by every measure(); calls on one object must not overlap.
+    """
+
+    def __init__(self, grads, stream=None):
+        torch = B._torch()
+        grads = list(grads)
+        self.n = len(grads)
+        self.device = _device_of(grads, "grads")
+        self._arr = (B.GradTensor * max(self.n, 1))()
+        self._plan = B.TensorPlan()
+        self._table = self._numels = self.grads = None
+        self.set_grads(grads, stream)
+        with B.device_and_stream(self.device, stream):
+            self.total = torch.empty(2, dtype=torch.float32, device=self.device)
+            self.norms = torch.empty(self.n, dtype=torch.float32, device=self.device)
+        self.norm, self.factor = self.total[0:1], self.total[1:2]
+
+    def set_grads(self, grads, stream=None):
+        """New gradient tensors of the same sizes; written to the table where an address differs."""
+        torch = B._torch()
+        grads = list(grads)
+        if len(grads) != self.n:
+            raise ValueError(f"{self.n} gradients are expected")
+        _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
+        self._numels = [g.numel() for g in grads]
+        codes = B.dtype_codes()
+        same = self._table is not None
+        for d, g in zip(self._arr, grads):
+            ptr, code = g.data_ptr() or None, codes[g.dtype]
+            same = same and d.g == ptr and d.dtype == code
+            d.g, d.numel, d.dtype = ptr, g.numel(), code
+        self.grads = grads
+        if same:
+            return
+        lib = B.load_library()
+        self._plan.kind = 0
+        with B.device_and_stream(self.device, stream):
+            if self._table is None:
+                need = ctypes.c_size_t(0)
+                B._check(lib.grad_norm_plan_bytes(self._arr, self.n, need), "grad_norm_plan_bytes")
+                self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+            rc = lib.grad_norm_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
+                                    B._stream_handle(stream, self.device))
+        B._check(rc, "grad_norm_plan")
+
+    def measure(self, max_norm: float, stream=None):
+        """(total, norms): total[0] the norm over all gradients, total[1] the factor
+        min(1, max_norm / (norm + 1e-6)), norms[i] the norm of gradient i."""
+        with B.device_and_stream(self.device, stream):
+            rc = B.load_library().grad_norm(self._plan, max_norm, self.total.data_ptr(), self.norms.data_ptr() or None,
+                                            B._stream_handle(stream, self.device))
+        B._check(rc, "grad_norm")
+        return self.total, self.norms
+
+    def scale_(self, factor=None, stream=None):
+        """The gradients times `factor` in place (one-element float32 device tensor; by
+        default the last measure()'s clip factor). Nothing is read or written where it is 1."""
+        ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device)
+        with B.device_and_stream(self.device, stream):
+            rc = B.load_library().grad_scale(self._plan, ptr, B._stream_handle(stream, self.device))
+        B._check(rc, "grad_scale")
