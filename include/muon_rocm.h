@@ -381,9 +381,11 @@ int adamw_multi_plan_bytes(const adamw_tensor* tensors, int32_t count, size_t* b
 /* Checks `count` tensors (host array), enqueues the table's writing into `device` (256-byte
  * aligned, `bytes` of adamw_multi_plan_bytes) on `stream` and fills *plan. Steps with this
  * plan come after it on the stream. A gradient at another address needs a new plan call
- * (into the same buffer, if it follows the last step on the stream).
+ * (into the same buffer, if it follows the last step on the stream). Plan calls are
+ * refused on a stream that is being captured: what a graph records is not yet written.
+ * On an error after the first launch plan->kind is 0 and steps with it are refused.
  * Errors: INVALID_ARG (NULL pointers, negative numel, unknown type or bits, non-finite
- * scale), ALIGN (w, m, v, g, copy not 16-byte aligned, scales not 4-byte), ALIAS (any two
+ * scale, a capture), ALIGN (w, m, v, g, copy not 16-byte aligned, scales not 4-byte), ALIAS (any two
  * of all w, copy, m, v, m_scale, v_scale, g ranges or the table overlap, gradients with each
  * other excepted), WORKSPACE (device
  * NULL or too small), TOO_LARGE (2^40 elements in a tensor, 2^31 blocks), HIP. */

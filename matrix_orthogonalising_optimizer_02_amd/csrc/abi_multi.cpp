@@ -95,6 +95,17 @@ int check_plan(const tensor_plan* p, int32_t kind) {
     return MUON_OK;
 }
 
+// A table that a capture records is not written: steps outside the graph, or before its
+// first replay, would follow whatever addresses the buffer holds.
+int check_not_capturing(hipStream_t s) {
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(s, &status);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("hipStreamIsCapturing: ") + hipGetErrorString(e));
+    if (status != hipStreamCaptureStatusNone)
+        return fail(MUON_ERR_INVALID_ARG, "a plan cannot be captured into a graph: make it before the capture");
+    return MUON_OK;
+}
+
 // A plan's tables by its counts alone: the block length of a gradient plan is in `reserved`
 // as a multiple of kGradBlockElems.
 GradArgs grad_args(const tensor_plan& p) {
@@ -163,6 +174,8 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
         }
     }
     if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (sz.blocks && (rc = check_not_capturing(s))) return rc;
     tensor_plan p{};
     p.device = device;
     p.bytes = sz.bytes;
@@ -171,7 +184,6 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
     p.blocks = int32_t(sz.blocks);
     *plan = p;
     if (sz.blocks == 0) return MUON_OK;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     MultiDescArgs a{};
     a.table = static_cast<MultiDesc*>(device);
     int32_t block = 0;
@@ -197,14 +209,19 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
         block += int32_t(ceil_div(t.numel, kMultiBlockElems));
         if (a.n == kMultiPerLaunch || i == count - 1) {
             rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw table", [&] { return launch_multi_table(a, s); });
-            if (rc) return rc;
+            if (rc) {
+                plan->kind = 0;
+                return rc;
+            }
             a.first += a.n;
             a.n = 0;
         }
     }
     int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
-    return run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw map",
-                     [&] { return launch_multi_map(a.table, count, map, int(sz.blocks), s); });
+    rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw map",
+                   [&] { return launch_multi_map(a.table, count, map, int(sz.blocks), s); });
+    if (rc) plan->kind = 0;
+    return rc;
 }
 
 MUON_API int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t step, uint64_t seed,
@@ -272,6 +289,8 @@ MUON_API int grad_norm_plan(const grad_tensor* grads, int32_t count, void* devic
         ranges.push_back({addr(t.g), addr(t.g) + uintptr_t(t.numel) * e, true});
     }
     if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (count && (rc = check_not_capturing(s))) return rc;
     tensor_plan p{};
     p.device = device;
     p.bytes = sz.bytes;
@@ -281,7 +300,6 @@ MUON_API int grad_norm_plan(const grad_tensor* grads, int32_t count, void* devic
     p.reserved = int32_t(sz.block_elems / kGradBlockElems);
     *plan = p;
     if (count == 0) return MUON_OK;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     GradDescArgs a{};
     a.table = static_cast<GradDesc*>(device);
     int32_t block = 0;
@@ -296,15 +314,20 @@ MUON_API int grad_norm_plan(const grad_tensor* grads, int32_t count, void* devic
         d.blk_end = block;
         if (a.n == kGradPerLaunch || i == count - 1) {
             rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient table", [&] { return launch_grad_table(a, s); });
-            if (rc) return rc;
+            if (rc) {
+                plan->kind = 0;
+                return rc;
+            }
             a.first += a.n;
             a.n = 0;
         }
     }
     if (sz.blocks == 0) return MUON_OK;
     int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
-    return run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient map",
-                     [&] { return launch_grad_map(a.table, count, map, int(sz.blocks), s); });
+    rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient map",
+                   [&] { return launch_grad_map(a.table, count, map, int(sz.blocks), s); });
+    if (rc) plan->kind = 0;
+    return rc;
 }
 
 MUON_API int grad_norm(const tensor_plan* plan, float max_norm, float* total, float* norms, void* stream) {

@@ -47,11 +47,11 @@ struct Hyper {
     float b1, b2, ob1, ob2, eps, step, inv_sqrt_bc2, decay, gs;
 };
 
-// sqrt(v) with an error that differs from the rounding to nearest once in some millions:
-// r = 1/sqrt(v) from the hardware (1 ulp), s = v r, and one Newton step on s whose
-// residual is exact. Seven operations where the library's sqrtf has about sixteen. A v
-// below 2^-126 (a gradient below 4e-18) gets a root up to 2 times too small, nowhere near
-// any eps that keeps the step finite.
+// sqrt(v): r = 1/sqrt(v) from the hardware (1 ulp), s = v r, and one Newton step on s
+// whose residual is exact; seven operations where sqrtf has about sixteen. The same bits
+// as sqrtf on 3e8 values between 2^-97 and 2^127; nearer to 2^-126 the residual loses
+// digits and one value in fifty is an ulp off, and a v below 2^-126 (a gradient below
+// 4e-18) gets a root up to 2 times too small, nowhere near any eps in use.
 __device__ __forceinline__ float root(float v) {
     const float r = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
     const float s = v * r;

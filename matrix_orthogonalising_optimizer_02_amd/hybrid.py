@@ -17,6 +17,7 @@ from __future__ import annotations
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import binding as B
+from .multi import AdamWMulti, GradNorm
 
 BLOCK_PREFIX = "blocks."
 
@@ -101,34 +102,61 @@ class HybridOptimizer:
     named_params: mapping name -> fp32 CUDA tensor (contiguous). step(grads) takes a
     mapping with the same names and advances every parameter by one step; both groups
     share the 0-based step counter (Muon's refresh schedule, AdamW's bias correction).
+
+    adamw_state_bits: None for adamw_step (fp32 moments, one launch for every 48 tensors);
+    32 or 8 for AdamWMulti, one launch whatever their number, with moments of that width
+    (8: a quarter of the memory, rounded stochastically from `seed`). AdamW's gradients
+    may then be bfloat16 or float16 too, Muon's stay fp32.
+    max_grad_norm: clip all gradients together to this l2 norm (needs 32 or 8 above). The
+    factor stays on the device: Muon's gradients are scaled in place, AdamW's where they
+    are read. `grad_norm` then holds the last step's norm and factor (float32 [2]).
     """
 
     def __init__(self, named_params: Dict[str, "object"], muon_hp: Optional[B.MuonHParams] = None,
-                 adamw_hp: Optional[B.AdamWHParams] = None):
+                 adamw_hp: Optional[B.AdamWHParams] = None, adamw_state_bits: Optional[int] = None,
+                 max_grad_norm: Optional[float] = None, seed: int = 0):
         import torch
+        if adamw_state_bits not in (None, 8, 32):
+            raise ValueError("adamw_state_bits must be None, 8 or 32")
+        if max_grad_norm is not None and adamw_state_bits is None:
+            raise ValueError("max_grad_norm needs adamw_state_bits 8 or 32")
+        if max_grad_norm is not None and not 0.0 < max_grad_norm < float("inf"):
+            raise ValueError("max_grad_norm must be finite and > 0")
         self.names = list(named_params)
         shapes = [(n, tuple(named_params[n].shape)) for n in self.names]
         self.muon_names, self.adamw_names = split_param_groups(shapes)
         self.params = named_params
         self.muon_hp = muon_hp or B.default_hparams()
         self.adamw_hp = adamw_hp or B.adamw_default_hparams()
+        self.adamw_state_bits, self.max_grad_norm, self.seed = adamw_state_bits, max_grad_norm, seed
         self.momenta = {n: torch.zeros_like(named_params[n]) for n in self.muon_names}
-        self.exp_avg = {n: torch.zeros_like(named_params[n]) for n in self.adamw_names}
-        self.exp_avg_sq = {n: torch.zeros_like(named_params[n]) for n in self.adamw_names}
+        small = adamw_state_bits is not None
+        self.exp_avg = {} if small else {n: torch.zeros_like(named_params[n]) for n in self.adamw_names}
+        self.exp_avg_sq = {} if small else {n: torch.zeros_like(named_params[n]) for n in self.adamw_names}
         dev = next(iter(named_params.values())).device if named_params else "cuda"
         self.workspace = B.make_workspace([tuple(named_params[n].shape) for n in self.muon_names], dev) \
             if self.muon_names else None
         self._adamw = None  # descriptor array, built at the first step
+        if small and self.adamw_names:
+            self._adamw = AdamWMulti([named_params[n] for n in self.adamw_names], None, self.adamw_hp, adamw_state_bits,
+                                     seed=seed)
+        self._norm = self._muon_norm = None
+        self.grad_norm = None
         self.step_count = 0
 
     def step(self, grads: Dict[str, "object"], stream=None, update_rms=None):
+        factor = None
+        if self.max_grad_norm is not None and self.names:
+            factor = self._clip(grads, stream)
         if self.muon_names:
             B.muon_step([self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names],
                         [grads[n] for n in self.muon_names], self.step_count, self.muon_hp, self.workspace,
                         stream, update_rms)
         if self.adamw_names:
             g = [grads[n] for n in self.adamw_names]
-            if self._adamw is None:
+            if self.adamw_state_bits is not None:
+                self._adamw.step(self.step_count, factor, stream, g)
+            elif self._adamw is None:
                 self._adamw = B.AdamWGroup([self.params[n] for n in self.adamw_names], g,
                                            [self.exp_avg[n] for n in self.adamw_names],
                                            [self.exp_avg_sq[n] for n in self.adamw_names], self.adamw_hp)
@@ -138,13 +166,35 @@ class HybridOptimizer:
                 self._adamw.step(self.step_count, stream, None if same else g)
         self.step_count += 1
 
+    def _clip(self, grads, stream):
+        """Measures all gradients, scales Muon's; the factor for AdamW's (device tensor)."""
+        g, gm = [grads[n] for n in self.names], [grads[n] for n in self.muon_names]
+        if self._norm is None:
+            self._norm = GradNorm(g, stream)
+            self._muon_norm = GradNorm(gm, stream) if gm else None
+        else:
+            self._norm.set_grads(g, stream)
+            if gm:
+                self._muon_norm.set_grads(gm, stream)
+        self.grad_norm, _ = self._norm.measure(self.max_grad_norm, stream)
+        if gm:
+            self._muon_norm.scale_(self._norm.factor, stream)
+        return self._norm.factor
+
     def state_dict(self):
-        return {"step": self.step_count,
-                "momenta": {n: t.clone() for n, t in self.momenta.items()},
-                "exp_avg": {n: t.clone() for n, t in self.exp_avg.items()},
-                "exp_avg_sq": {n: t.clone() for n, t in self.exp_avg_sq.items()}}
+        state = {"step": self.step_count, "momenta": {n: t.clone() for n, t in self.momenta.items()}}
+        if self.adamw_state_bits is None:
+            state["exp_avg"] = {n: t.clone() for n, t in self.exp_avg.items()}
+            state["exp_avg_sq"] = {n: t.clone() for n, t in self.exp_avg_sq.items()}
+        else:
+            state["adamw"] = self._adamw.state_dict() if self._adamw is not None else None
+        return state
 
     def load_state_dict(self, state):
+        if (self.adamw_state_bits is None) != ("exp_avg" in state):
+            raise ValueError("the saved AdamW states are of another kind than this optimizer's")
+        if self.adamw_state_bits is not None and self._adamw is not None:
+            self._adamw.load_state_dict(state["adamw"])
         self.step_count = int(state["step"])
         for key, dst in (("momenta", self.momenta), ("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
             for n, t in dst.items():

@@ -66,8 +66,11 @@ def _scalar_ptr(t, name, device):
 class AdamWMulti:
     """AdamW over a list of fp32 parameters of any shapes, in one launch a step.
 
-    The gradient tensors given here (float32, bfloat16 or float16) are read at every step,
-    unless step() or set_grads() is passed new ones.
+    The gradient tensors given here, or to set_grads() or step() later (float32, bfloat16
+    or float16), are read at every step until others are given. Their addresses stand in a
+    table on the device that is written when they change, which cannot be captured into a
+    graph: give the gradients before a capture. Replayed steps read the table too, so new
+    gradients are new for them as well.
     state_bits: 32, or 8 for moments in e4m3 with one scale for every 256 elements (a
     quarter of the memory), rounded stochastically from `seed`, the step and the position.
     copies: optional 16-bit tensors that receive the updated weights.
@@ -78,7 +81,7 @@ class AdamWMulti:
     (float32, ceil(numel / 256) entries). Otherwise the states start at zero.
     """
 
-    def __init__(self, params, grads, hp: Optional[B.AdamWHParams] = None, state_bits: int = 32, copies=None,
+    def __init__(self, params, grads=None, hp: Optional[B.AdamWHParams] = None, state_bits: int = 32, copies=None,
                  lr_scales=None, wd_scales=None, seed: int = 0, states=None, stream=None):
         torch = B._torch()
         if state_bits not in (8, 32):
@@ -112,7 +115,8 @@ class AdamWMulti:
         self._plan = B.TensorPlan()
         self._table = None
         self.grads = None
-        self.set_grads(grads, stream)
+        if grads is not None:
+            self.set_grads(grads, stream)
 
     def _make_states(self, states):
         torch = B._torch()
@@ -150,7 +154,7 @@ class AdamWMulti:
             raise ValueError("one gradient per parameter")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
         codes = B.dtype_codes()
-        same = self._table is not None
+        same = self._plan.kind != 0
         for d, g in zip(self._arr, grads):
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.g_dtype == code
@@ -173,6 +177,8 @@ class AdamWMulti:
         """One step at 0-based `step`. grad_scale: optional one-element float32 device tensor."""
         if grads is not None:
             self.set_grads(grads, stream)
+        if self.grads is None:
+            raise ValueError("the step has no gradients")
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale,
@@ -211,6 +217,7 @@ class AdamWMulti:
 class GradNorm:
     """l2 norms of a list of gradients, their total and the clip factor, on the device.
 
+    The gradients' addresses are kept in a table, as AdamWMulti's (not within a capture).
     `total` (float32 [2]: the norm, the factor) and `norms` (float32 [count]) belong to the
     object and are overwritten by every measure(); calls on one object must not overlap.
     """
@@ -238,7 +245,7 @@ class GradNorm:
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
         self._numels = [g.numel() for g in grads]
         codes = B.dtype_codes()
-        same = self._table is not None
+        same = self._plan.kind != 0
         for d, g in zip(self._arr, grads):
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.dtype == code
