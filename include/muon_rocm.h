@@ -483,8 +483,8 @@ typedef struct norm_param {
  * and strides). One launch.
  * Errors: INVALID_ARG, ALIGN, ALIAS (y, mean or rstd overlaps another buffer, by the
  * span from its first to its last element), TOO_LARGE (cols above MUON_NORM_MAX_COLS,
- * rows or groups of 2^31 or more, a span above 2^46 elements), HIP. rows == 0 or cols == 0 is a
- * no-op. */
+ * rows or groups above 2^30, a span above 2^46 elements), HIP. rows == 0 or cols == 0 is
+ * a no-op. */
 int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_param* w, const norm_param* b,
                  const norm_rows* y, float* mean, float* rstd, void* stream);
 

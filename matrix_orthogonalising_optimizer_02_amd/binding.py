@@ -245,9 +245,15 @@ def ns5_plan(shapes: Sequence[Sequence[int]]):
 
 # ------------------------------------------------------------ tensor helpers ----
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _check_tensor(t, name):
@@ -293,6 +299,15 @@ def dtype_codes():
         torch = _torch()
         _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     return _dtype_codes
+
+
+def raw_stream(stream, device):
+    """The hipStream_t of `stream` (None: the device's current stream) as an int."""
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream))
+    torch = _torch()
+    current = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s time
+    return current(device.index) if current is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 _same_place = contextlib.nullcontext()

@@ -142,12 +142,14 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
     Sizes sz;
     int rc = adamw_sizes(tensors, count, &sz);
     if (rc) return rc;
-    std::vector<Range> ranges, grads;
+    std::vector<Range> ranges;
+    int bits = -1;  // of all tensors so far; 0 once they differ
     for (int i = 0; i < count; ++i) {
         const adamw_tensor& t = tensors[i];
         if (t.numel == 0) continue;
         if (t.state_bits != 8 && t.state_bits != 32) return fail(MUON_ERR_INVALID_ARG, "state_bits must be 8 or 32" + at(i));
         const bool small = t.state_bits == 8;
+        bits = bits < 0 || bits == t.state_bits ? t.state_bits : 0;
         if (!t.w || !t.g || !t.m || !t.v || (small && (!t.m_scale || !t.v_scale)))
             return fail(MUON_ERR_INVALID_ARG, "NULL pointer" + at(i));
         if (t.g_dtype < MUON_DTYPE_F32 || t.g_dtype > MUON_DTYPE_F16) return fail(MUON_ERR_INVALID_ARG, "unknown g_dtype" + at(i));
@@ -182,6 +184,7 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
     p.kind = kPlanAdamw;
     p.count = count;
     p.blocks = int32_t(sz.blocks);
+    p.reserved = bits;
     *plan = p;
     if (sz.blocks == 0) return MUON_OK;
     MultiDescArgs a{};
@@ -248,6 +251,7 @@ MUON_API int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, 
     a.tensor_of_block = reinterpret_cast<const int32_t*>(static_cast<const char*>(plan->device) +
                                                          align256(size_t(plan->count) * sizeof(MultiDesc)));
     a.blocks = plan->blocks;
+    a.bits = plan->reserved;
     a.key = mix32(mix32(mix32(uint32_t(seed)) + uint32_t(seed >> 32)) + uint32_t(step));
     a.beta1 = hp->beta1;
     a.beta2 = hp->beta2;

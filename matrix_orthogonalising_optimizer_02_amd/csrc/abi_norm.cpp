@@ -19,7 +19,8 @@ namespace {
 static_assert(kF32 == MUON_DTYPE_F32 && kBF16 == MUON_DTYPE_BF16 && kF16 == MUON_DTYPE_F16, "type codes");
 static_assert(kNormMaxCols == MUON_NORM_MAX_COLS, "column limit");
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSpan = int64_t(1) << 46;
 
 int fail(int code, const std::string& what) { return set_last_error(code, what); }
@@ -38,7 +39,7 @@ int check_desc(const norm_desc* d) {
     if (d->cols > kNormMaxCols)
         return fail(MUON_ERR_TOO_LARGE, "cols above " + std::to_string(kNormMaxCols));
     if (d->rows > kMaxRows || d->groups > kMaxRows || d->inner > kMaxRows)
-        return fail(MUON_ERR_TOO_LARGE, "rows, groups or inner of 2^31 or more");
+        return fail(MUON_ERR_TOO_LARGE, "rows, groups or inner above 2^30");
     return MUON_OK;
 }
 
@@ -111,6 +112,8 @@ NormArgs base_args(const norm_desc& d, const NormPlan& p) {
     a.inner_mul = uint32_t(((uint64_t((int64_t(1) << l) - d.inner) << 32) / uint64_t(d.inner)) + 1);
     a.chunks = p.chunks;
     a.chunk_rows = p.chunk_rows;
+    a.team_waves = p.lanes / 64;
+    a.teams = p.teams;
     a.wdtype = d.wdtype;
     a.eps = d.eps;
     a.offset = d.weight_offset;
@@ -145,7 +148,7 @@ MUON_API int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_
     if ((rc = check_overlaps(ranges))) return rc;
     if (d.rows == 0 || d.cols == 0) return MUON_OK;
     const NormPlan p = plan_norm_forward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-    if (d.groups * int64_t(p.chunks) > kMaxRows) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+    if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
     NormArgs a = base_args(d, p);
     a.x = rows_ptr(*x);
     a.y = rows_ptr(*y);
@@ -201,7 +204,7 @@ MUON_API int norm_backward(const norm_desc* desc, const norm_rows* dy, const nor
         return rc;
     if (d.cols == 0) return MUON_OK;
     const NormPlan p = plan_norm_backward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-    if (d.groups * int64_t(p.chunks) > kMaxRows) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+    if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
     const bool grads = present(dw) || present(db);
     const size_t need = grads ? partial_bytes(d, p) : 0;
     if (need) {

@@ -3,7 +3,9 @@
 // HBM-bound: the gradients are read once. A block sums the squares of one run of a tensor
 // in fp64 (fp32 squares would overflow from 1.8e19 and vanish below 1e-23; the vector
 // units have fp64 to spare at this rate) and leaves one partial sum; a second launch adds
-// them, one block a tensor and one for the total, each in a fixed order.
+// them, one block a tensor and one for the total, each in a fixed order. Loads carry the
+// non-temporal hint: 700 M fp32 elements in 405 us (6.9 TB/s), 459 us without; bf16 209 us.
+// Scaling in place: 1074 us (5.2 TB/s), 5 us where the factor is 1.
 #include "lanes.hpp"
 #include "train.hpp"
 
@@ -64,11 +66,11 @@ __device__ __forceinline__ double run_squares(const void* g, int64_t begin, int6
     for (; i + 256 * kVec * kUnroll <= end; i += 256 * kVec * kUnroll) {
         u32x4 r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) r[k] = load16(p + (i + (int64_t)(k * 256 + threadIdx.x) * kVec) * kSize);
+        for (int k = 0; k < kUnroll; ++k) r[k] = stream16(p + (i + (int64_t)(k * 256 + threadIdx.x) * kVec) * kSize);
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) add16<T>(r[k], acc);
     }
-    for (; i + 256 * kVec <= end; i += 256 * kVec) add16<T>(load16(p + (i + (int64_t)threadIdx.x * kVec) * kSize), acc);
+    for (; i + 256 * kVec <= end; i += 256 * kVec) add16<T>(stream16(p + (i + (int64_t)threadIdx.x * kVec) * kSize), acc);
     for (i += threadIdx.x; i < end; i += 256) acc[0] = square_add(element<T>(g, i), acc[0]);
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
@@ -102,30 +104,39 @@ __global__ __launch_bounds__(256) void k_grad_total(GradArgs a) {
     a.total[1] = f >= 1.0 ? 1.f : (float)f;  // a NaN stays one
 }
 
+// 16 bytes of elements times f, rounded to their type.
+template <int T>
+__device__ __forceinline__ u32x4 scale16(u32x4 r, float f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const unsigned u = r[e];
+        if constexpr (T == kF32) {
+            r[e] = __float_as_uint(__uint_as_float(u) * f);
+        } else if constexpr (T == kBF16) {
+            const float2_t t = {__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f};
+            r[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(t, bf162_t));
+        } else {
+            const half2_t h = __builtin_bit_cast(half2_t, u);
+            const float2_t t = {(float)h[0] * f, (float)h[1] * f};
+            r[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(t, half2_t));
+        }
+    }
+    return r;
+}
+
 template <int T>
 __device__ __forceinline__ void run_scale(void* g, float f, int64_t begin, int64_t end) {
-    constexpr int kVec = T == kF32 ? 4 : 8, kSize = T == kF32 ? 4 : 2;
-    char* p = reinterpret_cast<char*>(g);
+    constexpr int kVec = T == kF32 ? 4 : 8, kSize = T == kF32 ? 4 : 2, kUnroll = 4;
+    char* p = reinterpret_cast<char*>(g) + (int64_t)threadIdx.x * kVec * kSize;
     int64_t i = begin;
-    for (; i + 256 * kVec <= end; i += 256 * kVec) {
-        char* q = p + (i + (int64_t)threadIdx.x * kVec) * kSize;
-        u32x4 r = load16(q);
+    for (; i + 256 * kVec * kUnroll <= end; i += 256 * kVec * kUnroll) {
+        u32x4 r[kUnroll];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned u = r[e];
-            if constexpr (T == kF32) {
-                r[e] = __float_as_uint(__uint_as_float(u) * f);
-            } else if constexpr (T == kBF16) {
-                const float2_t t = {__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f};
-                r[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(t, bf162_t));
-            } else {
-                const half2_t h = __builtin_bit_cast(half2_t, u);
-                const float2_t t = {(float)h[0] * f, (float)h[1] * f};
-                r[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(t, half2_t));
-            }
-        }
-        store16(q, r);
+        for (int k = 0; k < kUnroll; ++k) r[k] = stream16(p + (i + k * 256 * kVec) * kSize);
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) put_stream16(p + (i + k * 256 * kVec) * kSize, scale16<T>(r[k], f));
     }
+    for (; i + 256 * kVec <= end; i += 256 * kVec) put_stream16(p + i * kSize, scale16<T>(stream16(p + i * kSize), f));
     for (i += threadIdx.x; i < end; i += 256) {
         const float v = element<T>(g, i) * f;
         if constexpr (T == kF32) reinterpret_cast<float*>(g)[i] = v;

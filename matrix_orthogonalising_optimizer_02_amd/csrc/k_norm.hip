@@ -7,11 +7,18 @@
 //
 // Both passes are HBM-bound: forward reads x and writes y, backward reads x and dy and
 // writes dx, and a row stays in registers between its statistics and its output, so every
-// element moves once. A row is shared by 8 to 64 lanes of a wave or by the waves of a
-// block, 16 bytes a lane and load; a block walks through consecutive rows of one group
-// with that group's weights in registers, and asks for the next row before it reduces the
-// present one. Statistics are two-pass over the registers (the mean first, then the
-// squares of the differences), all sums in fp32 in a fixed order.
+// element moves once. A row is shared by 8 to 64 lanes of a wave or by 2 to 16 whole waves
+// (a "team"), 16 bytes a lane and load, with the group's weights and the sums for their
+// gradients in registers. The blocks of a group take its rows in turn, so that all blocks
+// together read one stretch of memory at a time ([8192, 4096] fp32 backward 76 us; 84 us
+// where each block has a stretch of its own), and ask for the next rows before they reduce
+// the present one. Statistics are two-pass over the registers (the mean first, then the
+// squares of the differences), all sums in fp32 in a fixed order. Outputs are stored with
+// the non-temporal hint ([8192, 5120] bf16 forward 31 us; 40 us without), inputs are read
+// without it (a preceding kernel may have left them in the cache).
+// Measured: [8192, 5120] bf16 in 8 groups, forward 29.4 us (5.7 TB/s), backward 52.9 us
+// (4.8 TB/s with the weights' gradients, 5.4 TB/s without); [65536, 5120] backward 400 us
+// (5.0 TB/s); a copy reaches 6.25 TB/s.
 #include "lanes.hpp"
 #include "train.hpp"
 
@@ -82,66 +89,45 @@ struct Elem<kF16> {
     }
 };
 
-// The vector at p, of which the first `valid` elements exist; zeros in the others.
-template <int T>
-__device__ __forceinline__ u32x4 load_raw(const typename Elem<T>::type* p, int valid) {
-    constexpr int kVec = Elem<T>::kVec;
-    u32x4 r = {0u, 0u, 0u, 0u};
-    if (valid >= kVec) {
-        r = load16(p);
-    } else if (valid > 0) {
-        if constexpr (T == kF32) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < valid) r[e] = __float_as_uint(p[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < valid)
-                    r[e / 2] |= (unsigned)reinterpret_cast<const unsigned short*>(p)[e] << (16 * (e & 1));
-        }
-    }
-    return r;
-}
-
-template <int T>
-__device__ __forceinline__ void store_raw(typename Elem<T>::type* p, u32x4 r, int valid) {
-    constexpr int kVec = Elem<T>::kVec;
-    if (valid >= kVec) {
-        store16(p, r);
-    } else if (valid > 0) {
-        if constexpr (T == kF32) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < valid) p[e] = __uint_as_float(r[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < valid)
-                    reinterpret_cast<unsigned short*>(p)[e] = (unsigned short)(r[e / 2] >> (16 * (e & 1)));
-        }
-    }
-}
-
-// `kVec` weights (or biases) starting at element `at` of a row of type `wdtype`, in fp32.
+// A lane's vector of a row of at least kVec elements. The last vector of a row whose length
+// kVec does not divide starts kVec elements before the row's end, so that every access is
+// whole and unconditional; its first `skip` elements are the vector before's, count in no
+// sum and are written twice with the same bits. A lane past the row's end has skip == kVec
+// and writes nothing.
 template <int kVec>
-__device__ __forceinline__ void load_params(const void* base, int64_t at, int wdtype, int valid, float* f) {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) f[e] = 0.f;
+struct Span {
+    int col, skip;
+    __device__ __forceinline__ Span(int cols, int index) {
+        const int c = index * kVec;
+        col = min(c, cols - kVec);
+        skip = min(c - col, kVec);
+    }
+};
+
+// f with the elements that do not count set to 0. kExact: the row fills all lanes' vectors.
+template <bool kExact, int kVec>
+__device__ __forceinline__ float counted(const Span<kVec>& sp, int e, float f) {
+    return kExact || e >= sp.skip ? f : 0.f;
+}
+
+// kVec weights (or biases) from element `at` of a row of type `wdtype`, in fp32.
+template <int kVec>
+__device__ __forceinline__ void load_params(const void* base, int64_t at, int wdtype, float* f) {
     if (wdtype == kF32) {
         const float* p = reinterpret_cast<const float*>(base) + at;
 #pragma unroll
-        for (int q = 0; q < kVec / 4; ++q) Elem<kF32>::unpack(load_raw<kF32>(p + 4 * q, valid - 4 * q), f + 4 * q);
+        for (int q = 0; q < kVec / 4; ++q) Elem<kF32>::unpack(load16(p + 4 * q), f + 4 * q);
     } else {
-        // the two 16-bit types differ in the conversion alone; a 4-element vector (fp32 rows)
-        // is the first half of an 8-element one
-        const __bf16* p = reinterpret_cast<const __bf16*>(base) + at;
-        const u32x4 r = load_raw<kBF16>(p, min(valid, kVec));
-        float t[8];
-        if (wdtype == kBF16) Elem<kBF16>::unpack(r, t);
-        else Elem<kF16>::unpack(r, t);
+        // the two 16-bit types differ in the conversion alone
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(base) + at;
+        if constexpr (kVec == 8) {
+            const u32x4 r = load16(p);
+            if (wdtype == kBF16) Elem<kBF16>::unpack(r, f);
+            else Elem<kF16>::unpack(r, f);
+        } else {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = t[e];
+            for (int e = 0; e < kVec; ++e) f[e] = wdtype == kBF16 ? bf2f(p[e]) : (float)__builtin_bit_cast(_Float16, p[e]);
+        }
     }
 }
 
@@ -158,327 +144,476 @@ __device__ __forceinline__ int64_t row_offset(const NormArgs& a, const RowsPtr& 
     return (int64_t)q * p.s0 + (int64_t)(r - q * (unsigned)a.inner) * p.s1;
 }
 
-// kLanes: lanes of a row within a wave, or 0 where the whole block shares a row.
+// The threads that share a row: kLanes of a wave, or (0) a.team_waves whole waves.
 template <int kLanes>
-struct RowTeam {
-    static __device__ __forceinline__ int lane() { return kLanes ? threadIdx.x & (kLanes - 1) : threadIdx.x; }
-    static __device__ __forceinline__ int team() { return kLanes ? threadIdx.x / (kLanes ? kLanes : 1) : 0; }
-    static __device__ __forceinline__ int lanes() { return kLanes ? kLanes : blockDim.x; }
-    static __device__ __forceinline__ int teams() { return kLanes ? blockDim.x / (kLanes ? kLanes : 1) : 1; }
+struct Team {
+    int lane, team, lanes, teams;
+    __device__ __forceinline__ explicit Team(const NormArgs& a) {
+        if constexpr (kLanes != 0) {
+            lanes = kLanes;
+            lane = threadIdx.x & (kLanes - 1);
+            team = threadIdx.x / (kLanes ? kLanes : 1);
+            teams = blockDim.x / (kLanes ? kLanes : 1);
+        } else {
+            lanes = a.team_waves * 64;
+            teams = a.teams;
+            team = __builtin_amdgcn_readfirstlane((int)threadIdx.x / lanes);
+            lane = threadIdx.x - team * lanes;
+        }
+    }
 };
 
 constexpr int kMaxWaves = 16;
 
-// Sum over the row's lanes. Whole-block rows go through `red` (one slot a wave): the
-// caller alternates between two buffers, so that the one barrier of the next sum stands
-// between a buffer's reads and its next writes.
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-    if constexpr (kLanes) {
-        return lanes_sum<kLanes>(v);
+// kCount sums over the row's lanes. Teams of several waves exchange them through `red`,
+// one slot a wave, behind one barrier of the whole block: every team runs the same number
+// of sums. The caller alternates between two buffers, so that the next sum's barrier
+// stands between a buffer's reads and its next writes.
+template <int kLanes, int kCount>
+__device__ __forceinline__ void row_sums(float (&v)[kCount], float (*red)[kCount], const Team<kLanes>& t, int team_waves) {
+    if constexpr (kLanes != 0) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) v[i] = lanes_sum<kLanes>(v[i]);
     } else {
-        v = lanes_sum<64>(v);
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) v[i] = lanes_sum<64>(v[i]);
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) red[threadIdx.x >> 6][i] = v[i];
+        }
         __syncthreads();
-        const int nw = blockDim.x >> 6;
-        float s = red[0];
-        for (int i = 1; i < nw; ++i) s += red[i];
-        return s;
+        const int first = t.team * team_waves;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) v[i] = red[first][i];
+        for (int w = 1; w < team_waves; ++w)
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) v[i] += red[first + w][i];
     }
 }
 
-template <int T, bool kRms, int kLanes, int kN>
-__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_norm_forward(NormArgs a) {
+constexpr int kSubThreads = 512;  // most threads of a block whose rows share a wave
+
+template <int T, bool kRms, int kLanes, int kN, bool kExact>
+__global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_forward(NormArgs a) {
     typedef Elem<T> E;
     typedef typename E::type elem;
-    typedef RowTeam<kLanes> Team;
     constexpr int kVec = E::kVec;
-    __shared__ float red[2][kMaxWaves];
+    __shared__ float red[2][kMaxWaves][1];
+    const Team<kLanes> t(a);
     const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
     const unsigned row0 = (unsigned)group * a.rows_per_group;
-    const int begin = chunk * a.chunk_rows;
-    const int end = min(begin + a.chunk_rows, a.rows_per_group);
-    int col[kN], valid[kN];
-    float w[kN][kVec], b[kN][kVec];
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-        col[k] = (k * Team::lanes() + Team::lane()) * kVec;
-        valid[k] = a.cols - col[k];
-        if (a.w) {
-            load_params<kVec>(a.w, (int64_t)group * a.w_stride + col[k], a.wdtype, valid[k], w[k]);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) w[k][e] += a.offset;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) w[k][e] = 1.f;
-        }
-        if (a.b) {
-            load_params<kVec>(a.b, (int64_t)group * a.b_stride + col[k], a.wdtype, valid[k], b[k]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) b[k][e] = 0.f;
-        }
-    }
-    const int step = Team::teams();
+    const int begin = chunk * t.teams, end = a.rows_per_group, step = a.chunks * t.teams;
     // every lane of a wave takes part in every sum: a team past the end repeats the last
     // row and writes nothing
     u32x4 next[kN];
-    {
-        const unsigned r = row0 + min(begin + Team::team(), end - 1);
+    auto fetch = [&](int at) {
+        const unsigned r = row0 + min(at + t.team, end - 1);
         const elem* p = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, r);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) next[k] = load_raw<T>(p + col[k], valid[k]);
+        for (int k = 0; k < kN; ++k)
+            next[k] = load16(p + Span<kVec>(a.cols, k * t.lanes + t.lane).col);
+    };
+    fetch(begin);
+    float w[kN][kVec], b[kN][kVec];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            w[k][e] = 1.f;
+            b[k][e] = 0.f;
+        }
+        if (a.w) {
+            load_params<kVec>(a.w, (int64_t)group * a.w_stride + sp.col, a.wdtype, w[k]);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w[k][e] += a.offset;
+        }
+        if (a.b) load_params<kVec>(a.b, (int64_t)group * a.b_stride + sp.col, a.wdtype, b[k]);
     }
+    int flip = 0;
     for (int at = begin; at < end; at += step) {
-        const unsigned r = row0 + min(at + Team::team(), end - 1);
-        const bool mine = at + Team::team() < end;
+        const unsigned r = row0 + min(at + t.team, end - 1);
+        const bool mine = at + t.team < end;
         float x[kN][kVec];
 #pragma unroll
         for (int k = 0; k < kN; ++k) E::unpack(next[k], x[k]);
-        if (at + step < end) {
-            const unsigned rn = row0 + min(at + step + Team::team(), end - 1);
-            const elem* p = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, rn);
-#pragma unroll
-            for (int k = 0; k < kN; ++k) next[k] = load_raw<T>(p + col[k], valid[k]);
-        }
+        if (at + step < end) fetch(at + step);
         float mean = 0.f;
         if constexpr (!kRms) {
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < kN; ++k)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) s += x[k][e];
-            mean = row_sum<kLanes>(s, red[0]) * a.inv_cols;
-#pragma unroll
             for (int k = 0; k < kN; ++k) {
-                if (valid[k] >= kVec) {
+                const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) x[k][e] -= mean;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) x[k][e] = e < valid[k] ? x[k][e] - mean : 0.f;
-                }
+                for (int e = 0; e < kVec; ++e) s += k < kN - 1 ? x[k][e] : counted<kExact>(sp, e, x[k][e]);
             }
+            float sum[1] = {s};
+            row_sums<kLanes, 1>(sum, red[0], t, a.team_waves);
+            mean = sum[0] * a.inv_cols;
         }
         float sq = 0.f;
 #pragma unroll
-        for (int k = 0; k < kN; ++k)
+        for (int k = 0; k < kN; ++k) {
+            const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) sq = fmaf(x[k][e], x[k][e], sq);
+            for (int e = 0; e < kVec; ++e) {
+                if constexpr (!kRms) x[k][e] -= mean;
+                const float d = k < kN - 1 ? x[k][e] : counted<kExact>(sp, e, x[k][e]);
+                sq = fmaf(d, d, sq);
+            }
+        }
         // the rms form has one sum a row, and alternates over the rows
-        const int buf = kRms ? ((at - begin) & 1) : 1;
-        const float rstd = 1.f / sqrtf(fmaf(row_sum<kLanes>(sq, red[buf]), a.inv_cols, a.eps));
+        float sum[1] = {sq};
+        row_sums<kLanes, 1>(sum, red[kRms ? flip : 1], t, a.team_waves);
+        flip ^= 1;
+        const float rstd = 1.f / sqrtf(fmaf(sum[0], a.inv_cols, a.eps));
         if (mine) {
-            if (Team::lane() == 0) {
+            if (t.lane == 0) {
                 if (!kRms && a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
             }
             elem* q = reinterpret_cast<elem*>(a.y.data) + row_offset(a, a.y, r);
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
+                const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
                 float y[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) y[e] = fmaf(x[k][e] * rstd, w[k][e], b[k][e]);
-                store_raw<T>(q + col[k], E::pack(y), valid[k]);
+                if (kExact || k < kN - 1 || sp.skip < kVec) put_stream16(q + sp.col, E::pack(y));
             }
         }
     }
 }
 
-template <int T, bool kRms, int kLanes, int kN>
-__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_norm_backward(NormArgs a) {
+template <int T, bool kRms, int kLanes, int kN, bool kExact>
+__global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(NormArgs a) {
     typedef Elem<T> E;
     typedef typename E::type elem;
-    typedef RowTeam<kLanes> Team;
     constexpr int kVec = E::kVec;
-    __shared__ float red[2][2][kMaxWaves];
+    __shared__ float red[2][kMaxWaves][2];
+    const Team<kLanes> t(a);
     const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
     const unsigned row0 = (unsigned)group * a.rows_per_group;
-    const int begin = chunk * a.chunk_rows;
-    const int end = min(begin + a.chunk_rows, a.rows_per_group);
-    int col[kN], valid[kN];
-    float w[kN][kVec], dw[kN][kVec], db[kN][kVec];
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-        col[k] = (k * Team::lanes() + Team::lane()) * kVec;
-        valid[k] = a.cols - col[k];
-        if (a.w) {
-            load_params<kVec>(a.w, (int64_t)group * a.w_stride + col[k], a.wdtype, valid[k], w[k]);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) w[k][e] += a.offset;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) w[k][e] = 1.f;
-        }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) dw[k][e] = db[k][e] = 0.f;
-    }
-    const int step = Team::teams();
-    u32x4 xn[kN], gn[kN];
-    float mean_n = 0.f, rstd_n = 0.f;
-    auto fetch = [&](int at) {
-        const unsigned r = row0 + min(at + Team::team(), end - 1);
-        const bool mine = at + Team::team() < end;
+    const int begin = chunk * t.teams, end = a.rows_per_group, step = a.chunks * t.teams;
+    // Rows asked for in advance: two where a lane holds 8 elements. 16 elements leave no
+    // registers for that ([1024, 16384] fp32: 53 us without, 76 us with one row and spills).
+    constexpr int kAhead = kN * kVec <= 8 ? 2 : 0;
+    struct Row {
+        u32x4 x[kN], g[kN];
+        float mean, rstd;
+    };
+    Row ahead[kAhead ? kAhead : 1];
+    auto fetch = [&](Row& row, int at) {
+        const unsigned r = row0 + min(at + t.team, end - 1);
         const elem* px = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, r);
         const elem* pg = reinterpret_cast<const elem*>(a.dy.data) + row_offset(a, a.dy, r);
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            xn[k] = load_raw<T>(px + col[k], valid[k]);
-            // a team past the end adds nothing to the sums over rows
-            gn[k] = load_raw<T>(pg + col[k], mine ? valid[k] : 0);
+            const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
+            row.x[k] = load16(px + sp.col);
+            row.g[k] = load16(pg + sp.col);
         }
-        if constexpr (!kRms) mean_n = a.mean[r];
-        rstd_n = a.rstd[r];
+        row.mean = kRms ? 0.f : a.mean[r];
+        row.rstd = a.rstd[r];
     };
-    if (begin < end) fetch(begin);
-    for (int at = begin; at < end; at += step) {
-        const unsigned r = row0 + min(at + Team::team(), end - 1);
-        const bool mine = at + Team::team() < end;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (begin + i * step < end) fetch(ahead[i], begin + i * step);
+    float w[kN][kVec], dw[kN][kVec], db[kN][kVec];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            w[k][e] = 1.f;
+            dw[k][e] = db[k][e] = 0.f;
+        }
+        if (a.w) {
+            load_params<kVec>(a.w, (int64_t)group * a.w_stride + sp.col, a.wdtype, w[k]);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w[k][e] += a.offset;
+        }
+    }
+    int flip = 0;
+    auto process = [&](Row& row, int at) {
+        const bool mine = at + t.team < end;  // a team past the end adds and writes nothing
+        if constexpr (kAhead == 0) fetch(row, at);
+        const float mean = row.mean, rstd = row.rstd;
         float h[kN][kVec], g[kN][kVec];
-        const float mean = mean_n, rstd = rstd_n;
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            E::unpack(xn[k], h[k]);
-            E::unpack(gn[k], g[k]);
+            E::unpack(row.x[k], h[k]);
+            E::unpack(row.g[k], g[k]);
         }
-        if (at + step < end) fetch(at + step);
-        float s1 = 0.f, s2 = 0.f;
+        if (kAhead && at + kAhead * step < end) fetch(row, at + kAhead * step);
+        float sums[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kN; ++k)
+        for (int k = 0; k < kN; ++k) {
+            const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const float hv = kRms ? h[k][e] * rstd : (h[k][e] - mean) * rstd;
-                dw[k][e] = fmaf(g[k][e], hv, dw[k][e]);
-                db[k][e] += g[k][e];
-                const float av = g[k][e] * w[k][e];
-                s1 += av;
-                s2 = fmaf(av, hv, s2);
+                // the weights' sums take an element that does not count too: its lane does
+                // not write them
+                const float gv = mine ? g[k][e] : 0.f;
+                dw[k][e] = fmaf(gv, hv, dw[k][e]);
+                db[k][e] += gv;
+                const float av = gv * w[k][e];
+                const float ac = k < kN - 1 ? av : counted<kExact>(sp, e, av);
+                sums[0] += ac;
+                sums[1] = fmaf(ac, hv, sums[1]);
                 h[k][e] = hv;
                 g[k][e] = av;
             }
-        if constexpr (kLanes != 0) {
-            if constexpr (!kRms) s1 = lanes_sum<kLanes>(s1);
-            s2 = lanes_sum<kLanes>(s2);
-        } else {
-            // both sums behind one barrier; the buffers alternate over the rows
-            if constexpr (!kRms) s1 = lanes_sum<64>(s1);
-            s2 = lanes_sum<64>(s2);
-            float (*buf)[kMaxWaves] = red[(at - begin) & 1];
-            if ((threadIdx.x & 63) == 0) {
-                buf[0][threadIdx.x >> 6] = s1;
-                buf[1][threadIdx.x >> 6] = s2;
-            }
-            __syncthreads();
-            const int nw = blockDim.x >> 6;
-            s1 = buf[0][0];
-            s2 = buf[1][0];
-            for (int i = 1; i < nw; ++i) {
-                s1 += buf[0][i];
-                s2 += buf[1][i];
-            }
         }
+        row_sums<kLanes, 2>(sums, red[flip], t, a.team_waves);
+        flip ^= 1;
         if (mine) {
-            const float c1 = kRms ? 0.f : s1 * a.inv_cols, c2 = s2 * a.inv_cols;
-            elem* q = reinterpret_cast<elem*>(a.y.data) + row_offset(a, a.y, r);
+            const float c1 = kRms ? 0.f : sums[0] * a.inv_cols, c2 = sums[1] * a.inv_cols;
+            elem* q = reinterpret_cast<elem*>(a.y.data) + row_offset(a, a.y, row0 + at + t.team);
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
+                const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
                 float d[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) d[e] = rstd * fmaf(-h[k][e], c2, g[k][e] - c1);
-                store_raw<T>(q + col[k], E::pack(d), valid[k]);
+                if (kExact || k < kN - 1 || sp.skip < kVec) put_stream16(q + sp.col, E::pack(d));
             }
+        }
+    };
+    for (int at = begin; at < end;) {
+#pragma unroll
+        for (int i = 0; i < (kAhead ? kAhead : 1); ++i) {
+            process(ahead[i], at);
+            at += step;
+            if (at >= end) break;
         }
     }
     if (!a.dw && !a.db) return;
-    // the block's sums over its rows: first over its teams (through LDS, in team order)
-    if constexpr (kLanes != 0) {
-        constexpr int kTeams = 256 / kLanes, kWidth = kLanes * kVec * kN;
-        __shared__ float sums[kTeams][kWidth];
+    // The block's sums over its rows: over its teams through LDS, in team order, then to
+    // the gradients or to the block's partial sums.
+    extern __shared__ float part[];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < 2; ++which) {
+        void* out = which ? a.db : a.dw;
+        if (!out) continue;
+        const int64_t to = (int64_t)group * (which ? a.db_stride : a.dw_stride);
+        float* partial = a.partial + ((int64_t)which * a.groups * a.chunks + blockIdx.x) * a.cols;
+        if constexpr (kLanes != 0) {
+            // [team][column], each team's row of LDS
+            const Span<kVec> sp(a.cols, t.lane);
+            constexpr int kWidth = kLanes * kVec;
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kN; ++k)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-                    sums[Team::team()][col[k] + e] = which ? db[k][e] : dw[k][e];
+            for (int e = 0; e < kVec; ++e)
+                if (e >= sp.skip) part[t.team * kWidth + sp.col + e] = which ? db[0][e] : dw[0][e];
             __syncthreads();
-            void* out = which ? a.db : a.dw;
-            const int64_t stride = which ? a.db_stride : a.dw_stride;
-            if (out) {
-                for (int c = threadIdx.x; c < a.cols; c += 256) {
-                    float s = sums[0][c];
-                    for (int t = 1; t < kTeams; ++t) s += sums[t][c];
-                    if (a.chunks == 1) store_param(out, (int64_t)group * stride + c, a.wdtype, s);
-                    else a.partial[((int64_t)which * a.groups * a.chunks + blockIdx.x) * a.cols + c] = s;
-                }
+            for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+                float s = part[c];
+                for (int i = 1; i < t.teams; ++i) s += part[i * kWidth + c];
+                if (a.chunks == 1) store_param(out, to + c, a.wdtype, s);
+                else partial[c] = s;
             }
-        }
-    } else {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            void* out = which ? a.db : a.dw;
-            const int64_t stride = which ? a.db_stride : a.dw_stride;
-            if (!out) continue;
-            float* part = a.partial + ((int64_t)which * a.groups * a.chunks + blockIdx.x) * a.cols;
+        } else if (t.teams == 1) {  // every column is one thread's
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
+                const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
                 const float* v = which ? db[k] : dw[k];
-                if (a.chunks == 1) {
+                if (a.chunks > 1 && sp.skip == 0) {
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if (e < valid[k]) store_param(out, (int64_t)group * stride + col[k] + e, a.wdtype, v[e]);
+                    for (int q = 0; q < kVec / 4; ++q) store16(partial + sp.col + 4 * q, Elem<kF32>::pack(v + 4 * q));
                 } else {
 #pragma unroll
-                    for (int q = 0; q < kVec / 4; ++q)
-                        store_raw<kF32>(part + col[k] + 4 * q, Elem<kF32>::pack(v + 4 * q), valid[k] - 4 * q);
+                    for (int e = 0; e < kVec; ++e) {
+                        if (e < sp.skip) continue;
+                        if (a.chunks > 1) partial[sp.col + e] = v[e];
+                        else store_param(out, to + sp.col + e, a.wdtype, v[e]);
+                    }
                 }
+            }
+        } else {
+            for (int i = 0; i < t.teams; ++i) {
+                __syncthreads();
+                if (t.team != i) continue;
+#pragma unroll
+                for (int k = 0; k < kN; ++k) {
+                    const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        if (e < sp.skip) continue;
+                        const float v = which ? db[k][e] : dw[k][e];
+                        part[sp.col + e] = i ? part[sp.col + e] + v : v;
+                    }
+                }
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+                if (a.chunks == 1) store_param(out, to + c, a.wdtype, part[c]);
+                else partial[c] = part[c];
             }
         }
     }
 }
 
-// Adds the blocks' partial sums of one group, 64 columns a block: each of 16 waves takes
-// every sixteenth partial row, and the waves' sums are added in order.
-constexpr int kWgradCols = 64, kWgradWaves = 16;
-__global__ __launch_bounds__(kWgradCols * kWgradWaves) void k_norm_wgrad(NormArgs a) {
-    __shared__ float sums[kWgradWaves][kWgradCols];
-    const int which = blockIdx.z, group = blockIdx.y;
-    void* out = which ? a.db : a.dw;
-    if (!out) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * kWgradCols + lane;
-    float s = 0.f;
-    if (c < a.cols) {
-        const float* p = a.partial + ((int64_t)which * a.groups * a.chunks + (int64_t)group * a.chunks) * a.cols + c;
-        for (int i = wave; i < a.chunks; i += kWgradWaves) s += p[(int64_t)i * a.cols];
+// Rows shorter than a vector: a thread a row.
+constexpr int kTinyCols = 8;
+template <int T>
+__device__ __forceinline__ float load_elem(const void* base, int64_t i) {
+    if constexpr (T == kF32) return reinterpret_cast<const float*>(base)[i];
+    else if constexpr (T == kBF16) return bf2f(reinterpret_cast<const unsigned short*>(base)[i]);
+    else return (float)reinterpret_cast<const _Float16*>(base)[i];
+}
+
+__device__ __forceinline__ float load_param(const void* base, int64_t i, int wdtype) {
+    return wdtype == kF32 ? load_elem<kF32>(base, i) : wdtype == kBF16 ? load_elem<kBF16>(base, i) : load_elem<kF16>(base, i);
+}
+
+template <int T, bool kRms>
+__global__ __launch_bounds__(256) void k_norm_forward_tiny(NormArgs a) {
+    const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
+    const int at = chunk * a.chunk_rows + threadIdx.x;
+    if (threadIdx.x >= a.chunk_rows || at >= a.rows_per_group) return;
+    const unsigned r = (unsigned)group * a.rows_per_group + at;
+    const int64_t px = row_offset(a, a.x, r), py = row_offset(a, a.y, r);
+    float x[kTinyCols], mean = 0.f, sq = 0.f;
+#pragma unroll
+    for (int e = 0; e < kTinyCols; ++e) {
+        x[e] = e < a.cols ? load_elem<T>(a.x.data, px + e) : 0.f;
+        mean += x[e];
     }
-    sums[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < a.cols) {
-        for (int t = 1; t < kWgradWaves; ++t) s += sums[t][lane];
-        store_param(out, (int64_t)group * (which ? a.db_stride : a.dw_stride) + c, a.wdtype, s);
+    mean = kRms ? 0.f : mean * a.inv_cols;
+#pragma unroll
+    for (int e = 0; e < kTinyCols; ++e) {
+        x[e] = e < a.cols ? x[e] - mean : 0.f;
+        sq = fmaf(x[e], x[e], sq);
+    }
+    const float rstd = 1.f / sqrtf(fmaf(sq, a.inv_cols, a.eps));
+    if (!kRms && a.mean) a.mean[r] = mean;
+    if (a.rstd) a.rstd[r] = rstd;
+#pragma unroll
+    for (int e = 0; e < kTinyCols; ++e) {
+        if (e >= a.cols) break;
+        const float w = a.w ? a.offset + load_param(a.w, (int64_t)group * a.w_stride + e, a.wdtype) : 1.f;
+        const float b = a.b ? load_param(a.b, (int64_t)group * a.b_stride + e, a.wdtype) : 0.f;
+        store_param(a.y.data, py + e, T, fmaf(x[e] * rstd, w, b));
     }
 }
 
-template <bool kFwd, int T, bool kRms, int kLanes, int kN>
+template <int T, bool kRms>
+__global__ __launch_bounds__(256) void k_norm_backward_tiny(NormArgs a) {
+    __shared__ float red[4];
+    const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
+    const int begin = chunk * a.chunk_rows, end = min(begin + a.chunk_rows, a.rows_per_group);
+    float w[kTinyCols], dw[kTinyCols], db[kTinyCols];
+#pragma unroll
+    for (int e = 0; e < kTinyCols; ++e) {
+        w[e] = a.w && e < a.cols ? a.offset + load_param(a.w, (int64_t)group * a.w_stride + e, a.wdtype) : 1.f;
+        dw[e] = db[e] = 0.f;
+    }
+    for (int at = begin + threadIdx.x; at < end; at += 256) {
+        const unsigned r = (unsigned)group * a.rows_per_group + at;
+        const int64_t px = row_offset(a, a.x, r), pg = row_offset(a, a.dy, r), pd = row_offset(a, a.y, r);
+        const float mean = kRms ? 0.f : a.mean[r], rstd = a.rstd[r];
+        float h[kTinyCols], g[kTinyCols], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < kTinyCols; ++e) {
+            const bool in = e < a.cols;
+            h[e] = in ? (load_elem<T>(a.x.data, px + e) - mean) * rstd : 0.f;
+            g[e] = in ? load_elem<T>(a.dy.data, pg + e) : 0.f;
+            dw[e] = fmaf(g[e], h[e], dw[e]);
+            db[e] += g[e];
+            g[e] *= w[e];
+            s1 += g[e];
+            s2 = fmaf(g[e], h[e], s2);
+        }
+        const float c1 = kRms ? 0.f : s1 * a.inv_cols, c2 = s2 * a.inv_cols;
+#pragma unroll
+        for (int e = 0; e < kTinyCols; ++e)
+            if (e < a.cols) store_param(a.y.data, pd + e, T, rstd * fmaf(-h[e], c2, g[e] - c1));
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        void* out = which ? a.db : a.dw;
+        if (!out) continue;
+#pragma unroll
+        for (int e = 0; e < kTinyCols; ++e) {
+            const float s = block_sum_256(which ? db[e] : dw[e], red);
+            if (threadIdx.x != 0 || e >= a.cols) continue;
+            if (a.chunks == 1) store_param(out, (int64_t)group * (which ? a.db_stride : a.dw_stride) + e, a.wdtype, s);
+            else a.partial[((int64_t)which * a.groups * a.chunks + blockIdx.x) * a.cols + e] = s;
+        }
+    }
+}
+
+// Adds the blocks' partial sums of one group. The threads of a block are `slices` rows of
+// columns: each takes every slices-th partial row, eight loads at a time, and the slices'
+// sums are added in order.
+constexpr int kWgradThreads = 512;
+__global__ __launch_bounds__(kWgradThreads) void k_norm_wgrad(NormArgs a, int slices) {
+    __shared__ float sums[kWgradThreads];
+    const int which = a.dw ? blockIdx.z : 1, group = blockIdx.y;
+    const int width = kWgradThreads / slices;  // both powers of two
+    const int lane = threadIdx.x & (width - 1), slice = threadIdx.x / width;
+    const int c = blockIdx.x * width + lane;
+    constexpr int kUnroll = 8;
+    float s[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) s[k] = 0.f;
+    if (c < a.cols) {
+        const float* p = a.partial + ((int64_t)which * a.groups * a.chunks + (int64_t)group * a.chunks) * a.cols + c;
+        int i = slice;
+        for (; i + (kUnroll - 1) * slices < a.chunks; i += kUnroll * slices)
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) s[k] += p[(int64_t)(i + k * slices) * a.cols];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+            if (i + k * slices < a.chunks) s[k] += p[(int64_t)(i + k * slices) * a.cols];
+    }
+    float t = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    sums[threadIdx.x] = t;
+    __syncthreads();
+    if (slice == 0 && c < a.cols) {
+        for (int k = 1; k < slices; ++k) t += sums[k * width + lane];
+        store_param(which ? a.db : a.dw, (int64_t)group * (which ? a.db_stride : a.dw_stride) + c, a.wdtype, t);
+    }
+}
+
+template <bool kFwd, int T, bool kRms, int kLanes, int kN, bool kExact>
 hipError_t launch(const NormPlan& p, const NormArgs& a, hipStream_t s) {
     const dim3 grid(unsigned(a.groups) * unsigned(p.chunks)), block(p.threads);
-    if constexpr (kFwd) hipLaunchKernelGGL((k_norm_forward<T, kRms, kLanes, kN>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_norm_backward<T, kRms, kLanes, kN>), grid, block, 0, s, a);
+    if constexpr (kFwd) {
+        hipLaunchKernelGGL((k_norm_forward<T, kRms, kLanes, kN, kExact>), grid, block, 0, s, a);
+    } else {
+        // a team's sums for all columns, or the block's: at most 16 KiB and 8 KiB
+        const bool shared = (a.dw || a.db) && p.teams > 1;
+        const size_t lds = shared ? size_t(4) * (kLanes ? p.threads * Elem<T>::kVec : a.cols) : 0;
+        hipLaunchKernelGGL((k_norm_backward<T, kRms, kLanes, kN, kExact>), grid, block, lds, s, a);
+    }
     return hipGetLastError();
+}
+
+template <bool kFwd, int T, bool kRms, int kLanes>
+hipError_t launch_lanes(const NormPlan& p, const NormArgs& a, hipStream_t s) {
+    if (a.cols == kLanes * Elem<T>::kVec) return launch<kFwd, T, kRms, kLanes, 1, true>(p, a, s);
+    return launch<kFwd, T, kRms, kLanes, 1, false>(p, a, s);
 }
 
 template <bool kFwd, int T, bool kRms>
 hipError_t launch_shape(const NormPlan& p, const NormArgs& a, hipStream_t s) {
-    if (p.lanes == 8) return launch<kFwd, T, kRms, 8, 1>(p, a, s);
-    if (p.lanes == 16) return launch<kFwd, T, kRms, 16, 1>(p, a, s);
-    if (p.lanes == 32) return launch<kFwd, T, kRms, 32, 1>(p, a, s);
-    if (p.lanes == 64) return launch<kFwd, T, kRms, 64, 1>(p, a, s);
-    if (p.vecs == 1) return launch<kFwd, T, kRms, 0, 1>(p, a, s);
-    if (p.vecs == 2) return launch<kFwd, T, kRms, 0, 2>(p, a, s);
+    if (p.lanes == 1) {
+        const dim3 grid(unsigned(a.groups) * unsigned(p.chunks)), block(256);
+        if constexpr (kFwd) hipLaunchKernelGGL((k_norm_forward_tiny<T, kRms>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_norm_backward_tiny<T, kRms>), grid, block, 0, s, a);
+        return hipGetLastError();
+    }
+    if (p.lanes == 8) return launch_lanes<kFwd, T, kRms, 8>(p, a, s);
+    if (p.lanes == 16) return launch_lanes<kFwd, T, kRms, 16>(p, a, s);
+    if (p.lanes == 32) return launch_lanes<kFwd, T, kRms, 32>(p, a, s);
+    if (p.lanes == 64) return launch_lanes<kFwd, T, kRms, 64>(p, a, s);
+    if (p.vecs == 1) return launch<kFwd, T, kRms, 0, 1, false>(p, a, s);
+    if (p.vecs == 2) return launch<kFwd, T, kRms, 0, 2, false>(p, a, s);
     if constexpr (T == kF32) {
-        if (p.vecs == 4) return launch<kFwd, T, kRms, 0, 4>(p, a, s);
+        if (p.vecs == 4) return launch<kFwd, T, kRms, 0, 4, false>(p, a, s);
     }
     return hipErrorInvalidValue;
 }
@@ -491,53 +626,69 @@ hipError_t launch_type(bool rms, int dtype, const NormPlan& p, const NormArgs& a
     return rms ? launch_shape<kFwd, kF16, true>(p, a, s) : launch_shape<kFwd, kF16, false>(p, a, s);
 }
 
-NormPlan plan_shape(int dtype, int64_t cols) {
+// Shapes, measured on MI355X. Forward: a lane holds one vector up to 256 vectors a row, two
+// beyond, in blocks of 4 waves, 24 waves a compute unit in all ([8192, 5120] bf16 29.4 us;
+// 42 us with one vector a lane and 10 waves a row, 31 us with 40 waves a unit). Backward: one
+// vector of 16-bit elements up to 1024 vectors a row (so that a lane's eight columns leave
+// registers for two rows in advance), two of fp32 from 129 vectors on, blocks of 8 waves or
+// one row, and about 10 waves a unit: every block's partial sums are written and read once
+// more, so that fewer blocks win ([8192, 5120] bf16 52.9 us; 58 us with 20 waves, 66 us
+// with 30).
+constexpr int kForwardVectors = 256, kForwardBlockWaves = 4, kForwardWaves = 24;
+constexpr int kBackwardVectors = 1024, kBackwardVectors32 = 128, kBackwardBlockWaves = 8, kBackwardWaves = 10;
+constexpr int kComputeUnits = 256;
+
+// one_vec: rows of up to this many vectors are spread over enough waves that a lane holds one.
+NormPlan plan_shape(int dtype, int64_t cols, int64_t one_vec, int block_waves) {
     const int vec = dtype == kF32 ? 4 : 8;
     const int64_t vectors = (cols + vec - 1) / vec;
     NormPlan p{};
-    if (vectors <= 64) {
+    p.vecs = 1;
+    p.teams = 1;
+    p.threads = 256;
+    if (cols < vec) {
+        p.lanes = 1;
+        p.teams = 256;
+    } else if (vectors <= 64) {
         p.lanes = vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64;
-        p.vecs = 1;
-        p.threads = 256;
-        p.rows_at_once = 256 / p.lanes;
+        p.threads = std::min(block_waves * 64, kSubThreads);
+        p.teams = p.threads / p.lanes;
     } else {
-        p.vecs = vectors <= 256 ? 1 : vectors <= 2048 ? 2 : 4;
-        p.threads = int(((vectors + p.vecs - 1) / p.vecs + 63) / 64 * 64);
-        p.lanes = p.threads > 64 ? p.threads : 128;
-        p.threads = p.lanes;
-        p.rows_at_once = 1;
+        // only the last of a lane's vectors may lie past the row's end
+        p.vecs = vectors <= one_vec ? 1 : vectors <= 2048 ? 2 : 4;
+        p.lanes = std::max(128, int(((vectors + p.vecs - 1) / p.vecs + 63) / 64 * 64));
+        p.teams = std::max(1, block_waves * 64 / p.lanes);
+        p.threads = p.teams * p.lanes;
     }
     return p;
 }
 
-void plan_chunks(NormPlan& p, int64_t rows_per_group, int64_t groups, int64_t blocks, int64_t least_rows) {
-    const int64_t want = std::max<int64_t>(1, blocks / std::max<int64_t>(groups, 1));
-    const int64_t most = std::max<int64_t>(1, (rows_per_group + least_rows - 1) / least_rows);
-    int64_t chunks = std::min(want, most);
-    int64_t rows = std::max<int64_t>(1, (rows_per_group + chunks - 1) / chunks);
-    rows = (rows + p.rows_at_once - 1) / p.rows_at_once * p.rows_at_once;
-    p.chunk_rows = int(rows);
-    p.chunks = int(std::max<int64_t>(1, (rows_per_group + rows - 1) / rows));
+// Splits every group into blocks: so many that the card's compute units hold `waves` waves
+// each, of at least `least` passes of a block.
+void plan_chunks(NormPlan& p, int64_t rows_per_group, int64_t groups, int64_t waves, int64_t least) {
+    const int64_t blocks = kComputeUnits * std::max<int64_t>(1, waves * 64 / p.threads);
+    const int64_t want = std::max<int64_t>(1, (blocks + groups / 2) / std::max<int64_t>(groups, 1));
+    const int64_t most = std::max<int64_t>(1, rows_per_group / (least * p.teams));
+    p.chunks = int(std::min(want, most));
+    p.chunk_rows = int((rows_per_group + p.chunks - 1) / p.chunks);
 }
 
 }  // namespace
 
-#ifndef MUON_NORM_FWD_BLOCKS
-#define MUON_NORM_FWD_BLOCKS 2048
-#endif
-#ifndef MUON_NORM_BWD_BLOCKS
-#define MUON_NORM_BWD_BLOCKS 1024
-#endif
-
 NormPlan plan_norm_forward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups) {
-    NormPlan p = plan_shape(dtype, cols);
-    plan_chunks(p, rows_per_group, groups, MUON_NORM_FWD_BLOCKS, p.rows_at_once);
+    NormPlan p = plan_shape(dtype, cols, kForwardVectors, kForwardBlockWaves);
+    if (p.lanes == 1) {  // one pass of a block
+        p.chunk_rows = p.teams;
+        p.chunks = int((rows_per_group + p.teams - 1) / p.teams);
+        return p;
+    }
+    plan_chunks(p, rows_per_group, groups, kForwardWaves, 1);
     return p;
 }
 
 NormPlan plan_norm_backward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups) {
-    NormPlan p = plan_shape(dtype, cols);
-    plan_chunks(p, rows_per_group, groups, MUON_NORM_BWD_BLOCKS, 4 * p.rows_at_once);
+    NormPlan p = plan_shape(dtype, cols, dtype == kF32 ? kBackwardVectors32 : kBackwardVectors, kBackwardBlockWaves);
+    plan_chunks(p, rows_per_group, groups, kBackwardWaves, 4);
     return p;
 }
 
@@ -550,8 +701,11 @@ hipError_t launch_norm_backward(bool rms, int dtype, const NormPlan& p, const No
 }
 
 hipError_t launch_norm_wgrad(const NormArgs& a, hipStream_t s) {
-    const dim3 grid((a.cols + kWgradCols - 1) / kWgradCols, a.groups, 2);
-    hipLaunchKernelGGL(k_norm_wgrad, grid, dim3(kWgradCols * kWgradWaves), 0, s, a);
+    int slices = 1;
+    while (slices < 16 && slices * 16 < a.chunks) slices *= 2;
+    const int width = kWgradThreads / slices;
+    const dim3 grid((a.cols + width - 1) / width, a.groups, a.dw && a.db ? 2 : 1);
+    hipLaunchKernelGGL(k_norm_wgrad, grid, dim3(kWgradThreads), 0, s, a, slices);
     return hipGetLastError();
 }
 

@@ -6,16 +6,17 @@
 
 namespace muon {
 
-// 16 or 8 bytes at any element alignment (global memory takes unaligned dword accesses).
-struct __attribute__((packed, aligned(2))) Packed16 {
-    u32x4 v;
-};
-struct __attribute__((packed, aligned(2))) Packed8 {
-    u32x2 v;
-};
-__device__ __forceinline__ u32x4 load16(const void* p) { return reinterpret_cast<const Packed16*>(p)->v; }
-__device__ __forceinline__ void store16(void* p, u32x4 v) { reinterpret_cast<Packed16*>(p)->v = v; }
-__device__ __forceinline__ u32x2 load8(const void* p) { return reinterpret_cast<const Packed8*>(p)->v; }
+// 16 bytes at any element alignment (global memory takes unaligned dword accesses).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+__device__ __forceinline__ u32x4 load16(const void* p) { return *reinterpret_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ void store16(void* p, u32x4 v) { *reinterpret_cast<u32x4_any*>(p) = v; }
+// The same with the non-temporal hint, for data that a kernel touches once.
+__device__ __forceinline__ u32x4 stream16(const void* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+}
+__device__ __forceinline__ void put_stream16(void* p, u32x4 v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+}
 
 template <int kCtrl>
 __device__ __forceinline__ unsigned dpp(unsigned v) {

@@ -40,7 +40,9 @@ struct NormArgs {
     uint32_t inner_mul;        // r / inner = (mulhi(r, inner_mul) + r) >> inner_shift, 33-bit sum, for inner > 1
     int32_t inner_shift;
     int32_t chunks;            // blocks of a group
-    int32_t chunk_rows;        // rows of a block: ceil(rows_per_group / chunks)
+    int32_t chunk_rows;        // rows of a block (rows shorter than a vector)
+    int32_t team_waves;        // waves that share a row (rows of whole waves)
+    int32_t teams;             // rows that a block takes at a time
     int32_t wdtype;
     float eps, offset;
     float inv_cols;
@@ -49,15 +51,15 @@ struct NormArgs {
 // Columns up to this fit the registers of one 1024-thread block, 16 a thread.
 constexpr int kNormMaxCols = 16 * 1024;
 
-// How the kernels split a norm's rows: `lanes` threads share a row (a power of two up to
-// 64, or whole waves), each holding `vecs` 16-byte vectors of it.
+// How the kernels split a norm's rows: `lanes` threads share a row (1 for rows shorter than
+// a vector, 8 to 64, or the whole block), each holding `vecs` 16-byte vectors of it.
 struct NormPlan {
     int lanes;
     int vecs;
+    int teams;         // rows that a block takes at a time
     int threads;       // of a block
-    int rows_at_once;  // rows that a block holds at a time
-    int chunks;
-    int chunk_rows;
+    int chunks;        // blocks of a group
+    int chunk_rows;    // rows of a block
 };
 NormPlan plan_norm_forward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);
 NormPlan plan_norm_backward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);
@@ -71,7 +73,8 @@ hipError_t launch_norm_wgrad(const NormArgs& a, hipStream_t s);
 // are written by kernels whose arguments carry the descriptors: no copy from host memory,
 // so nothing of the caller's has to outlive the call.
 constexpr int kQBlock = 256;             // elements of 8-bit state that share a scale
-constexpr int kMultiBlockElems = 4096;   // elements of a block of the AdamW step
+constexpr int kMultiThreads = 256;       // of a block of the AdamW step
+constexpr int kMultiBlockElems = 16 * kMultiThreads;  // its elements
 
 struct MultiDesc {
     float* w;
@@ -100,6 +103,7 @@ struct MultiArgs {
     const MultiDesc* table;
     const int32_t* tensor_of_block;
     int32_t blocks;
+    int32_t bits;          // 8 or 32: the width of all states; 0: both occur
     uint32_t key;          // of (seed, step)
     float beta1, beta2, one_minus_beta1, one_minus_beta2;
     float eps;

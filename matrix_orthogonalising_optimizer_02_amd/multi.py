@@ -8,6 +8,7 @@ gradients' norms and the clip factor that feeds it.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional
 
 from . import binding as B
@@ -49,6 +50,12 @@ def _per_tensor(values, n, name):
     if len(values) != n:
         raise ValueError(f"one {name} per parameter")
     return values
+
+
+def _unchanged(grads, before, ptrs, plan):
+    """Whether the same tensors at the same addresses were given last, and their table written."""
+    return plan.kind != 0 and before is not None and len(grads) == len(before) \
+        and all(map(operator.is_, grads, before)) and [g.data_ptr() for g in grads] == ptrs
 
 
 def _scalar_ptr(t, name, device):
@@ -114,7 +121,7 @@ class AdamWMulti:
                 codes[c.dtype] if c is not None else 0, state_bits, lr_scales[i], wd_scales[i])
         self._plan = B.TensorPlan()
         self._table = None
-        self.grads = None
+        self.grads = self._ptrs = None
         if grads is not None:
             self.set_grads(grads, stream)
 
@@ -150,6 +157,8 @@ class AdamWMulti:
         one differs from before; steps that follow on the stream read them."""
         torch = B._torch()
         grads = list(grads)
+        if _unchanged(grads, self.grads, self._ptrs, self._plan):
+            return
         if len(grads) != self.n:
             raise ValueError("one gradient per parameter")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
@@ -159,7 +168,7 @@ class AdamWMulti:
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.g_dtype == code
             d.g, d.g_dtype = ptr, code
-        self.grads = grads
+        self.grads, self._ptrs = grads, [g.data_ptr() for g in grads]
         if same:
             return
         lib = B.load_library()
@@ -170,7 +179,7 @@ class AdamWMulti:
                 B._check(lib.adamw_multi_plan_bytes(self._arr, self.n, need), "adamw_multi_plan_bytes")
                 self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
             rc = lib.adamw_multi_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
-                                      B._stream_handle(stream, self.device))
+                                      B.raw_stream(stream, self.device))
         B._check(rc, "adamw_multi_plan")
 
     def step(self, step: int, grad_scale=None, stream=None, grads=None):
@@ -182,7 +191,7 @@ class AdamWMulti:
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale,
-                                                   B._stream_handle(stream, self.device))
+                                                   B.raw_stream(stream, self.device))
         B._check(rc, "adamw_multi_step")
 
     def moments(self, i: int):
@@ -229,7 +238,7 @@ class GradNorm:
         self.device = _device_of(grads, "grads")
         self._arr = (B.GradTensor * max(self.n, 1))()
         self._plan = B.TensorPlan()
-        self._table = self._numels = self.grads = None
+        self._table = self._numels = self.grads = self._ptrs = None
         self.set_grads(grads, stream)
         with B.device_and_stream(self.device, stream):
             self.total = torch.empty(2, dtype=torch.float32, device=self.device)
@@ -240,6 +249,8 @@ class GradNorm:
         """New gradient tensors of the same sizes; written to the table where an address differs."""
         torch = B._torch()
         grads = list(grads)
+        if _unchanged(grads, self.grads, self._ptrs, self._plan):
+            return
         if len(grads) != self.n:
             raise ValueError(f"{self.n} gradients are expected")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
@@ -250,7 +261,7 @@ class GradNorm:
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.dtype == code
             d.g, d.numel, d.dtype = ptr, g.numel(), code
-        self.grads = grads
+        self.grads, self._ptrs = grads, [g.data_ptr() for g in grads]
         if same:
             return
         lib = B.load_library()
@@ -261,7 +272,7 @@ class GradNorm:
                 B._check(lib.grad_norm_plan_bytes(self._arr, self.n, need), "grad_norm_plan_bytes")
                 self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
             rc = lib.grad_norm_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
-                                    B._stream_handle(stream, self.device))
+                                    B.raw_stream(stream, self.device))
         B._check(rc, "grad_norm_plan")
 
     def measure(self, max_norm: float, stream=None):
@@ -269,7 +280,7 @@ class GradNorm:
         min(1, max_norm / (norm + 1e-6)), norms[i] the norm of gradient i."""
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_norm(self._plan, max_norm, self.total.data_ptr(), self.norms.data_ptr() or None,
-                                            B._stream_handle(stream, self.device))
+                                            B.raw_stream(stream, self.device))
         B._check(rc, "grad_norm")
         return self.total, self.norms
 
@@ -278,5 +289,5 @@ class GradNorm:
         default the last measure()'s clip factor). Nothing is read or written where it is 1."""
         ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device)
         with B.device_and_stream(self.device, stream):
-            rc = B.load_library().grad_scale(self._plan, ptr, B._stream_handle(stream, self.device))
+            rc = B.load_library().grad_scale(self._plan, ptr, B.raw_stream(stream, self.device))
         B._check(rc, "grad_scale")

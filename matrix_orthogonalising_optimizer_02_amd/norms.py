@@ -18,13 +18,15 @@ _KINDS = {"layer": NORM_LAYER, "rms": NORM_RMS}
 
 def _row_levels(t, name):
     """The leading dimensions of t as at most two (size, stride) levels, innermost first."""
+    shape = t.shape
+    cols = shape[-1]
     if t.is_contiguous():
-        n = t.numel() // t.shape[-1] if t.shape[-1] else 0
-        return [(n, t.shape[-1])] if n > 1 else []
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        n = t.numel() // cols if cols else 0
+        return [(n, cols)] if n > 1 else []
+    if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have adjacent elements in its last dimension")
     levels = []
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if levels and stride == levels[-1][0] * levels[-1][1]:
@@ -38,6 +40,8 @@ def _row_levels(t, name):
 
 def _layout(tensors):
     """(inner, row structs) for [(tensor, name)] of one shape."""
+    if all(t.is_contiguous() for t, _ in tensors):
+        return 1, [B.NormRows(t.data_ptr() or None, t.shape[-1], 0) for t, _ in tensors]
     levels = [_row_levels(t, name) for t, name in tensors]
     inner = 1
     for lv, (_, name) in zip(levels, tensors):
@@ -56,34 +60,50 @@ def _layout(tensors):
     return inner, rows
 
 
-def _check(t, name, device=None, dtype=None, shape=None):
+def _check_x(x):
     torch = B._torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("x must live on a GPU")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    if x.dtype not in B.dtype_codes():
+        raise ValueError("x must be float32, bfloat16 or float16")
+
+
+def _check_like(t, name, x):
+    """t has x's shape, type and device."""
+    if not isinstance(t, B._torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on a GPU")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must live on {device}")
+    if t.dtype != x.dtype:
+        raise ValueError(f"{name} must have dtype {x.dtype}")
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}")
+    if t.device != x.device:
+        raise ValueError(f"{name} must live on {x.device}")
 
 
-def _param(t, name, cols, groups, device, dtypes):
+def _param(t, name, cols, groups, x, dtypes):
     """(groups, struct) of a weight or bias whose last dimension is the row's."""
-    _check(t, name, device)
+    if not isinstance(t, B._torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dict.fromkeys(dtypes))}")
+    if t.device != x.device:
+        raise ValueError(f"{name} must live on {x.device}")
     if t.dim() < 1 or t.shape[-1] != cols:
         raise ValueError(f"{name} must have {cols} elements in its last dimension")
     n = t.numel() // cols if cols else 1
     if groups is not None and n != groups:
         raise ValueError(f"{name} must have {groups} rows, as the weight")
-    levels = _row_levels(t, name)
-    if len(levels) > 1:
-        raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
-    return n, B.NormParam(t.data_ptr() or None, levels[0][1] if levels else cols)
+    stride = cols
+    if not t.is_contiguous():
+        levels = _row_levels(t, name)
+        if len(levels) > 1:
+            raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
+        stride = levels[0][1] if levels else cols
+    return n, B.NormParam(t.data_ptr() or None, stride)
 
 
 def _desc(x, weight, bias, kind, eps, weight_offset, inner):
@@ -92,22 +112,16 @@ def _desc(x, weight, bias, kind, eps, weight_offset, inner):
     if kind not in _KINDS:
         raise ValueError("kind must be 'layer' or 'rms'")
     codes = B.dtype_codes()
-    if x.dtype not in codes:
-        raise ValueError("x must be float32, bfloat16 or float16")
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
     cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
     groups, w, b, wdtype = None, None, None, torch.float32
     if weight is not None:
-        groups, w = _param(weight, "weight", cols, None, x.device, (torch.float32, x.dtype))
         wdtype = weight.dtype
+        groups, w = _param(weight, "weight", cols, None, x, (torch.float32, x.dtype))
     if bias is not None:
-        allowed = (wdtype,) if weight is not None else (torch.float32, x.dtype)
-        groups, b = _param(bias, "bias", cols, groups, x.device, allowed)
+        groups, b = _param(bias, "bias", cols, groups, x, (torch.float32, x.dtype) if weight is None else (wdtype,))
         wdtype = bias.dtype
-    d = B.NormDesc(rows, cols, 1 if groups is None else groups, inner, _KINDS[kind], codes[x.dtype], codes[wdtype],
-                   eps, weight_offset)
+    d = B.NormDesc(x.numel() // cols if cols else 0, cols, 1 if groups is None else groups, inner, _KINDS[kind],
+                   codes[x.dtype], codes[wdtype], eps, weight_offset)
     return d, w, b
 
 
@@ -123,26 +137,32 @@ def norm_forward(x, weight=None, bias=None, *, kind: str = "layer", eps: float =
     receives y, and may be x.
     """
     torch = B._torch()
-    _check(x, "x")
-    with B.device_and_stream(x.device, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        if out is not None:
-            _check(out, "out", x.device, x.dtype, x.shape)
+    _check_x(x)
+    device = x.device
+    with B.device_and_stream(device, stream):
+        if out is None:
+            y = x.new_empty(x.shape)
+        else:
+            _check_like(out, "out", x)
+            y = out
         inner, (rx, ry) = _layout(((x, "x"), (y, "out")))
         d, w, b = _desc(x, weight, bias, kind, eps, weight_offset, inner)
         mean = rstd = None
+        pm = pr = None
         if stats:
-            rstd = torch.empty(d.rows, dtype=torch.float32, device=x.device)
+            rstd = x.new_empty(d.rows, dtype=torch.float32)
+            pr = rstd.data_ptr() or None
             if kind == "layer":
-                mean = torch.empty(d.rows, dtype=torch.float32, device=x.device)
-        rc = B.load_library().norm_forward(d, rx, w, b, ry, mean.data_ptr() or None if mean is not None else None,
-                                           rstd.data_ptr() or None if rstd is not None else None,
-                                           B._stream_handle(stream, x.device))
-    B._check(rc, "norm_forward")
+                mean = x.new_empty(d.rows, dtype=torch.float32)
+                pm = mean.data_ptr() or None
+        rc = B.load_library().norm_forward(d, rx, w, b, ry, pm, pr, B.raw_stream(stream, device))
+    if rc:
+        B._check(rc, "norm_forward")
     return y, mean, rstd
 
 
 def norm_backward_workspace_bytes(desc: "B.NormDesc") -> int:
+    """Bytes of norm_backward's workspace for a call's descriptor."""
     out = ctypes.c_size_t(0)
     B._check(B.load_library().norm_backward_workspace_bytes(desc, out), "norm_backward_workspace_bytes")
     return int(out.value)
@@ -159,42 +179,48 @@ def norm_backward(dy, x, weight, mean, rstd, *, kind: str = "layer", weight_offs
     optional uint8 device buffer of norm_backward_workspace_bytes().
     """
     torch = B._torch()
-    _check(x, "x")
-    _check(dy, "dy", x.device, x.dtype, x.shape)
-    with B.device_and_stream(x.device, stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        if out is not None:
-            _check(out, "out", x.device, x.dtype, x.shape)
+    _check_x(x)
+    _check_like(dy, "dy", x)
+    device = x.device
+    with B.device_and_stream(device, stream):
+        if out is None:
+            dx = x.new_empty(x.shape)
+        else:
+            _check_like(out, "out", x)
+            dx = out
         inner, (rdy, rx, rdx) = _layout(((dy, "dy"), (x, "x"), (dx, "out")))
         dbias = None
         if bias_grad:
-            if weight is None and grad_shape is None:
-                grad_shape = x.shape[-1:]
-            shape = weight.shape if weight is not None else tuple(grad_shape)
-            dtype = weight.dtype if weight is not None else (grad_dtype or torch.float32)
-            dbias = torch.empty(shape, dtype=dtype, device=x.device)
+            if weight is not None:
+                dbias = weight.new_empty(weight.shape)
+            else:
+                dbias = x.new_empty(x.shape[-1:] if grad_shape is None else tuple(grad_shape),
+                                    dtype=grad_dtype or torch.float32)
         d, w, db = _desc(x, weight, dbias, kind, 1.0, weight_offset, inner)
         dweight = dw = None
         if weight_grad and weight is not None:
-            dweight = torch.empty(weight.shape, dtype=weight.dtype, device=x.device)
+            dweight = weight.new_empty(weight.shape)
             dw = B.NormParam(dweight.data_ptr() or None, d.cols)
+        stats = []
         for t, nm in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None:
-                _check(t, nm, x.device, torch.float32)
-                if t.numel() != d.rows or not t.is_contiguous():
-                    raise ValueError(f"{nm} must be a contiguous float32 tensor with one entry per row")
+            if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != d.rows
+                                  or not t.is_contiguous() or t.device != device):
+                raise ValueError(f"{nm} must be a contiguous float32 tensor on {device} with one entry per row")
+            stats.append(t.data_ptr() or None if t is not None else None)
         ws, wsb = None, 0
         if workspace is not None:
+            if workspace.device != device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+                raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
             ws, wsb = workspace.data_ptr(), workspace.numel()
         elif dw is not None or db is not None:
             wsb = norm_backward_workspace_bytes(d)
             if wsb:
-                workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+                workspace = torch.empty(wsb, dtype=torch.uint8, device=device)
                 ws = workspace.data_ptr()
-        rc = B.load_library().norm_backward(d, rdy, rx, w, mean.data_ptr() or None if mean is not None else None,
-                                            rstd.data_ptr() or None if rstd is not None else None, rdx, dw, db, ws, wsb,
-                                            B._stream_handle(stream, x.device))
-    B._check(rc, "norm_backward")
+        rc = B.load_library().norm_backward(d, rdy, rx, w, stats[0], stats[1], rdx, dw, db, ws, wsb,
+                                            B.raw_stream(stream, device))
+    if rc:
+        B._check(rc, "norm_backward")
     return dx, dweight, dbias
 
 

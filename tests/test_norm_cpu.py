@@ -48,7 +48,7 @@ def backward(lib, d=None, dy=rows(0), x=rows(1), w=param(2), mean=ptr(3), rstd=p
 BAD_DESCS = [(dict(rows=-1), -1), (dict(cols=-1), -1), (dict(groups=0), -1), (dict(groups=5), -1), (dict(inner=0), -1),
              (dict(inner=3), -1), (dict(kind=2), -1), (dict(dtype=3), -1), (dict(dtype=-1), -1), (dict(wdtype=2), -1),
              (dict(eps=0.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
-             (dict(weight_offset=float("nan")), -1), (dict(cols=16385), -6), (dict(rows=1 << 31, groups=1), -6)]
+             (dict(weight_offset=float("nan")), -1), (dict(cols=16385), -6), (dict(rows=(1 << 30) + 1, groups=1), -6)]
 
 
 @fake_only
