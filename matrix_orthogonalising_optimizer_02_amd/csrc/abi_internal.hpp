@@ -5,7 +5,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <exception>
 #include <functional>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -29,6 +31,20 @@ int check_overlaps(std::vector<Range>& ranges);
 // Runs `launch`, bracketed by events of kernel class `cls` while timing is enabled;
 // MUON_ERR_HIP (with the error text set) when it fails.
 int run_timed(int cls, hipStream_t stream, const char* name, const std::function<hipError_t()>& launch);
+
+// Runs the body of a C entry point; no C++ exception leaves it (the lists of a call that do
+// not fit the host's memory give MUON_ERR_TOO_LARGE).
+template <class F>
+int guarded(F&& body) {
+    try {
+        set_last_error(MUON_OK, "");
+        return body();
+    } catch (const std::bad_alloc&) {
+        return set_last_error(MUON_ERR_TOO_LARGE, "out of host memory");
+    } catch (const std::exception& e) {
+        return set_last_error(MUON_ERR_INVALID_ARG, e.what());
+    }
+}
 
 // rownorm_update on a scratch buffer of scratch_cap bytes that get_scratch returns for
 // the current device (NULL with *error set on failure). Validates and plans on the host

@@ -127,245 +127,252 @@ GradArgs grad_args(const tensor_plan& p) {
 using namespace muon;
 
 MUON_API int adamw_multi_plan_bytes(const adamw_tensor* tensors, int32_t count, size_t* bytes) {
-    set_last_error(MUON_OK, "");
-    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-    Sizes sz;
-    const int rc = adamw_sizes(tensors, count, &sz);
-    if (rc == MUON_OK) *bytes = sz.bytes;
-    return rc;
+    return guarded([&]() -> int {
+        if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+        Sizes sz;
+        const int rc = adamw_sizes(tensors, count, &sz);
+        if (rc == MUON_OK) *bytes = sz.bytes;
+        return rc;
+    });
 }
 
 MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* device, size_t bytes, tensor_plan* plan,
                               void* stream) {
-    set_last_error(MUON_OK, "");
-    if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
-    Sizes sz;
-    int rc = adamw_sizes(tensors, count, &sz);
-    if (rc) return rc;
-    std::vector<Range> ranges;
-    int bits = -1;  // of all tensors so far; 0 once they differ
-    for (int i = 0; i < count; ++i) {
-        const adamw_tensor& t = tensors[i];
-        if (t.numel == 0) continue;
-        if (t.state_bits != 8 && t.state_bits != 32) return fail(MUON_ERR_INVALID_ARG, "state_bits must be 8 or 32" + at(i));
-        const bool small = t.state_bits == 8;
-        bits = bits < 0 || bits == t.state_bits ? t.state_bits : 0;
-        if (!t.w || !t.g || !t.m || !t.v || (small && (!t.m_scale || !t.v_scale)))
-            return fail(MUON_ERR_INVALID_ARG, "NULL pointer" + at(i));
-        if (t.g_dtype < MUON_DTYPE_F32 || t.g_dtype > MUON_DTYPE_F16) return fail(MUON_ERR_INVALID_ARG, "unknown g_dtype" + at(i));
-        if (t.copy && t.copy_dtype != MUON_DTYPE_BF16 && t.copy_dtype != MUON_DTYPE_F16)
-            return fail(MUON_ERR_INVALID_ARG, "copy_dtype must be a 16-bit type" + at(i));
-        if (!std::isfinite(t.lr_scale) || !std::isfinite(t.wd_scale))
-            return fail(MUON_ERR_INVALID_ARG, "lr_scale and wd_scale must be finite" + at(i));
-        if ((addr(t.w) | addr(t.g) | addr(t.m) | addr(t.v) | addr(t.copy)) & 15)
-            return fail(MUON_ERR_ALIGN, "tensor pointer not 16-byte aligned" + at(i));
-        if (small && ((addr(t.m_scale) | addr(t.v_scale)) & 3))
-            return fail(MUON_ERR_ALIGN, "scales not 4-byte aligned" + at(i));
-        const auto add = [&](const void* p, int64_t n, bool write) {
-            ranges.push_back({addr(p), addr(p) + uintptr_t(n), write});
-        };
-        const int64_t state = t.numel * (small ? 1 : 4), scales = ceil_div(t.numel, kQBlock) * 4;
-        add(t.w, t.numel * 4, true);
-        add(t.m, state, true);
-        add(t.v, state, true);
-        add(t.g, t.numel * elem_size(t.g_dtype), false);
-        if (t.copy) add(t.copy, t.numel * 2, true);
-        if (small) {
-            add(t.m_scale, scales, true);
-            add(t.v_scale, scales, true);
-        }
-    }
-    if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (sz.blocks && (rc = check_not_capturing(s))) return rc;
-    tensor_plan p{};
-    p.device = device;
-    p.bytes = sz.bytes;
-    p.kind = kPlanAdamw;
-    p.count = count;
-    p.blocks = int32_t(sz.blocks);
-    p.reserved = bits;
-    *plan = p;
-    if (sz.blocks == 0) return MUON_OK;
-    MultiDescArgs a{};
-    a.table = static_cast<MultiDesc*>(device);
-    int32_t block = 0;
-    for (int i = 0; i < count; ++i) {
-        const adamw_tensor& t = tensors[i];
-        MultiDesc& d = a.d[a.n++];
-        d = MultiDesc{};
-        d.w = t.w;
-        d.copy = t.copy;
-        d.g = t.g;
-        d.m = t.m;
-        d.v = t.v;
-        d.ms = t.m_scale;
-        d.vs = t.v_scale;
-        d.n = t.numel;
-        d.blk_begin = block;
-        d.index = i;
-        d.lr_scale = t.lr_scale;
-        d.wd_scale = t.wd_scale;
-        d.g_type = int8_t(t.g_dtype);
-        d.copy_type = int8_t(t.copy_dtype);
-        d.bits = int8_t(t.state_bits);
-        block += int32_t(ceil_div(t.numel, kMultiBlockElems));
-        if (a.n == kMultiPerLaunch || i == count - 1) {
-            rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw table", [&] { return launch_multi_table(a, s); });
-            if (rc) {
-                plan->kind = 0;
-                return rc;
+    return guarded([&]() -> int {
+        if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+        Sizes sz;
+        int rc = adamw_sizes(tensors, count, &sz);
+        if (rc) return rc;
+        std::vector<Range> ranges;
+        int bits = -1;  // of all tensors so far; 0 once they differ
+        for (int i = 0; i < count; ++i) {
+            const adamw_tensor& t = tensors[i];
+            if (t.numel == 0) continue;
+            if (t.state_bits != 8 && t.state_bits != 32) return fail(MUON_ERR_INVALID_ARG, "state_bits must be 8 or 32" + at(i));
+            const bool small = t.state_bits == 8;
+            bits = bits < 0 || bits == t.state_bits ? t.state_bits : 0;
+            if (!t.w || !t.g || !t.m || !t.v || (small && (!t.m_scale || !t.v_scale)))
+                return fail(MUON_ERR_INVALID_ARG, "NULL pointer" + at(i));
+            if (t.g_dtype < MUON_DTYPE_F32 || t.g_dtype > MUON_DTYPE_F16) return fail(MUON_ERR_INVALID_ARG, "unknown g_dtype" + at(i));
+            if (t.copy && t.copy_dtype != MUON_DTYPE_BF16 && t.copy_dtype != MUON_DTYPE_F16)
+                return fail(MUON_ERR_INVALID_ARG, "copy_dtype must be a 16-bit type" + at(i));
+            if (!std::isfinite(t.lr_scale) || !std::isfinite(t.wd_scale))
+                return fail(MUON_ERR_INVALID_ARG, "lr_scale and wd_scale must be finite" + at(i));
+            if ((addr(t.w) | addr(t.g) | addr(t.m) | addr(t.v) | addr(t.copy)) & 15)
+                return fail(MUON_ERR_ALIGN, "tensor pointer not 16-byte aligned" + at(i));
+            if (small && ((addr(t.m_scale) | addr(t.v_scale)) & 3))
+                return fail(MUON_ERR_ALIGN, "scales not 4-byte aligned" + at(i));
+            const auto add = [&](const void* p, int64_t n, bool write) {
+                ranges.push_back({addr(p), addr(p) + uintptr_t(n), write});
+            };
+            const int64_t state = t.numel * (small ? 1 : 4), scales = ceil_div(t.numel, kQBlock) * 4;
+            add(t.w, t.numel * 4, true);
+            add(t.m, state, true);
+            add(t.v, state, true);
+            add(t.g, t.numel * elem_size(t.g_dtype), false);
+            if (t.copy) add(t.copy, t.numel * 2, true);
+            if (small) {
+                add(t.m_scale, scales, true);
+                add(t.v_scale, scales, true);
             }
-            a.first += a.n;
-            a.n = 0;
         }
-    }
-    int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
-    rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw map",
-                   [&] { return launch_multi_map(a.table, count, map, int(sz.blocks), s); });
-    if (rc) plan->kind = 0;
-    return rc;
+        if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        if (sz.blocks && (rc = check_not_capturing(s))) return rc;
+        tensor_plan p{};
+        p.device = device;
+        p.bytes = sz.bytes;
+        p.kind = kPlanAdamw;
+        p.count = count;
+        p.blocks = int32_t(sz.blocks);
+        p.reserved = bits;
+        *plan = p;
+        if (sz.blocks == 0) return MUON_OK;
+        MultiDescArgs a{};
+        a.table = static_cast<MultiDesc*>(device);
+        int32_t block = 0;
+        for (int i = 0; i < count; ++i) {
+            const adamw_tensor& t = tensors[i];
+            MultiDesc& d = a.d[a.n++];
+            d = MultiDesc{};
+            d.w = t.w;
+            d.copy = t.copy;
+            d.g = t.g;
+            d.m = t.m;
+            d.v = t.v;
+            d.ms = t.m_scale;
+            d.vs = t.v_scale;
+            d.n = t.numel;
+            d.blk_begin = block;
+            d.index = i;
+            d.lr_scale = t.lr_scale;
+            d.wd_scale = t.wd_scale;
+            d.g_type = int8_t(t.g_dtype);
+            d.copy_type = int8_t(t.copy_dtype);
+            d.bits = int8_t(t.state_bits);
+            block += int32_t(ceil_div(t.numel, kMultiBlockElems));
+            if (a.n == kMultiPerLaunch || i == count - 1) {
+                rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw table", [&] { return launch_multi_table(a, s); });
+                if (rc) {
+                    plan->kind = 0;
+                    return rc;
+                }
+                a.first += a.n;
+                a.n = 0;
+            }
+        }
+        int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
+        rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw map",
+                       [&] { return launch_multi_map(a.table, count, map, int(sz.blocks), s); });
+        if (rc) plan->kind = 0;
+        return rc;
+    });
 }
 
 MUON_API int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t step, uint64_t seed,
                               const float* grad_scale, void* stream) {
-    set_last_error(MUON_OK, "");
-    const int rc = check_plan(plan, kPlanAdamw);
-    if (rc) return rc;
-    if (!hp) return fail(MUON_ERR_INVALID_ARG, "hparams is NULL");
-    if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
-        return fail(MUON_ERR_INVALID_ARG, "lr and weight_decay must be finite");
-    if (!(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f))
-        return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-    if (!(hp->eps >= FLT_MIN) || !std::isfinite(hp->eps))
-        return fail(MUON_ERR_INVALID_ARG, "eps must be a finite, normal number > 0");
-    if (step < 0) return fail(MUON_ERR_INVALID_ARG, "step < 0");
-    if (addr(grad_scale) & 3) return fail(MUON_ERR_ALIGN, "grad_scale not 4-byte aligned");
-    if (plan->blocks == 0) return MUON_OK;
-    // bias corrections in double on the host (t = step + 1)
-    const double t = double(step) + 1.0;
-    const double bc1 = 1.0 - std::pow(double(hp->beta1), t);
-    const double bc2 = 1.0 - std::pow(double(hp->beta2), t);
-    MultiArgs a{};
-    a.table = static_cast<const MultiDesc*>(plan->device);
-    a.tensor_of_block = reinterpret_cast<const int32_t*>(static_cast<const char*>(plan->device) +
-                                                         align256(size_t(plan->count) * sizeof(MultiDesc)));
-    a.blocks = plan->blocks;
-    a.bits = plan->reserved;
-    a.key = mix32(mix32(mix32(uint32_t(seed)) + uint32_t(seed >> 32)) + uint32_t(step));
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.one_minus_beta1 = float(1.0 - double(hp->beta1));
-    a.one_minus_beta2 = float(1.0 - double(hp->beta2));
-    a.eps = hp->eps;
-    a.lr_bc1 = float(double(hp->lr) / bc1);
-    a.inv_sqrt_bc2 = float(1.0 / std::sqrt(bc2));
-    a.lr_wd = double(hp->lr) * double(hp->weight_decay);
-    a.grad_scale = grad_scale;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return run_timed(MUON_KCLASS_ADAMW_MULTI, s, "adamw multi", [&] { return launch_multi_step(a, s); });
+    return guarded([&]() -> int {
+        const int rc = check_plan(plan, kPlanAdamw);
+        if (rc) return rc;
+        if (!hp) return fail(MUON_ERR_INVALID_ARG, "hparams is NULL");
+        if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
+            return fail(MUON_ERR_INVALID_ARG, "lr and weight_decay must be finite");
+        if (!(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f))
+            return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+        if (!(hp->eps >= FLT_MIN) || !std::isfinite(hp->eps))
+            return fail(MUON_ERR_INVALID_ARG, "eps must be a finite, normal number > 0");
+        if (step < 0) return fail(MUON_ERR_INVALID_ARG, "step < 0");
+        if (addr(grad_scale) & 3) return fail(MUON_ERR_ALIGN, "grad_scale not 4-byte aligned");
+        if (plan->blocks == 0) return MUON_OK;
+        // bias corrections in double on the host (t = step + 1)
+        const double t = double(step) + 1.0;
+        const double bc1 = 1.0 - std::pow(double(hp->beta1), t);
+        const double bc2 = 1.0 - std::pow(double(hp->beta2), t);
+        MultiArgs a{};
+        a.table = static_cast<const MultiDesc*>(plan->device);
+        a.tensor_of_block = reinterpret_cast<const int32_t*>(static_cast<const char*>(plan->device) +
+                                                             align256(size_t(plan->count) * sizeof(MultiDesc)));
+        a.blocks = plan->blocks;
+        a.bits = plan->reserved;
+        a.key = mix32(mix32(mix32(uint32_t(seed)) + uint32_t(seed >> 32)) + uint32_t(step));
+        a.beta1 = hp->beta1;
+        a.beta2 = hp->beta2;
+        a.one_minus_beta1 = float(1.0 - double(hp->beta1));
+        a.one_minus_beta2 = float(1.0 - double(hp->beta2));
+        a.eps = hp->eps;
+        a.lr_bc1 = float(double(hp->lr) / bc1);
+        a.inv_sqrt_bc2 = float(1.0 / std::sqrt(bc2));
+        a.lr_wd = double(hp->lr) * double(hp->weight_decay);
+        a.grad_scale = grad_scale;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        return run_timed(MUON_KCLASS_ADAMW_MULTI, s, "adamw multi", [&] { return launch_multi_step(a, s); });
+    });
 }
 
 MUON_API int grad_norm_plan_bytes(const grad_tensor* grads, int32_t count, size_t* bytes) {
-    set_last_error(MUON_OK, "");
-    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-    Sizes sz;
-    const int rc = grad_sizes(grads, count, &sz);
-    if (rc == MUON_OK) *bytes = sz.bytes;
-    return rc;
+    return guarded([&]() -> int {
+        if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+        Sizes sz;
+        const int rc = grad_sizes(grads, count, &sz);
+        if (rc == MUON_OK) *bytes = sz.bytes;
+        return rc;
+    });
 }
 
 MUON_API int grad_norm_plan(const grad_tensor* grads, int32_t count, void* device, size_t bytes, tensor_plan* plan,
                             void* stream) {
-    set_last_error(MUON_OK, "");
-    if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
-    Sizes sz;
-    int rc = grad_sizes(grads, count, &sz);
-    if (rc) return rc;
-    std::vector<Range> ranges;
-    for (int i = 0; i < count; ++i) {
-        const grad_tensor& t = grads[i];
-        if (t.numel == 0) continue;
-        if (!t.g) return fail(MUON_ERR_INVALID_ARG, "NULL pointer" + at(i));
-        if (t.dtype < MUON_DTYPE_F32 || t.dtype > MUON_DTYPE_F16) return fail(MUON_ERR_INVALID_ARG, "unknown dtype" + at(i));
-        const int e = elem_size(t.dtype);
-        if (addr(t.g) % e) return fail(MUON_ERR_ALIGN, "gradient not aligned to its element" + at(i));
-        ranges.push_back({addr(t.g), addr(t.g) + uintptr_t(t.numel) * e, true});
-    }
-    if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (count && (rc = check_not_capturing(s))) return rc;
-    tensor_plan p{};
-    p.device = device;
-    p.bytes = sz.bytes;
-    p.kind = kPlanGrads;
-    p.count = count;
-    p.blocks = int32_t(sz.blocks);
-    p.reserved = int32_t(sz.block_elems / kGradBlockElems);
-    *plan = p;
-    if (count == 0) return MUON_OK;
-    GradDescArgs a{};
-    a.table = static_cast<GradDesc*>(device);
-    int32_t block = 0;
-    for (int i = 0; i < count; ++i) {
-        GradDesc& d = a.d[a.n++];
-        d = GradDesc{};
-        d.g = grads[i].g;
-        d.n = grads[i].numel;
-        d.type = grads[i].dtype;
-        d.blk_begin = block;
-        block += int32_t(ceil_div(grads[i].numel, sz.block_elems));
-        d.blk_end = block;
-        if (a.n == kGradPerLaunch || i == count - 1) {
-            rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient table", [&] { return launch_grad_table(a, s); });
-            if (rc) {
-                plan->kind = 0;
-                return rc;
-            }
-            a.first += a.n;
-            a.n = 0;
+    return guarded([&]() -> int {
+        if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+        Sizes sz;
+        int rc = grad_sizes(grads, count, &sz);
+        if (rc) return rc;
+        std::vector<Range> ranges;
+        for (int i = 0; i < count; ++i) {
+            const grad_tensor& t = grads[i];
+            if (t.numel == 0) continue;
+            if (!t.g) return fail(MUON_ERR_INVALID_ARG, "NULL pointer" + at(i));
+            if (t.dtype < MUON_DTYPE_F32 || t.dtype > MUON_DTYPE_F16) return fail(MUON_ERR_INVALID_ARG, "unknown dtype" + at(i));
+            const int e = elem_size(t.dtype);
+            if (addr(t.g) % e) return fail(MUON_ERR_ALIGN, "gradient not aligned to its element" + at(i));
+            ranges.push_back({addr(t.g), addr(t.g) + uintptr_t(t.numel) * e, true});
         }
-    }
-    if (sz.blocks == 0) return MUON_OK;
-    int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
-    rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient map",
-                   [&] { return launch_grad_map(a.table, count, map, int(sz.blocks), s); });
-    if (rc) plan->kind = 0;
-    return rc;
+        if ((rc = check_buffer(device, bytes, sz.bytes, ranges)) || (rc = check_overlaps(ranges))) return rc;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        if (count && (rc = check_not_capturing(s))) return rc;
+        tensor_plan p{};
+        p.device = device;
+        p.bytes = sz.bytes;
+        p.kind = kPlanGrads;
+        p.count = count;
+        p.blocks = int32_t(sz.blocks);
+        p.reserved = int32_t(sz.block_elems / kGradBlockElems);
+        *plan = p;
+        if (count == 0) return MUON_OK;
+        GradDescArgs a{};
+        a.table = static_cast<GradDesc*>(device);
+        int32_t block = 0;
+        for (int i = 0; i < count; ++i) {
+            GradDesc& d = a.d[a.n++];
+            d = GradDesc{};
+            d.g = grads[i].g;
+            d.n = grads[i].numel;
+            d.type = grads[i].dtype;
+            d.blk_begin = block;
+            block += int32_t(ceil_div(grads[i].numel, sz.block_elems));
+            d.blk_end = block;
+            if (a.n == kGradPerLaunch || i == count - 1) {
+                rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient table", [&] { return launch_grad_table(a, s); });
+                if (rc) {
+                    plan->kind = 0;
+                    return rc;
+                }
+                a.first += a.n;
+                a.n = 0;
+            }
+        }
+        if (sz.blocks == 0) return MUON_OK;
+        int32_t* map = reinterpret_cast<int32_t*>(static_cast<char*>(device) + sz.map);
+        rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "gradient map",
+                       [&] { return launch_grad_map(a.table, count, map, int(sz.blocks), s); });
+        if (rc) plan->kind = 0;
+        return rc;
+    });
 }
 
 MUON_API int grad_norm(const tensor_plan* plan, float max_norm, float* total, float* norms, void* stream) {
-    set_last_error(MUON_OK, "");
-    int rc = check_plan(plan, kPlanGrads);
-    if (rc) return rc;
-    if (!total) return fail(MUON_ERR_INVALID_ARG, "total is NULL");
-    if (!(max_norm > 0.f) || !std::isfinite(max_norm)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be finite and > 0");
-    if ((addr(total) | addr(norms)) & 3) return fail(MUON_ERR_ALIGN, "total or norms not 4-byte aligned");
-    std::vector<Range> ranges{{addr(total), addr(total) + 8, true},
-                              {addr(plan->device), addr(plan->device) + plan->bytes, true}};
-    if (norms) ranges.push_back({addr(norms), addr(norms) + uintptr_t(plan->count) * 4, true});
-    if ((rc = check_overlaps(ranges))) return rc;
-    GradArgs a = grad_args(*plan);
-    a.max_norm = max_norm;
-    a.total = total;
-    a.norms = norms;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (a.blocks) {
-        rc = run_timed(MUON_KCLASS_GRAD_NORM, s, "gradient norm", [&] { return launch_grad_norm(a, s); });
+    return guarded([&]() -> int {
+        int rc = check_plan(plan, kPlanGrads);
         if (rc) return rc;
-    }
-    return run_timed(MUON_KCLASS_GRAD_TOTAL, s, "gradient total", [&] { return launch_grad_total(a, s); });
+        if (!total) return fail(MUON_ERR_INVALID_ARG, "total is NULL");
+        if (!(max_norm > 0.f) || !std::isfinite(max_norm)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be finite and > 0");
+        if ((addr(total) | addr(norms)) & 3) return fail(MUON_ERR_ALIGN, "total or norms not 4-byte aligned");
+        std::vector<Range> ranges{{addr(total), addr(total) + 8, true},
+                                  {addr(plan->device), addr(plan->device) + plan->bytes, true}};
+        if (norms) ranges.push_back({addr(norms), addr(norms) + uintptr_t(plan->count) * 4, true});
+        if ((rc = check_overlaps(ranges))) return rc;
+        GradArgs a = grad_args(*plan);
+        a.max_norm = max_norm;
+        a.total = total;
+        a.norms = norms;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        if (a.blocks) {
+            rc = run_timed(MUON_KCLASS_GRAD_NORM, s, "gradient norm", [&] { return launch_grad_norm(a, s); });
+            if (rc) return rc;
+        }
+        return run_timed(MUON_KCLASS_GRAD_TOTAL, s, "gradient total", [&] { return launch_grad_total(a, s); });
+    });
 }
 
 MUON_API int grad_scale(const tensor_plan* plan, const float* factor, void* stream) {
-    set_last_error(MUON_OK, "");
-    const int rc = check_plan(plan, kPlanGrads);
-    if (rc) return rc;
-    if (!factor) return fail(MUON_ERR_INVALID_ARG, "factor is NULL");
-    if (addr(factor) & 3) return fail(MUON_ERR_ALIGN, "factor not 4-byte aligned");
-    GradArgs a = grad_args(*plan);
-    a.factor = factor;
-    if (a.blocks == 0) return MUON_OK;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return run_timed(MUON_KCLASS_GRAD_SCALE, s, "gradient scale", [&] { return launch_grad_scale(a, s); });
+    return guarded([&]() -> int {
+        const int rc = check_plan(plan, kPlanGrads);
+        if (rc) return rc;
+        if (!factor) return fail(MUON_ERR_INVALID_ARG, "factor is NULL");
+        if (addr(factor) & 3) return fail(MUON_ERR_ALIGN, "factor not 4-byte aligned");
+        GradArgs a = grad_args(*plan);
+        a.factor = factor;
+        if (a.blocks == 0) return MUON_OK;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        return run_timed(MUON_KCLASS_GRAD_SCALE, s, "gradient scale", [&] { return launch_grad_scale(a, s); });
+    });
 }

@@ -132,113 +132,116 @@ using namespace muon;
 
 MUON_API int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_param* w, const norm_param* b,
                           const norm_rows* y, float* mean, float* rstd, void* stream) {
-    set_last_error(MUON_OK, "");
-    int rc = check_desc(desc);
-    if (rc) return rc;
-    const norm_desc& d = *desc;
-    if (d.kind == MUON_NORM_RMS) mean = nullptr;
-    std::vector<Range> ranges;
-    Range rx, ry;
-    if ((rc = check_rows(d, x, "x", false, &rx)) || (rc = check_rows(d, y, "y", true, &ry))) return rc;
-    if (!same_rows(d, *x, *y)) ranges.push_back(rx);
-    ranges.push_back(ry);
-    if ((rc = check_param(d, w, "w", false, ranges)) || (rc = check_param(d, b, "b", false, ranges)) ||
-        (rc = check_stats(d, mean, "mean", true, ranges)) || (rc = check_stats(d, rstd, "rstd", true, ranges)))
-        return rc;
-    if ((rc = check_overlaps(ranges))) return rc;
-    if (d.rows == 0 || d.cols == 0) return MUON_OK;
-    const NormPlan p = plan_norm_forward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-    if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
-    NormArgs a = base_args(d, p);
-    a.x = rows_ptr(*x);
-    a.y = rows_ptr(*y);
-    if (present(w)) {
-        a.w = w->data;
-        a.w_stride = w->stride;
-    }
-    if (present(b)) {
-        a.b = b->data;
-        a.b_stride = b->stride;
-    }
-    a.mean = mean;
-    a.rstd = rstd;
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    return run_timed(MUON_KCLASS_NORM_FORWARD, s, "norm forward",
-                     [&] { return launch_norm_forward(d.kind == MUON_NORM_RMS, d.dtype, p, a, s); });
+    return guarded([&]() -> int {
+        int rc = check_desc(desc);
+        if (rc) return rc;
+        const norm_desc& d = *desc;
+        if (d.kind == MUON_NORM_RMS) mean = nullptr;
+        std::vector<Range> ranges;
+        Range rx, ry;
+        if ((rc = check_rows(d, x, "x", false, &rx)) || (rc = check_rows(d, y, "y", true, &ry))) return rc;
+        if (!same_rows(d, *x, *y)) ranges.push_back(rx);
+        ranges.push_back(ry);
+        if ((rc = check_param(d, w, "w", false, ranges)) || (rc = check_param(d, b, "b", false, ranges)) ||
+            (rc = check_stats(d, mean, "mean", true, ranges)) || (rc = check_stats(d, rstd, "rstd", true, ranges)))
+            return rc;
+        if ((rc = check_overlaps(ranges))) return rc;
+        if (d.rows == 0 || d.cols == 0) return MUON_OK;
+        const NormPlan p = plan_norm_forward(d.dtype, d.cols, d.rows / d.groups, d.groups);
+        if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+        NormArgs a = base_args(d, p);
+        a.x = rows_ptr(*x);
+        a.y = rows_ptr(*y);
+        if (present(w)) {
+            a.w = w->data;
+            a.w_stride = w->stride;
+        }
+        if (present(b)) {
+            a.b = b->data;
+            a.b_stride = b->stride;
+        }
+        a.mean = mean;
+        a.rstd = rstd;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        return run_timed(MUON_KCLASS_NORM_FORWARD, s, "norm forward",
+                         [&] { return launch_norm_forward(d.kind == MUON_NORM_RMS, d.dtype, p, a, s); });
+    });
 }
 
 MUON_API int norm_backward_workspace_bytes(const norm_desc* desc, size_t* bytes) {
-    set_last_error(MUON_OK, "");
-    if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
-    const int rc = check_desc(desc);
-    if (rc) return rc;
-    *bytes = desc->cols == 0 ? 0
-                             : partial_bytes(*desc, plan_norm_backward(desc->dtype, desc->cols,
-                                                                       desc->rows / desc->groups, desc->groups));
-    return MUON_OK;
+    return guarded([&]() -> int {
+        if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+        const int rc = check_desc(desc);
+        if (rc) return rc;
+        *bytes = desc->cols == 0 ? 0
+                                 : partial_bytes(*desc, plan_norm_backward(desc->dtype, desc->cols,
+                                                                           desc->rows / desc->groups, desc->groups));
+        return MUON_OK;
+    });
 }
 
 MUON_API int norm_backward(const norm_desc* desc, const norm_rows* dy, const norm_rows* x, const norm_param* w,
                            const float* mean, const float* rstd, const norm_rows* dx, const norm_param* dw,
                            const norm_param* db, void* workspace, size_t workspace_bytes, void* stream) {
-    set_last_error(MUON_OK, "");
-    int rc = check_desc(desc);
-    if (rc) return rc;
-    const norm_desc& d = *desc;
-    const bool layer = d.kind == MUON_NORM_LAYER;
-    if (!layer) mean = nullptr;
-    const bool has_rows = d.rows > 0 && d.cols > 0;
-    if (has_rows && (!rstd || (layer && !mean))) return fail(MUON_ERR_INVALID_ARG, "mean or rstd is NULL");
-    if (present(dw) && !present(w)) return fail(MUON_ERR_INVALID_ARG, "dw without w");
-    std::vector<Range> ranges;
-    Range rdy, rx, rdx;
-    if ((rc = check_rows(d, dy, "dy", false, &rdy)) || (rc = check_rows(d, x, "x", false, &rx)) ||
-        (rc = check_rows(d, dx, "dx", true, &rdx)))
-        return rc;
-    if (!same_rows(d, *dy, *dx)) ranges.push_back(rdy);
-    if (!same_rows(d, *x, *dx)) ranges.push_back(rx);
-    ranges.push_back(rdx);
-    if ((rc = check_param(d, w, "w", false, ranges)) || (rc = check_param(d, dw, "dw", true, ranges)) ||
-        (rc = check_param(d, db, "db", true, ranges)) || (rc = check_stats(d, mean, "mean", false, ranges)) ||
-        (rc = check_stats(d, rstd, "rstd", false, ranges)))
-        return rc;
-    if (d.cols == 0) return MUON_OK;
-    const NormPlan p = plan_norm_backward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-    if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
-    const bool grads = present(dw) || present(db);
-    const size_t need = grads ? partial_bytes(d, p) : 0;
-    if (need) {
-        if (!workspace) return fail(MUON_ERR_WORKSPACE, "workspace is NULL");
-        if (workspace_bytes < need)
-            return fail(MUON_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(workspace);
-        if (lo & 255) return fail(MUON_ERR_ALIGN, "workspace not 256-byte aligned");
-        ranges.push_back({lo, lo + need, true});
-    }
-    if ((rc = check_overlaps(ranges))) return rc;
-    if (!has_rows && !grads) return MUON_OK;
-    NormArgs a = base_args(d, p);
-    a.x = rows_ptr(*x);
-    a.dy = rows_ptr(*dy);
-    a.y = rows_ptr(*dx);
-    if (present(w)) {
-        a.w = w->data;
-        a.w_stride = w->stride;
-    }
-    a.mean = const_cast<float*>(mean);
-    a.rstd = const_cast<float*>(rstd);
-    if (present(dw)) {
-        a.dw = dw->data;
-        a.dw_stride = dw->stride;
-    }
-    if (present(db)) {
-        a.db = db->data;
-        a.db_stride = db->stride;
-    }
-    a.partial = static_cast<float*>(workspace);
-    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    rc = run_timed(MUON_KCLASS_NORM_BACKWARD, s, "norm backward",
-                   [&] { return launch_norm_backward(!layer, d.dtype, p, a, s); });
-    if (rc || need == 0) return rc;
-    return run_timed(MUON_KCLASS_NORM_WGRAD, s, "norm weight gradient", [&] { return launch_norm_wgrad(a, s); });
+    return guarded([&]() -> int {
+        int rc = check_desc(desc);
+        if (rc) return rc;
+        const norm_desc& d = *desc;
+        const bool layer = d.kind == MUON_NORM_LAYER;
+        if (!layer) mean = nullptr;
+        const bool has_rows = d.rows > 0 && d.cols > 0;
+        if (has_rows && (!rstd || (layer && !mean))) return fail(MUON_ERR_INVALID_ARG, "mean or rstd is NULL");
+        if (present(dw) && !present(w)) return fail(MUON_ERR_INVALID_ARG, "dw without w");
+        std::vector<Range> ranges;
+        Range rdy, rx, rdx;
+        if ((rc = check_rows(d, dy, "dy", false, &rdy)) || (rc = check_rows(d, x, "x", false, &rx)) ||
+            (rc = check_rows(d, dx, "dx", true, &rdx)))
+            return rc;
+        if (!same_rows(d, *dy, *dx)) ranges.push_back(rdy);
+        if (!same_rows(d, *x, *dx)) ranges.push_back(rx);
+        ranges.push_back(rdx);
+        if ((rc = check_param(d, w, "w", false, ranges)) || (rc = check_param(d, dw, "dw", true, ranges)) ||
+            (rc = check_param(d, db, "db", true, ranges)) || (rc = check_stats(d, mean, "mean", false, ranges)) ||
+            (rc = check_stats(d, rstd, "rstd", false, ranges)))
+            return rc;
+        if (d.cols == 0) return MUON_OK;
+        const NormPlan p = plan_norm_backward(d.dtype, d.cols, d.rows / d.groups, d.groups);
+        if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+        const bool grads = present(dw) || present(db);
+        const size_t need = grads ? partial_bytes(d, p) : 0;
+        if (need) {
+            if (!workspace) return fail(MUON_ERR_WORKSPACE, "workspace is NULL");
+            if (workspace_bytes < need)
+                return fail(MUON_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(workspace);
+            if (lo & 255) return fail(MUON_ERR_ALIGN, "workspace not 256-byte aligned");
+            ranges.push_back({lo, lo + need, true});
+        }
+        if ((rc = check_overlaps(ranges))) return rc;
+        if (!has_rows && !grads) return MUON_OK;
+        NormArgs a = base_args(d, p);
+        a.x = rows_ptr(*x);
+        a.dy = rows_ptr(*dy);
+        a.y = rows_ptr(*dx);
+        if (present(w)) {
+            a.w = w->data;
+            a.w_stride = w->stride;
+        }
+        a.mean = const_cast<float*>(mean);
+        a.rstd = const_cast<float*>(rstd);
+        if (present(dw)) {
+            a.dw = dw->data;
+            a.dw_stride = dw->stride;
+        }
+        if (present(db)) {
+            a.db = db->data;
+            a.db_stride = db->stride;
+        }
+        a.partial = static_cast<float*>(workspace);
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        rc = run_timed(MUON_KCLASS_NORM_BACKWARD, s, "norm backward",
+                       [&] { return launch_norm_backward(!layer, d.dtype, p, a, s); });
+        if (rc || need == 0) return rc;
+        return run_timed(MUON_KCLASS_NORM_WGRAD, s, "norm weight gradient", [&] { return launch_norm_wgrad(a, s); });
+    });
 }

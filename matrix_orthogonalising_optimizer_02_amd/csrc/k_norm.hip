@@ -16,9 +16,9 @@
 // squares of the differences), all sums in fp32 in a fixed order. Outputs are stored with
 // the non-temporal hint ([8192, 5120] bf16 forward 31 us; 40 us without), inputs are read
 // without it (a preceding kernel may have left them in the cache).
-// Measured: [8192, 5120] bf16 in 8 groups, forward 29.4 us (5.7 TB/s), backward 52.9 us
-// (4.8 TB/s with the weights' gradients, 5.4 TB/s without); [65536, 5120] backward 400 us
-// (5.0 TB/s); a copy reaches 6.25 TB/s.
+// Measured: [8192, 5120] bf16 in 8 groups, forward 28.9 us (5.8 TB/s), backward 53.3 us
+// (4.7 TB/s with the weights' gradients, 5.6 TB/s without); [65536, 5120] backward 380 us
+// (5.3 TB/s); a copy reaches 6.25 TB/s.
 #include "lanes.hpp"
 #include "train.hpp"
 
@@ -182,14 +182,34 @@ __device__ __forceinline__ void row_sums(float (&v)[kCount], float (*red)[kCount
             for (int i = 0; i < kCount; ++i) red[threadIdx.x >> 6][i] = v[i];
         }
         __syncthreads();
-        const int first = t.team * team_waves;
+        // at most 16 waves: a lane of each 16 reads a wave's sums, and they add up by exchange
+        const int slot = threadIdx.x & 15;
+        const bool one = slot < team_waves;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) v[i] = red[first][i];
-        for (int w = 1; w < team_waves; ++w)
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) v[i] += red[first + w][i];
+        for (int i = 0; i < kCount; ++i) {
+            const float r = red[one ? t.team * team_waves + slot : 0][i];
+            v[i] = lanes_sum<16>(one ? r : 0.f);
+        }
     }
 }
+
+// The rows of a block: every group's rows in turn, t.teams at a time. The groups start at
+// different places, so that blocks of different groups do not walk through memory in step:
+// groups of 1024 rows of 10 KiB are a multiple of 1 MiB apart, and meet in the same channels
+// ([65536, 5120] bf16 in 64 groups, backward 380 us; 392 us from the same row on).
+struct Turn {
+    int begin, step, count, phase;
+    __device__ __forceinline__ Turn(const NormArgs& a, int group, int chunk, int teams) {
+        begin = chunk * teams;
+        step = a.chunks * teams;
+        count = begin < a.rows_per_group ? (a.rows_per_group - begin + step - 1) / step : 0;
+        phase = (int)((int64_t)group * count / a.groups);
+    }
+    __device__ __forceinline__ int row(int i) const {
+        const int j = i + phase;
+        return begin + (j < count ? j : j - count) * step;
+    }
+};
 
 constexpr int kSubThreads = 512;  // most threads of a block whose rows share a wave
 
@@ -202,18 +222,21 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_forward(No
     const Team<kLanes> t(a);
     const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
     const unsigned row0 = (unsigned)group * a.rows_per_group;
-    const int begin = chunk * t.teams, end = a.rows_per_group, step = a.chunks * t.teams;
-    // every lane of a wave takes part in every sum: a team past the end repeats the last
-    // row and writes nothing
+    const Turn turn(a, group, chunk, t.teams);
+    const int end = a.rows_per_group;
+    // Every lane of a wave takes part in every sum: a team past the end has zeros and writes
+    // nothing. It reads nothing either, as other rows may be written over by then (y is x).
     u32x4 next[kN];
     auto fetch = [&](int at) {
-        const unsigned r = row0 + min(at + t.team, end - 1);
-        const elem* p = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, r);
+        const bool mine = at + t.team < end;
+        const elem* p = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, row0 + (mine ? at + t.team : at));
 #pragma unroll
-        for (int k = 0; k < kN; ++k)
-            next[k] = load16(p + Span<kVec>(a.cols, k * t.lanes + t.lane).col);
+        for (int k = 0; k < kN; ++k) {
+            next[k] = u32x4{0u, 0u, 0u, 0u};
+            if (mine) next[k] = load16(p + Span<kVec>(a.cols, k * t.lanes + t.lane).col);
+        }
     };
-    fetch(begin);
+    if (turn.count) fetch(turn.row(0));
     float w[kN][kVec], b[kN][kVec];
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
@@ -231,13 +254,14 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_forward(No
         if (a.b) load_params<kVec>(a.b, (int64_t)group * a.b_stride + sp.col, a.wdtype, b[k]);
     }
     int flip = 0;
-    for (int at = begin; at < end; at += step) {
-        const unsigned r = row0 + min(at + t.team, end - 1);
+    for (int i = 0; i < turn.count; ++i) {
+        const int at = turn.row(i);
         const bool mine = at + t.team < end;
+        const unsigned r = row0 + at + t.team;
         float x[kN][kVec];
 #pragma unroll
         for (int k = 0; k < kN; ++k) E::unpack(next[k], x[k]);
-        if (at + step < end) fetch(at + step);
+        if (i + 1 < turn.count) fetch(turn.row(i + 1));
         float mean = 0.f;
         if constexpr (!kRms) {
             float s = 0.f;
@@ -285,7 +309,8 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_forward(No
     }
 }
 
-template <int T, bool kRms, int kLanes, int kN, bool kExact>
+// kStream: x and dy are read with the non-temporal hint.
+template <int T, bool kRms, int kLanes, int kN, bool kExact, bool kStream>
 __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(NormArgs a) {
     typedef Elem<T> E;
     typedef typename E::type elem;
@@ -294,7 +319,8 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
     const Team<kLanes> t(a);
     const int group = blockIdx.x / a.chunks, chunk = blockIdx.x - group * a.chunks;
     const unsigned row0 = (unsigned)group * a.rows_per_group;
-    const int begin = chunk * t.teams, end = a.rows_per_group, step = a.chunks * t.teams;
+    const Turn turn(a, group, chunk, t.teams);
+    const int end = a.rows_per_group;
     // Rows asked for in advance: two where a lane holds 8 elements. 16 elements leave no
     // registers for that ([1024, 16384] fp32: 53 us without, 76 us with one row and spills).
     constexpr int kAhead = kN * kVec <= 8 ? 2 : 0;
@@ -303,22 +329,29 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
         float mean, rstd;
     };
     Row ahead[kAhead ? kAhead : 1];
+    // as in the forward pass, a team past the end has zeros
     auto fetch = [&](Row& row, int at) {
-        const unsigned r = row0 + min(at + t.team, end - 1);
+        const bool mine = at + t.team < end;
+        const unsigned r = row0 + (mine ? at + t.team : at);
         const elem* px = reinterpret_cast<const elem*>(a.x.data) + row_offset(a, a.x, r);
         const elem* pg = reinterpret_cast<const elem*>(a.dy.data) + row_offset(a, a.dy, r);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-            const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
-            row.x[k] = load16(px + sp.col);
-            row.g[k] = load16(pg + sp.col);
+        for (int k = 0; k < kN; ++k) row.x[k] = row.g[k] = u32x4{0u, 0u, 0u, 0u};
+        row.mean = row.rstd = 0.f;
+        if (mine) {
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
+                row.x[k] = kStream ? stream16(px + sp.col) : load16(px + sp.col);
+                row.g[k] = kStream ? stream16(pg + sp.col) : load16(pg + sp.col);
+            }
+            if constexpr (!kRms) row.mean = a.mean[r];
+            row.rstd = a.rstd[r];
         }
-        row.mean = kRms ? 0.f : a.mean[r];
-        row.rstd = a.rstd[r];
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (begin + i * step < end) fetch(ahead[i], begin + i * step);
+        if (i < turn.count) fetch(ahead[i], turn.row(i));
     float w[kN][kVec], dw[kN][kVec], db[kN][kVec];
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
@@ -335,7 +368,8 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
         }
     }
     int flip = 0;
-    auto process = [&](Row& row, int at) {
+    auto process = [&](Row& row, int i) {
+        const int at = turn.row(i);
         const bool mine = at + t.team < end;  // a team past the end adds and writes nothing
         if constexpr (kAhead == 0) fetch(row, at);
         const float mean = row.mean, rstd = row.rstd;
@@ -345,7 +379,7 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
             E::unpack(row.x[k], h[k]);
             E::unpack(row.g[k], g[k]);
         }
-        if (kAhead && at + kAhead * step < end) fetch(row, at + kAhead * step);
+        if (kAhead && i + kAhead < turn.count) fetch(row, turn.row(i + kAhead));
         float sums[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
@@ -353,12 +387,11 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const float hv = kRms ? h[k][e] * rstd : (h[k][e] - mean) * rstd;
-                // the weights' sums take an element that does not count too: its lane does
-                // not write them
-                const float gv = mine ? g[k][e] : 0.f;
-                dw[k][e] = fmaf(gv, hv, dw[k][e]);
-                db[k][e] += gv;
-                const float av = gv * w[k][e];
+                // the weights' sums take an element that does not count too: its lane
+                // does not write them
+                dw[k][e] = fmaf(g[k][e], hv, dw[k][e]);
+                db[k][e] += g[k][e];
+                const float av = g[k][e] * w[k][e];
                 const float ac = k < kN - 1 ? av : counted<kExact>(sp, e, av);
                 sums[0] += ac;
                 sums[1] = fmaf(ac, hv, sums[1]);
@@ -369,24 +402,24 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_backward(N
         row_sums<kLanes, 2>(sums, red[flip], t, a.team_waves);
         flip ^= 1;
         if (mine) {
-            const float c1 = kRms ? 0.f : sums[0] * a.inv_cols, c2 = sums[1] * a.inv_cols;
+            // rstd (a - c1 - h c2) as two fused steps
+            const float c1 = kRms ? 0.f : sums[0] * a.inv_cols * rstd, c2 = sums[1] * a.inv_cols * rstd;
             elem* q = reinterpret_cast<elem*>(a.y.data) + row_offset(a, a.y, row0 + at + t.team);
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
                 const Span<kVec> sp(a.cols, k * t.lanes + t.lane);
                 float d[kVec];
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) d[e] = rstd * fmaf(-h[k][e], c2, g[k][e] - c1);
+                for (int e = 0; e < kVec; ++e) d[e] = fmaf(g[k][e], rstd, -fmaf(h[k][e], c2, c1));
                 if (kExact || k < kN - 1 || sp.skip < kVec) put_stream16(q + sp.col, E::pack(d));
             }
         }
     };
-    for (int at = begin; at < end;) {
+    for (int i = 0; i < turn.count;) {
 #pragma unroll
-        for (int i = 0; i < (kAhead ? kAhead : 1); ++i) {
-            process(ahead[i], at);
-            at += step;
-            if (at >= end) break;
+        for (int k = 0; k < (kAhead ? kAhead : 1); ++k) {
+            process(ahead[k], i);
+            if (++i >= turn.count) break;
         }
     }
     if (!a.dw && !a.db) return;
@@ -587,7 +620,8 @@ hipError_t launch(const NormPlan& p, const NormArgs& a, hipStream_t s) {
         // a team's sums for all columns, or the block's: at most 16 KiB and 8 KiB
         const bool shared = (a.dw || a.db) && p.teams > 1;
         const size_t lds = shared ? size_t(4) * (kLanes ? p.threads * Elem<T>::kVec : a.cols) : 0;
-        hipLaunchKernelGGL((k_norm_backward<T, kRms, kLanes, kN, kExact>), grid, block, lds, s, a);
+        if (p.stream) hipLaunchKernelGGL((k_norm_backward<T, kRms, kLanes, kN, kExact, true>), grid, block, lds, s, a);
+        else hipLaunchKernelGGL((k_norm_backward<T, kRms, kLanes, kN, kExact, false>), grid, block, lds, s, a);
     }
     return hipGetLastError();
 }
@@ -637,6 +671,10 @@ hipError_t launch_type(bool rms, int dtype, const NormPlan& p, const NormArgs& a
 constexpr int kForwardVectors = 256, kForwardBlockWaves = 4, kForwardWaves = 24;
 constexpr int kBackwardVectors = 1024, kBackwardVectors32 = 128, kBackwardBlockWaves = 8, kBackwardWaves = 10;
 constexpr int kComputeUnits = 256;
+// x and dy of this many bytes are read with the non-temporal hint in the backward pass: they
+// leave the 256 MB memory-side cache before they could be of use ([8192, 4096] fp32, 268 MB,
+// 71.6 us; 76.0 without the hint. [131072, 128] bf16, 67 MB, 23.1 us; 21.6 without).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 // one_vec: rows of up to this many vectors are spread over enough waves that a lane holds one.
 NormPlan plan_shape(int dtype, int64_t cols, int64_t one_vec, int block_waves) {
@@ -689,6 +727,7 @@ NormPlan plan_norm_forward(int dtype, int64_t cols, int64_t rows_per_group, int6
 NormPlan plan_norm_backward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups) {
     NormPlan p = plan_shape(dtype, cols, dtype == kF32 ? kBackwardVectors32 : kBackwardVectors, kBackwardBlockWaves);
     plan_chunks(p, rows_per_group, groups, kBackwardWaves, 4);
+    p.stream = 2 * rows_per_group * groups * cols * elem_size(dtype) >= kStreamBytes;
     return p;
 }
 

@@ -40,7 +40,7 @@ struct NormArgs {
     uint32_t inner_mul;        // r / inner = (mulhi(r, inner_mul) + r) >> inner_shift, 33-bit sum, for inner > 1
     int32_t inner_shift;
     int32_t chunks;            // blocks of a group
-    int32_t chunk_rows;        // rows of a block (rows shorter than a vector)
+    int32_t chunk_rows;        // rows of a block, for rows shorter than a vector
     int32_t team_waves;        // waves that share a row (rows of whole waves)
     int32_t teams;             // rows that a block takes at a time
     int32_t wdtype;
@@ -59,7 +59,8 @@ struct NormPlan {
     int teams;         // rows that a block takes at a time
     int threads;       // of a block
     int chunks;        // blocks of a group
-    int chunk_rows;    // rows of a block
+    int chunk_rows;    // rows of a block (lanes == 1)
+    bool stream;       // backward: inputs too large for the caches
 };
 NormPlan plan_norm_forward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);
 NormPlan plan_norm_backward(int dtype, int64_t cols, int64_t rows_per_group, int64_t groups);

@@ -169,6 +169,8 @@ class HybridOptimizer:
     def _clip(self, grads, stream):
         """Measures all gradients, scales Muon's; the factor for AdamW's (device tensor)."""
         g, gm = [grads[n] for n in self.names], [grads[n] for n in self.muon_names]
+        for n, t in zip(self.muon_names, gm):  # what muon_step refuses is not scaled first
+            B._check_tensor(t, f"gradient of {n}")
         if self._norm is None:
             self._norm = GradNorm(g, stream)
             self._muon_norm = GradNorm(gm, stream) if gm else None

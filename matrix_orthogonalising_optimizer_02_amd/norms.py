@@ -264,7 +264,8 @@ def _autograd_function():
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """norm_forward's y for torch.autograd: affine with weight and bias of [cols], adaLN
-    with one row a sample and weight_offset 1, plain without either."""
+    with one row a sample and weight_offset 1, plain without either. To capture a backward
+    pass into a HIP graph, call norm_forward and norm_backward themselves."""
     return _autograd_function().apply(x, weight, bias, "layer", eps, weight_offset)
 
 
