@@ -429,3 +429,77 @@ def test_new_gradients_at_other_addresses(torch_dev):
         opt.step(0, grads=[g2[1], g2[0]])
     with pytest.raises(ValueError):
         opt.step(0, grad_scale=torch.ones(2, device=dev))
+
+
+def test_offsets_past_32_bits(torch_dev):
+    """One tensor of more than 2^32 elements with 8-bit states: its last blocks against the
+    oracle (the rounding bits have the index's high word in them), and its norm."""
+    torch, dev = torch_dev
+    ohp, hp = as_hp()
+    n = (1 << 32) + 4096 + 700
+    gen = torch.Generator(dev).manual_seed(9)
+    w = torch.zeros(n, device=dev)
+    g = torch.empty(n, dtype=torch.bfloat16, device=dev).normal_(0.0, 1e-3, generator=gen)
+    opt = muon.AdamWMulti([w], [g], hp, state_bits=8, seed=21)
+    norm = muon.GradNorm([g])
+    norm.measure(1e9)
+    opt.step(0, grad_scale=norm.factor)
+    torch.cuda.synchronize()
+    sq = sum(float(p.double().square().sum()) for p in g.split(1 << 28))
+    assert abs(float(norm.total[0]) / np.sqrt(sq) - 1) < 1.01 * U
+    for first, count in ((n - 700 - 2048, 2748), ((1 << 32) - 512, 1024), (0, 512), (1 << 31, 256)):
+        gv = host(g[first:first + count])
+        rw, rm, rv = A.adamw_step(np.zeros(count), gv, np.zeros(count), np.zeros(count), 0, ohp)
+        got = host(w[first:first + count])
+        assert (np.abs(got - rw) <= 14 * U * np.abs(rw) + 2.0 ** -148).all()
+        bm, bv = O8.rounding_bits(21, 0, 0, np.arange(first, first + count))
+        blocks = slice(first // 256, -(-(first + count) // 256))
+        em, eu = 5 * U * np.abs(rm) + 2.0 ** -148, 6 * U * np.sqrt(rv)
+        check_codes(codes(opt.exp_avg[0][first:first + count]), host(opt.exp_avg_scale[0][blocks]), rm, em, bm, 0, first)
+        check_codes(codes(opt.exp_avg_sq[0][first:first + count]), host(opt.exp_avg_sq_scale[0][blocks]), np.sqrt(rv), eu, bv, 1,
+                    first)
+
+
+def test_both_widths_in_one_plan(torch_dev):
+    """The C call takes states of both widths in one list: the same as two lists, apart from
+    the position that the rounding bits know."""
+    import ctypes
+    torch, dev = torch_dev
+    shapes = [(5000,), (300,), (9000,)]
+    w1, g = tensors(torch, dev, 740, WL.ROLE_W, shapes, 0.02), tensors(torch, dev, 740, WL.ROLE_G, shapes, 1e-3)
+    w2 = [x.clone() for x in w1]
+    small, wide = muon.AdamWMulti(w1, g, state_bits=8, seed=4), muon.AdamWMulti(w2, g, state_bits=32, seed=4)
+    mixed_w = [x.clone() for x in w1]
+    a, b = muon.AdamWMulti(mixed_w, g, state_bits=8, seed=4), muon.AdamWMulti(mixed_w, g, state_bits=32, seed=4)
+    arr = (B.AdamWTensor * 3)(a._arr[0], b._arr[1], a._arr[2])
+    need, plan = ctypes.c_size_t(), B.TensorPlan()
+    lib = B.load_library()
+    assert lib.adamw_multi_plan_bytes(arr, 3, need) == 0
+    table = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.adamw_multi_plan(arr, 3, table.data_ptr(), table.numel(), plan, stream) == 0
+    for step in range(2):
+        small.step(step)
+        wide.step(step)
+        assert lib.adamw_multi_step(plan, small.hp, step, 4, None, stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(mixed_w[0], w1[0]) and torch.equal(mixed_w[1], w2[1]) and torch.equal(mixed_w[2], w1[2])
+    assert torch.equal(a.exp_avg[2].view(torch.uint8), small.exp_avg[2].view(torch.uint8))
+
+
+def test_overflowing_second_moment(torch_dev):
+    """|g| above 1.8e19: v is infinite, the update 0 (fp32's own answer); 32-bit states keep
+    it to the element."""
+    torch, dev = torch_dev
+    for bits in (8, 32):
+        g = [torch.full((600,), 1e-3, device=dev)]
+        g[0][10] = 3e25
+        w = [torch.ones(600, device=dev)]
+        opt = muon.AdamWMulti(w, g, muon.adamw_default_hparams(weight_decay=0.0), state_bits=bits)
+        opt.step(0)
+        torch.cuda.synchronize()
+        assert float(w[0][10]) == 1.0 and bool(torch.isfinite(w[0]).all())
+        g[0][10] = 0.0
+        opt.step(1)
+        bad = ~torch.isfinite(w[0])
+        assert int(bad.sum()) == (256 if bits == 8 else 0)

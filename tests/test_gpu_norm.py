@@ -361,3 +361,59 @@ def test_autograd_expanded_gradient_and_frozen_inputs(torch_dev):
     b = torch.zeros(96, device=dev, requires_grad=True)
     muon.layer_norm(x.detach(), None, b).sum().backward()
     assert torch.equal(b.grad, torch.full((96,), 20.0, device=dev))
+
+
+def test_in_place_gradient_that_overflows(torch_dev):
+    """fp16 gradients that overflow to infinity, written over dy and over x: the weight's
+    gradient is the one of separate buffers, for row counts that leave teams without a row."""
+    torch, dev = torch_dev
+    for rows, cols in ((5, 64), (37, 128), (70, 320), (131, 1024), (300, 640)):
+        x = draw(torch, dev, 620, 0, (rows, cols), torch.float16, 1e-3)
+        dy = draw(torch, dev, 620, 1, (rows, cols), torch.float16, 300.0)
+        w = draw(torch, dev, 620, 2, (cols,), torch.float32)
+        _, mean, rstd = muon.norm_forward(x, w, eps=1e-8)
+        want = muon.norm_backward(dy, x, w, mean, rstd)
+        assert bool(torch.isinf(want[0]).any()) and bool(torch.isfinite(want[1]).all())
+        for target in ("dy", "x"):
+            a, g = x.clone(), dy.clone()
+            got = muon.norm_backward(g, a, w, mean, rstd, out=g if target == "dy" else a)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), (rows, cols, target)
+
+
+def test_offsets_past_32_bits(torch_dev):
+    """A tensor of more than 2^32 elements: its last rows as those of a small one."""
+    torch, dev = torch_dev
+    cols, rows = 4096, (1 << 20) + 7
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev).normal_(0.0, 1.0, generator=torch.Generator(dev).manual_seed(3))
+    w = draw(torch, dev, 630, 1, (cols,), torch.float32, 0.3, 1.0)
+    y, mean, rstd = muon.norm_forward(x, w)
+    for part in (slice(rows - 9, rows), slice((1 << 20) - 3, (1 << 20) + 2), slice(0, 5)):
+        p, m, r = muon.norm_forward(x[part].clone(), w)
+        assert torch.equal(p, y[part]) and torch.equal(m, mean[part]) and torch.equal(r, rstd[part])
+    dx, _, _ = muon.norm_backward(y, x, w, mean, rstd, out=y)
+    for part in (slice(rows - 9, rows), slice(0, 5)):
+        xs = x[part].clone()
+        p, m, r = muon.norm_forward(xs, w)
+        want, _, _ = muon.norm_backward(p, xs, w, m, r)
+        assert torch.equal(want, dx[part])
+
+
+def test_two_streams_at_once(torch_dev):
+    """Two calls at the same time on two streams, each with its own workspace."""
+    torch, dev = torch_dev
+    xs = [draw(torch, dev, 640 + i, 0, (8192, 1024), torch.bfloat16) for i in range(2)]
+    w = draw(torch, dev, 640, 1, (1024,), torch.float32)
+    refs = []
+    for x in xs:
+        y, m, r = muon.norm_forward(x, w, w)
+        refs.append((y, m, r) + muon.norm_backward(x, x, w, m, r))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        outs = []
+        for x, s in zip(xs, streams):
+            y, m, r = muon.norm_forward(x, w, w, stream=s)
+            outs.append((y, m, r) + muon.norm_backward(x, x, w, m, r, stream=s))
+        torch.cuda.synchronize()
+        for got, want in zip(outs, refs):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
