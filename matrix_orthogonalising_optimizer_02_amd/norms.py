@@ -9,11 +9,34 @@ and `rms_norm` are the same for torch.autograd.
 from __future__ import annotations
 
 import ctypes
+import struct
+
 from . import binding as B
 
 NORM_LAYER, NORM_RMS = 0, 1
 MAX_COLS = 16384
 _KINDS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+
+# The C structs norm_desc, norm_rows and norm_param as bytes: a small call's time is the
+# host's, and packing takes a fifth of building a ctypes.Structure.
+_pack_desc = struct.Struct("@4q3i2f4x").pack
+_pack_rows = struct.Struct("@P2q").pack
+_pack_param = struct.Struct("@Pq").pack
+_calls = None
+
+
+def _entry_points():
+    """norm_forward, norm_backward and the workspace query with plain pointer arguments."""
+    global _calls
+    if _calls is None:
+        lib = B.load_library()
+        vp = ctypes.c_void_p
+        forward, backward, size = lib["norm_forward"], lib["norm_backward"], lib["norm_backward_workspace_bytes"]
+        forward.argtypes = [vp] * 8
+        backward.argtypes = [vp] * 10 + [ctypes.c_size_t, vp]
+        size.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+        _calls = forward, backward, size
+    return _calls
 
 
 def _row_levels(t, name):
@@ -39,9 +62,13 @@ def _row_levels(t, name):
 
 
 def _layout(tensors):
-    """(inner, row structs) for [(tensor, name)] of one shape."""
-    if all(t.is_contiguous() for t, _ in tensors):
-        return 1, [B.NormRows(t.data_ptr() or None, t.shape[-1], 0) for t, _ in tensors]
+    """(inner, packed norm_rows) for [(tensor, name)] of one shape."""
+    for t, _ in tensors:
+        if not t.is_contiguous():
+            break
+    else:
+        cols = tensors[0][0].shape[-1]
+        return 1, [_pack_rows(t.data_ptr(), cols, 0) for t, _ in tensors]
     levels = [_row_levels(t, name) for t, name in tensors]
     inner = 1
     for lv, (_, name) in zip(levels, tensors):
@@ -56,7 +83,7 @@ def _layout(tensors):
         else:
             s1 = lv[0][1] if lv else 0
             s0 = s1 * inner
-        rows.append(B.NormRows(t.data_ptr() or None, s0, s1))
+        rows.append(_pack_rows(t.data_ptr(), s0, s1))
     return inner, rows
 
 
@@ -85,7 +112,7 @@ def _check_like(t, name, x):
 
 
 def _param(t, name, cols, groups, x, dtypes):
-    """(groups, struct) of a weight or bias whose last dimension is the row's."""
+    """(groups, packed norm_param) of a weight or bias whose last dimension is the row's."""
     if not isinstance(t, B._torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -103,26 +130,29 @@ def _param(t, name, cols, groups, x, dtypes):
         if len(levels) > 1:
             raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
         stride = levels[0][1] if levels else cols
-    return n, B.NormParam(t.data_ptr() or None, stride)
+    return n, _pack_param(t.data_ptr(), stride)
 
 
-def _desc(x, weight, bias, kind, eps, weight_offset, inner):
-    """(descriptor, weight struct, bias struct) of a call on x."""
-    torch = B._torch()
+def _desc(x, rows, cols, weight, bias, kind, eps, weight_offset, inner):
+    """(packed norm_desc, weight's, bias's packed norm_param) of a call on x."""
     if kind not in _KINDS:
         raise ValueError("kind must be 'layer' or 'rms'")
     codes = B.dtype_codes()
-    cols = x.shape[-1]
-    groups, w, b, wdtype = None, None, None, torch.float32
+    float32 = B._torch().float32
+    groups, w, b, wdtype = None, None, None, float32
     if weight is not None:
+        groups, w = _param(weight, "weight", cols, None, x, (float32, x.dtype))
         wdtype = weight.dtype
-        groups, w = _param(weight, "weight", cols, None, x, (torch.float32, x.dtype))
     if bias is not None:
-        groups, b = _param(bias, "bias", cols, groups, x, (torch.float32, x.dtype) if weight is None else (wdtype,))
+        groups, b = _param(bias, "bias", cols, groups, x, (float32, x.dtype) if weight is None else (wdtype,))
         wdtype = bias.dtype
-    d = B.NormDesc(x.numel() // cols if cols else 0, cols, 1 if groups is None else groups, inner, _KINDS[kind],
-                   codes[x.dtype], codes[wdtype], eps, weight_offset)
-    return d, w, b
+    return _pack_desc(rows, cols, 1 if groups is None else groups, inner, _KINDS[kind], codes[x.dtype], codes[wdtype],
+                      eps, weight_offset), w, b
+
+
+def _like(x):
+    """A new tensor of x's shape and type, rows adjacent."""
+    return B._torch().empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def norm_forward(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1e-6,
@@ -136,36 +166,53 @@ def norm_forward(x, weight=None, bias=None, *, kind: str = "layer", eps: float =
     norm_backward; neither is computed into memory with stats=False (both None then). out:
     receives y, and may be x.
     """
-    torch = B._torch()
     _check_x(x)
     device = x.device
-    with B.device_and_stream(device, stream):
-        if out is None:
-            y = x.new_empty(x.shape)
-        else:
-            _check_like(out, "out", x)
-            y = out
-        inner, (rx, ry) = _layout(((x, "x"), (y, "out")))
-        d, w, b = _desc(x, weight, bias, kind, eps, weight_offset, inner)
-        mean = rstd = None
-        pm = pr = None
-        if stats:
-            rstd = x.new_empty(d.rows, dtype=torch.float32)
-            pr = rstd.data_ptr() or None
-            if kind == "layer":
-                mean = x.new_empty(d.rows, dtype=torch.float32)
-                pm = mean.data_ptr() or None
-        rc = B.load_library().norm_forward(d, rx, w, b, ry, pm, pr, B.raw_stream(stream, device))
+    if stream is not None or B._torch().cuda.current_device() != device.index:
+        with B.device_and_stream(device, stream):
+            return _forward(x, weight, bias, kind, eps, weight_offset, out, stats, B.raw_stream(stream, device))
+    return _forward(x, weight, bias, kind, eps, weight_offset, out, stats, B.raw_stream(None, device))
+
+
+def _forward(x, weight, bias, kind, eps, weight_offset, out, stats, stream):
+    float32 = B._torch().float32
+    if out is None:
+        y = _like(x)
+    else:
+        _check_like(out, "out", x)
+        y = out
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    inner, (rx, ry) = _layout(((x, "x"), (y, "out")))
+    d, w, b = _desc(x, rows, cols, weight, bias, kind, eps, weight_offset, inner)
+    mean = rstd = pm = pr = None
+    if stats:
+        rstd = x.new_empty(rows, dtype=float32)
+        pr = rstd.data_ptr()
+        if kind == "layer":
+            mean = x.new_empty(rows, dtype=float32)
+            pm = mean.data_ptr()
+    rc = _entry_points()[0](d, rx, w, b, ry, pm, pr, stream)
     if rc:
         B._check(rc, "norm_forward")
     return y, mean, rstd
 
 
-def norm_backward_workspace_bytes(desc: "B.NormDesc") -> int:
-    """Bytes of norm_backward's workspace for a call's descriptor."""
+def _workspace_bytes(desc):
     out = ctypes.c_size_t(0)
-    B._check(B.load_library().norm_backward_workspace_bytes(desc, out), "norm_backward_workspace_bytes")
-    return int(out.value)
+    B._check(_entry_points()[2](desc, out), "norm_backward_workspace_bytes")
+    return out.value
+
+
+def norm_backward_workspace_bytes(rows: int, cols: int, groups: int = 1, kind: str = "layer", dtype=None,
+                                  weight_dtype=None) -> int:
+    """Bytes of norm_backward's workspace for [rows, cols] of dtype (default bfloat16) in
+    `groups` groups, weights of weight_dtype (default float32)."""
+    torch, codes = B._torch(), B.dtype_codes()
+    if kind not in _KINDS:
+        raise ValueError("kind must be 'layer' or 'rms'")
+    return _workspace_bytes(_pack_desc(rows, cols, groups, 1, _KINDS[kind], codes[dtype or torch.bfloat16],
+                                       codes[weight_dtype or torch.float32], 1.0, 0.0))
 
 
 def norm_backward(dy, x, weight, mean, rstd, *, kind: str = "layer", weight_offset: float = 0.0,
@@ -178,47 +225,57 @@ def norm_backward(dy, x, weight, mean, rstd, *, kind: str = "layer", weight_offs
     dtype as grad_shape and grad_dtype. out: receives dx, and may be dy or x. workspace:
     optional uint8 device buffer of norm_backward_workspace_bytes().
     """
-    torch = B._torch()
     _check_x(x)
     _check_like(dy, "dy", x)
     device = x.device
-    with B.device_and_stream(device, stream):
-        if out is None:
-            dx = x.new_empty(x.shape)
+    args = (dy, x, weight, mean, rstd, kind, weight_offset, weight_grad, bias_grad, out, workspace)
+    if stream is not None or B._torch().cuda.current_device() != device.index:
+        with B.device_and_stream(device, stream):
+            return _backward(*args, B.raw_stream(stream, device), grad_shape, grad_dtype)
+    return _backward(*args, B.raw_stream(None, device), grad_shape, grad_dtype)
+
+
+def _backward(dy, x, weight, mean, rstd, kind, weight_offset, weight_grad, bias_grad, out, workspace, stream, grad_shape,
+              grad_dtype):
+    torch = B._torch()
+    device = x.device
+    if out is None:
+        dx = _like(x)
+    else:
+        _check_like(out, "out", x)
+        dx = out
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    inner, (rdy, rx, rdx) = _layout(((dy, "dy"), (x, "x"), (dx, "out")))
+    dbias = None
+    if bias_grad:
+        if weight is not None:
+            dbias = _like(weight)
         else:
-            _check_like(out, "out", x)
-            dx = out
-        inner, (rdy, rx, rdx) = _layout(((dy, "dy"), (x, "x"), (dx, "out")))
-        dbias = None
-        if bias_grad:
-            if weight is not None:
-                dbias = weight.new_empty(weight.shape)
-            else:
-                dbias = x.new_empty(x.shape[-1:] if grad_shape is None else tuple(grad_shape),
-                                    dtype=grad_dtype or torch.float32)
-        d, w, db = _desc(x, weight, dbias, kind, 1.0, weight_offset, inner)
-        dweight = dw = None
-        if weight_grad and weight is not None:
-            dweight = weight.new_empty(weight.shape)
-            dw = B.NormParam(dweight.data_ptr() or None, d.cols)
-        stats = []
-        for t, nm in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != d.rows
-                                  or not t.is_contiguous() or t.device != device):
-                raise ValueError(f"{nm} must be a contiguous float32 tensor on {device} with one entry per row")
-            stats.append(t.data_ptr() or None if t is not None else None)
-        ws, wsb = None, 0
-        if workspace is not None:
-            if workspace.device != device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
-                raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-            ws, wsb = workspace.data_ptr(), workspace.numel()
-        elif dw is not None or db is not None:
-            wsb = norm_backward_workspace_bytes(d)
-            if wsb:
-                workspace = torch.empty(wsb, dtype=torch.uint8, device=device)
-                ws = workspace.data_ptr()
-        rc = B.load_library().norm_backward(d, rdy, rx, w, stats[0], stats[1], rdx, dw, db, ws, wsb,
-                                            B.raw_stream(stream, device))
+            dbias = x.new_empty(x.shape[-1:] if grad_shape is None else tuple(grad_shape),
+                                dtype=grad_dtype or torch.float32)
+    d, w, db = _desc(x, rows, cols, weight, dbias, kind, 1.0, weight_offset, inner)
+    dweight = dw = None
+    if weight_grad and weight is not None:
+        dweight = _like(weight)
+        dw = _pack_param(dweight.data_ptr(), cols)
+    stats = []
+    for t, nm in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != rows
+                              or not t.is_contiguous() or t.device != device):
+            raise ValueError(f"{nm} must be a contiguous float32 tensor on {device} with one entry per row")
+        stats.append(t.data_ptr() if t is not None else None)
+    ws, wsb = None, 0
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        ws, wsb = workspace.data_ptr(), workspace.numel()
+    elif dw is not None or db is not None:
+        wsb = _workspace_bytes(d)
+        if wsb:
+            workspace = x.new_empty(wsb, dtype=torch.uint8)
+            ws = workspace.data_ptr()
+    rc = _entry_points()[1](d, rdy, rx, w, stats[0], stats[1], rdx, dw, db, ws, wsb, stream)
     if rc:
         B._check(rc, "norm_backward")
     return dx, dweight, dbias

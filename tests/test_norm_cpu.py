@@ -147,7 +147,23 @@ def test_row_levels_and_layout():
     assert norms._row_levels(torch.zeros(1, 8).expand(6, 8), "x") == [(6, 0)]
     q, y = torch.zeros(7, 3, 4, 8)[:, 1], torch.zeros(7, 4, 8)
     inner, (rq, ry) = norms._layout(((q, "q"), (y, "y")))
+    rq, ry = (B.NormRows.from_buffer_copy(r) for r in (rq, ry))
     assert inner == 4 and (rq.stride0, rq.stride1) == (96, 8) and (ry.stride0, ry.stride1) == (32, 8)
+    assert rq.data == q.data_ptr()
+
+
+def test_packed_structs_are_the_headers():
+    """The byte forms of the calls' structs against the ctypes structures of the header."""
+    d = B.NormDesc.from_buffer_copy(norms._pack_desc(1, 2, 3, 4, 5, 6, 7, 0.5, 0.25))
+    assert [getattr(d, f) for f, _ in d._fields_] == [1, 2, 3, 4, 5, 6, 7, 0.5, 0.25]
+    assert len(norms._pack_desc(1, 2, 3, 4, 5, 6, 7, 0.5, 0.25)) == ctypes.sizeof(B.NormDesc)
+    r = B.NormRows.from_buffer_copy(norms._pack_rows(1 << 50, 2, 3))
+    assert (r.data, r.stride0, r.stride1) == (1 << 50, 2, 3)
+    p = B.NormParam.from_buffer_copy(norms._pack_param(0, 3))
+    assert (p.data, p.stride) == (None, 3)
+    assert norms.norm_backward_workspace_bytes(1 << 16, 128) >= 2 * 2 * 128 * 4
+    with pytest.raises(B.MuonError):
+        norms.norm_backward_workspace_bytes(10, 128, groups=3)
 
 
 def test_division_by_the_inner_rows():
