@@ -87,13 +87,14 @@ __global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
     if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(256) void k_grad_total(GradArgs a) {
+constexpr int kTotalThreads = 1024;
+__global__ __launch_bounds__(kTotalThreads) void k_grad_total(GradArgs a) {
     const int t = blockIdx.x;
     const bool total = t == a.count;
     const int begin = total ? 0 : a.table[t].blk_begin, end = total ? a.blocks : a.table[t].blk_end;
     double s = 0.0;
-    for (int i = begin + threadIdx.x; i < end; i += 256) s += a.partial[i];
-    s = sqrt(block_sum_d<256>(s));
+    for (int i = begin + threadIdx.x; i < end; i += kTotalThreads) s += a.partial[i];
+    s = sqrt(block_sum_d<kTotalThreads>(s));
     if (threadIdx.x != 0) return;
     if (!total) {
         if (a.norms) a.norms[t] = (float)s;
@@ -164,7 +165,7 @@ hipError_t launch_grad_norm(const GradArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_grad_total(const GradArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_grad_total, dim3(unsigned(a.count) + 1), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_grad_total, dim3(unsigned(a.count) + 1), dim3(kTotalThreads), 0, s, a);
     return hipGetLastError();
 }
 

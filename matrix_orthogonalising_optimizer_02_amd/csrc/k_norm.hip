@@ -14,11 +14,12 @@
 // where each block has a stretch of its own), and ask for the next rows before they reduce
 // the present one. Statistics are two-pass over the registers (the mean first, then the
 // squares of the differences), all sums in fp32 in a fixed order. Outputs are stored with
-// the non-temporal hint ([8192, 5120] bf16 forward 31 us; 40 us without), inputs are read
+// the non-temporal hint ([32768, 1024] bf16 forward 25 us; 31 us without), inputs are read
 // without it (a preceding kernel may have left them in the cache).
-// Measured: [8192, 5120] bf16 in 8 groups, forward 28.9 us (5.8 TB/s), backward 53.3 us
-// (4.7 TB/s with the weights' gradients, 5.6 TB/s without); [65536, 5120] backward 380 us
-// (5.3 TB/s); a copy reaches 6.25 TB/s.
+// Measured: [8192, 5120] bf16 in 8 groups, forward 28 to 29 us (5.9 TB/s), backward 53 us
+// (4.7 TB/s with the weights' gradients, 5.6 TB/s without); [65536, 5120] backward 374 us
+// (5.4 TB/s); a copy reaches 6.25 TB/s. The vector units are busy 43% of the forward pass
+// and 48% of the backward pass.
 #include "lanes.hpp"
 #include "train.hpp"
 
