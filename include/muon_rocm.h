@@ -388,7 +388,7 @@ int adamw_multi_plan_bytes(const adamw_tensor* tensors, int32_t count, size_t* b
  * scale, a capture), ALIGN (w, m, v, g, copy not 16-byte aligned, scales not 4-byte), ALIAS (any two
  * of all w, copy, m, v, m_scale, v_scale, g ranges or the table overlap, gradients with each
  * other excepted), WORKSPACE (device
- * NULL or too small), TOO_LARGE (2^40 elements in a tensor, 2^31 blocks), HIP. */
+ * NULL or too small), TOO_LARGE (2^36 elements or 2^22 - 1 tensors and more in all), HIP. */
 int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* device, size_t bytes, tensor_plan* plan,
                      void* stream);
 
@@ -483,7 +483,7 @@ typedef struct norm_param {
  * and strides). One launch.
  * Errors: INVALID_ARG, ALIGN, ALIAS (y, mean or rstd overlaps another buffer, by the
  * span from its first to its last element), TOO_LARGE (cols above MUON_NORM_MAX_COLS,
- * rows or groups above 2^30, a span above 2^46 elements), HIP. rows == 0 or cols == 0 is
+ * rows or groups above 2^30, groups that take 2^32 threads, a span above 2^46 elements), HIP. rows == 0 or cols == 0 is
  * a no-op. */
 int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_param* w, const norm_param* b,
                  const norm_rows* y, float* mean, float* rstd, void* stream);

@@ -18,7 +18,10 @@ namespace muon {
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+// A launch has at most 2^32 - 1 threads: in blocks of 256, or one of 1024 for each gradient's norm.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+constexpr int64_t kMaxBlocks = kMaxThreads / 256, kMaxTensors = kMaxThreads / 1024;
+static_assert(kMultiThreads == 256, "a step's blocks");
 constexpr int32_t kPlanAdamw = 0x41444d57, kPlanGrads = 0x4e4f524d;
 
 // Blocks of the gradient norm: runs of at least 16384 elements, and longer ones where the
@@ -35,6 +38,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int check_list(const void* list, int32_t count) {
     if (count < 0) return fail(MUON_ERR_INVALID_ARG, "count < 0");
     if (count > 0 && !list) return fail(MUON_ERR_INVALID_ARG, "the list of tensors is NULL");
+    if (count >= kMaxTensors) return fail(MUON_ERR_TOO_LARGE, "more tensors than a launch takes");
     return MUON_OK;
 }
 
@@ -65,7 +69,7 @@ int adamw_sizes(const adamw_tensor* t, int32_t count, Sizes* s) {
         if ((rc = check_numel(t[i].numel, i))) return rc;
         s->blocks += ceil_div(t[i].numel, kMultiBlockElems);
     }
-    if (s->blocks > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+    if (s->blocks > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "more blocks than a launch takes");
     s->map = align256(size_t(count) * sizeof(MultiDesc));
     s->bytes = s->blocks ? s->map + align256(size_t(s->blocks) * 4) : 0;
     return MUON_OK;
@@ -81,7 +85,7 @@ int grad_sizes(const grad_tensor* t, int32_t count, Sizes* s) {
     }
     s->block_elems = std::max(kGradBlockElems, ceil_div(ceil_div(total, kGradBlocks), kGradBlockElems) * kGradBlockElems);
     for (int i = 0; i < count; ++i) s->blocks += ceil_div(t[i].numel, s->block_elems);
-    if (s->blocks > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+    if (s->blocks > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "more blocks than a launch takes");
     s->map = align256(size_t(count) * sizeof(GradDesc));
     s->partial = s->map + align256(size_t(s->blocks) * 4);
     s->bytes = count ? s->partial + align256(size_t(s->blocks) * 8) : 0;

@@ -20,7 +20,7 @@ static_assert(kF32 == MUON_DTYPE_F32 && kBF16 == MUON_DTYPE_BF16 && kF16 == MUON
 static_assert(kNormMaxCols == MUON_NORM_MAX_COLS, "column limit");
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of a launch, a dimension
 constexpr int64_t kMaxSpan = int64_t(1) << 46;
 
 int fail(int code, const std::string& what) { return set_last_error(code, what); }
@@ -148,7 +148,8 @@ MUON_API int norm_forward(const norm_desc* desc, const norm_rows* x, const norm_
         if ((rc = check_overlaps(ranges))) return rc;
         if (d.rows == 0 || d.cols == 0) return MUON_OK;
         const NormPlan p = plan_norm_forward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-        if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+        if (d.groups * int64_t(p.chunks) > kMaxThreads / p.threads)
+            return fail(MUON_ERR_TOO_LARGE, "more groups than a launch takes");
         NormArgs a = base_args(d, p);
         a.x = rows_ptr(*x);
         a.y = rows_ptr(*y);
@@ -206,7 +207,8 @@ MUON_API int norm_backward(const norm_desc* desc, const norm_rows* dy, const nor
             return rc;
         if (d.cols == 0) return MUON_OK;
         const NormPlan p = plan_norm_backward(d.dtype, d.cols, d.rows / d.groups, d.groups);
-        if (d.groups * int64_t(p.chunks) > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "2^31 blocks or more");
+        if (d.groups * int64_t(p.chunks) > kMaxThreads / p.threads)
+            return fail(MUON_ERR_TOO_LARGE, "more groups than a launch takes");
         const bool grads = present(dw) || present(db);
         const size_t need = grads ? partial_bytes(d, p) : 0;
         if (need) {

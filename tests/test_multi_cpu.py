@@ -65,6 +65,11 @@ def test_adamw_plan_lists_and_buffers(lib):  # noqa: F811
     assert lib.adamw_multi_plan_bytes(two, -2, need) == INVALID
     big = (B.AdamWTensor * 9)(*[tensor(0, numel=1 << 40)] * 9)
     assert lib.adamw_multi_plan_bytes(big, 9, need) == LARGE
+    # blocks of 4096 elements and 256 threads in a launch of less than 2^32 threads
+    most = ((1 << 24) - 1) * 4096
+    assert lib.adamw_multi_plan_bytes((B.AdamWTensor * 1)(tensor(0, numel=most)), 1, need) == B.MUON_OK
+    assert lib.adamw_multi_plan_bytes((B.AdamWTensor * 1)(tensor(0, numel=most + 1)), 1, need) == LARGE
+    assert lib.adamw_multi_plan_bytes(two, (1 << 22) - 1, need) == LARGE
 
 
 @fake_only

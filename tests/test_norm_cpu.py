@@ -49,6 +49,7 @@ BAD_DESCS = [(dict(rows=-1), -1), (dict(cols=-1), -1), (dict(groups=0), -1), (di
              (dict(inner=3), -1), (dict(kind=2), -1), (dict(dtype=3), -1), (dict(dtype=-1), -1), (dict(wdtype=2), -1),
              (dict(eps=0.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
              (dict(weight_offset=float("nan")), -1), (dict(cols=16385), -6), (dict(rows=(1 << 30) + 1, groups=1), -6)]
+HUGE = dict(rows=1 << 30, groups=1 << 30, cols=8)  # a block a group: more threads than a launch takes
 
 
 @fake_only
@@ -82,6 +83,15 @@ def test_pointer_refusals(lib):  # noqa: F811
     assert forward(lib, rstd=BASE + 5 * GIB + 2) == B.MUON_ERR_ALIGN
     assert backward(lib, ws=BASE + 8 * GIB + 128, d=desc(rows=1 << 20)) == B.MUON_ERR_ALIGN
     assert forward(lib, x=rows(0, 1 << 41)) == B.MUON_ERR_TOO_LARGE
+
+
+@fake_only
+def test_more_groups_than_a_launch_takes(lib):  # noqa: F811
+    far = B.NormParam(BASE << 1, 8), B.NormParam(BASE << 2, 8)
+    args = dict(w=far[0], b=far[1], mean=None, rstd=None)
+    assert forward(lib, desc(**HUGE), x=B.NormRows(BASE, 8, 0), y=B.NormRows(BASE << 3, 8, 0), **args) == B.MUON_ERR_TOO_LARGE
+    assert backward(lib, desc(**HUGE), dy=B.NormRows(BASE, 8, 0), x=B.NormRows(BASE, 8, 0), w=far[0], mean=ptr(100), rstd=ptr(200),
+                    dx=B.NormRows(BASE << 3, 8, 0), dw=B.NormParam(BASE << 4, 8), db=None) == B.MUON_ERR_TOO_LARGE
 
 
 @fake_only
