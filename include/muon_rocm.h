@@ -401,6 +401,16 @@ int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* device, s
 int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t step, uint64_t seed,
                      const float* grad_scale, void* stream);
 
+/* The same step with its counter, and if wanted its learning rate, on the device: for steps
+ * that are captured into a graph, where a host argument would stay what it was at capture
+ * (with it the bias corrections and the rounding bits of 8-bit states, which have to change
+ * from step to step). counter: DEVICE int64, 8-byte aligned: the 0-based step, not below 0;
+ * the call uses its value and then adds one, so that every plan needs its own; a plan without
+ * elements launches nothing and leaves it. lr: DEVICE float, NULL = hp->lr. Two launches.
+ * Errors: as adamw_multi_step, INVALID_ARG for a NULL counter. */
+int adamw_multi_step_device(const tensor_plan* plan, const adamw_hparams* hp, int64_t* counter, const float* lr,
+                            uint64_t seed, const float* grad_scale, void* stream);
+
 /* ---- Gradient norm and clipping --------------------------------------------------------
  * n_i = l2 norm of tensor i, total = sqrt(sum n_i^2), factor = min(1, max_norm / (total +
  * 1e-6)): on the device, for adamw_multi_step's grad_scale and grad_scale() below. Squares

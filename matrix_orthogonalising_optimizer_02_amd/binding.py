@@ -38,7 +38,7 @@ EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_defa
             "adamw_default_hparams", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy",
             "rownorm_shard_workspace_bytes", "rownorm_shard_colsq", "rownorm_shard_apply",
             "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
-            "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
+            "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step", "adamw_multi_step_device",
             "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
@@ -164,6 +164,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.adamw_multi_plan_bytes.argtypes = [ctypes.POINTER(AdamWTensor), i32, size]
     lib.adamw_multi_plan.argtypes = [ctypes.POINTER(AdamWTensor), i32, vp, sz, plan, vp]
     lib.adamw_multi_step.argtypes = [plan, ctypes.POINTER(AdamWHParams), i64, ctypes.c_uint64, vp, vp]
+    lib.adamw_multi_step_device.argtypes = [plan, ctypes.POINTER(AdamWHParams), vp, vp, ctypes.c_uint64, vp, vp]
     lib.grad_norm_plan_bytes.argtypes = [ctypes.POINTER(GradTensor), i32, size]
     lib.grad_norm_plan.argtypes = [ctypes.POINTER(GradTensor), i32, vp, sz, plan, vp]
     lib.grad_norm.argtypes = [plan, ctypes.c_float, vp, vp, vp]
@@ -176,7 +177,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "ns5_plan", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
-                 "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale", "muon_ceiling_copy", "muon_ceiling_mfma",
+                 "adamw_multi_step_device", "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
+                 "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:

@@ -71,7 +71,8 @@ int adamw_sizes(const adamw_tensor* t, int32_t count, Sizes* s) {
     }
     if (s->blocks > kMaxBlocks) return fail(MUON_ERR_TOO_LARGE, "more blocks than a launch takes");
     s->map = align256(size_t(count) * sizeof(MultiDesc));
-    s->bytes = s->blocks ? s->map + align256(size_t(s->blocks) * 4) : 0;
+    // descriptors, the blocks' tensors, and the scalars of a step with a counter on the device
+    s->bytes = s->blocks ? s->map + align256(size_t(s->blocks) * 4) + align256(sizeof(MultiScalars)) : 0;
     return MUON_OK;
 }
 
@@ -233,42 +234,87 @@ MUON_API int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* 
     });
 }
 
+namespace muon {
+namespace {
+
+int check_step(const tensor_plan* plan, const adamw_hparams* hp, const float* grad_scale) {
+    const int rc = check_plan(plan, kPlanAdamw);
+    if (rc) return rc;
+    if (!hp) return fail(MUON_ERR_INVALID_ARG, "hparams is NULL");
+    if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
+        return fail(MUON_ERR_INVALID_ARG, "lr and weight_decay must be finite");
+    if (!(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f))
+        return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+    if (!(hp->eps >= FLT_MIN) || !std::isfinite(hp->eps))
+        return fail(MUON_ERR_INVALID_ARG, "eps must be a finite, normal number > 0");
+    if (addr(grad_scale) & 3) return fail(MUON_ERR_ALIGN, "grad_scale not 4-byte aligned");
+    return MUON_OK;
+}
+
+MultiArgs step_args(const tensor_plan& p, const adamw_hparams& hp, const float* grad_scale) {
+    MultiArgs a{};
+    a.table = static_cast<const MultiDesc*>(p.device);
+    a.tensor_of_block = reinterpret_cast<const int32_t*>(static_cast<const char*>(p.device) +
+                                                         align256(size_t(p.count) * sizeof(MultiDesc)));
+    a.blocks = p.blocks;
+    a.bits = p.reserved;
+    a.beta1 = hp.beta1;
+    a.beta2 = hp.beta2;
+    a.one_minus_beta1 = float(1.0 - double(hp.beta1));
+    a.one_minus_beta2 = float(1.0 - double(hp.beta2));
+    a.eps = hp.eps;
+    a.grad_scale = grad_scale;
+    return a;
+}
+
+uint32_t seed_key(uint64_t seed) { return mix32(mix32(uint32_t(seed)) + uint32_t(seed >> 32)); }
+
+}  // namespace
+}  // namespace muon
+
 MUON_API int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t step, uint64_t seed,
                               const float* grad_scale, void* stream) {
     return guarded([&]() -> int {
-        const int rc = check_plan(plan, kPlanAdamw);
+        const int rc = check_step(plan, hp, grad_scale);
         if (rc) return rc;
-        if (!hp) return fail(MUON_ERR_INVALID_ARG, "hparams is NULL");
-        if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
-            return fail(MUON_ERR_INVALID_ARG, "lr and weight_decay must be finite");
-        if (!(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f))
-            return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-        if (!(hp->eps >= FLT_MIN) || !std::isfinite(hp->eps))
-            return fail(MUON_ERR_INVALID_ARG, "eps must be a finite, normal number > 0");
         if (step < 0) return fail(MUON_ERR_INVALID_ARG, "step < 0");
-        if (addr(grad_scale) & 3) return fail(MUON_ERR_ALIGN, "grad_scale not 4-byte aligned");
         if (plan->blocks == 0) return MUON_OK;
         // bias corrections in double on the host (t = step + 1)
         const double t = double(step) + 1.0;
-        const double bc1 = 1.0 - std::pow(double(hp->beta1), t);
-        const double bc2 = 1.0 - std::pow(double(hp->beta2), t);
-        MultiArgs a{};
-        a.table = static_cast<const MultiDesc*>(plan->device);
-        a.tensor_of_block = reinterpret_cast<const int32_t*>(static_cast<const char*>(plan->device) +
-                                                             align256(size_t(plan->count) * sizeof(MultiDesc)));
-        a.blocks = plan->blocks;
-        a.bits = plan->reserved;
-        a.key = mix32(mix32(mix32(uint32_t(seed)) + uint32_t(seed >> 32)) + uint32_t(step));
-        a.beta1 = hp->beta1;
-        a.beta2 = hp->beta2;
-        a.one_minus_beta1 = float(1.0 - double(hp->beta1));
-        a.one_minus_beta2 = float(1.0 - double(hp->beta2));
-        a.eps = hp->eps;
-        a.lr_bc1 = float(double(hp->lr) / bc1);
-        a.inv_sqrt_bc2 = float(1.0 / std::sqrt(bc2));
-        a.lr_wd = double(hp->lr) * double(hp->weight_decay);
-        a.grad_scale = grad_scale;
+        MultiArgs a = step_args(*plan, *hp, grad_scale);
+        a.host.lr_bc1 = float(double(hp->lr) / (1.0 - std::pow(double(hp->beta1), t)));
+        a.host.inv_sqrt_bc2 = float(1.0 / std::sqrt(1.0 - std::pow(double(hp->beta2), t)));
+        a.host.lr_wd = double(hp->lr) * double(hp->weight_decay);
+        a.host.key = mix32(seed_key(seed) + uint32_t(step));
         hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        return run_timed(MUON_KCLASS_ADAMW_MULTI, s, "adamw multi", [&] { return launch_multi_step(a, s); });
+    });
+}
+
+MUON_API int adamw_multi_step_device(const tensor_plan* plan, const adamw_hparams* hp, int64_t* counter, const float* lr,
+                                     uint64_t seed, const float* grad_scale, void* stream) {
+    return guarded([&]() -> int {
+        int rc = check_step(plan, hp, grad_scale);
+        if (rc) return rc;
+        if (!counter) return fail(MUON_ERR_INVALID_ARG, "counter is NULL");
+        if (addr(counter) & 7) return fail(MUON_ERR_ALIGN, "counter not 8-byte aligned");
+        if (addr(lr) & 3) return fail(MUON_ERR_ALIGN, "lr not 4-byte aligned");
+        if (plan->blocks == 0) return MUON_OK;
+        MultiArgs a = step_args(*plan, *hp, grad_scale);
+        char* end = static_cast<char*>(plan->device) + plan->bytes;
+        MultiScalarArgs m{};
+        m.out = reinterpret_cast<MultiScalars*>(end - align256(sizeof(MultiScalars)));
+        m.counter = counter;
+        m.lr = lr;
+        m.lr_host = hp->lr;
+        m.beta1 = hp->beta1;
+        m.beta2 = hp->beta2;
+        m.weight_decay = hp->weight_decay;
+        m.seed_key = seed_key(seed);
+        a.scalars = m.out;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        rc = run_timed(MUON_KCLASS_TENSOR_PLAN, s, "adamw scalars", [&] { return launch_multi_scalars(m, s); });
+        if (rc) return rc;
         return run_timed(MUON_KCLASS_ADAMW_MULTI, s, "adamw multi", [&] { return launch_multi_step(a, s); });
     });
 }

@@ -318,13 +318,14 @@ __global__ __launch_bounds__(kMultiThreads) void k_adamw_multi(MultiArgs a) {
     h.ob1 = a.one_minus_beta1;
     h.ob2 = a.one_minus_beta2;
     h.eps = a.eps;
-    h.step = a.lr_bc1 * d.lr_scale;
-    h.inv_sqrt_bc2 = a.inv_sqrt_bc2;
-    h.decay = (float)(1.0 - a.lr_wd * (double)d.lr_scale * (double)d.wd_scale);
+    const MultiScalars sc = a.scalars ? *a.scalars : a.host;
+    h.step = sc.lr_bc1 * d.lr_scale;
+    h.inv_sqrt_bc2 = sc.inv_sqrt_bc2;
+    h.decay = (float)(1.0 - sc.lr_wd * (double)d.lr_scale * (double)d.wd_scale);
     h.gs = a.grad_scale ? *a.grad_scale : 1.f;
     const bool full = base + kMultiBlockElems <= d.n;
     if (kBits == 8 || (kBits == 0 && d.bits == 8)) {
-        const uint32_t key = mix32(a.key + (uint32_t)d.index * 0x510E527Fu);
+        const uint32_t key = mix32(sc.key + (uint32_t)d.index * 0x510E527Fu);
         if (!full) step8<false, -1>(d, h, base, key);
         else if (d.g_type == kF32) step8<true, kF32>(d, h, base, key);
         else if (d.g_type == kBF16) step8<true, kBF16>(d, h, base, key);
@@ -335,6 +336,21 @@ __global__ __launch_bounds__(kMultiThreads) void k_adamw_multi(MultiArgs a) {
         else if (d.g_type == kBF16) step32<true, kBF16>(d, h, base);
         else step32<true, kF16>(d, h, base);
     }
+}
+
+// The scalars of a step whose counter is on the device, and the counter's increase: one
+// thread, in double as the host's.
+__global__ void k_multi_scalars(MultiScalarArgs a) {
+    const int64_t step = *a.counter;
+    const double t = (double)step + 1.0, lr = a.lr ? (double)*a.lr : (double)a.lr_host;
+    MultiScalars s;
+    s.lr_bc1 = (float)(lr / (1.0 - pow((double)a.beta1, t)));
+    s.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow((double)a.beta2, t)));
+    s.lr_wd = lr * (double)a.weight_decay;
+    s.key = mix32(a.seed_key + (uint32_t)step);
+    s.pad_ = 0;
+    *a.out = s;
+    *a.counter = step + 1;
 }
 
 __global__ void k_grad_table(GradDescArgs a) {
@@ -351,6 +367,11 @@ hipError_t launch_multi_table(const MultiDescArgs& a, hipStream_t s) {
 
 hipError_t launch_multi_map(const MultiDesc* table, int count, int32_t* map, int blocks, hipStream_t s) {
     hipLaunchKernelGGL(k_map<MultiDesc>, dim3((unsigned(blocks) + 255) / 256), dim3(256), 0, s, table, count, map, blocks);
+    return hipGetLastError();
+}
+
+hipError_t launch_multi_scalars(const MultiScalarArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(k_multi_scalars, dim3(1), dim3(1), 0, s, a);
     return hipGetLastError();
 }
 

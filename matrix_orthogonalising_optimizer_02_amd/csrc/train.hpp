@@ -100,18 +100,33 @@ struct MultiDescArgs {
     int32_t first, n;
 };
 
+// A step's scalars that follow from its counter and learning rate.
+struct MultiScalars {
+    float lr_bc1;          // lr / (1 - beta1^t)
+    float inv_sqrt_bc2;    // 1 / sqrt(1 - beta2^t)
+    double lr_wd;          // lr * weight_decay
+    uint32_t key;          // of (seed, step)
+    uint32_t pad_;
+};
+
 struct MultiArgs {
     const MultiDesc* table;
     const int32_t* tensor_of_block;
     int32_t blocks;
     int32_t bits;          // 8 or 32: the width of all states; 0: both occur
-    uint32_t key;          // of (seed, step)
     float beta1, beta2, one_minus_beta1, one_minus_beta2;
     float eps;
-    float lr_bc1;          // lr / (1 - beta1^t)
-    float inv_sqrt_bc2;    // 1 / sqrt(1 - beta2^t)
-    double lr_wd;          // lr * weight_decay
+    MultiScalars host;     // used where `scalars` is null
+    const MultiScalars* scalars;  // on the device
     const float* grad_scale;
+};
+
+struct MultiScalarArgs {
+    MultiScalars* out;
+    int64_t* counter;
+    const float* lr;       // null: lr_host
+    float lr_host, beta1, beta2, weight_decay;
+    uint32_t seed_key;     // of the seed alone
 };
 
 struct GradDesc {
@@ -150,6 +165,7 @@ __host__ __device__ inline uint32_t mix32(uint32_t x) {
 
 hipError_t launch_multi_table(const MultiDescArgs& a, hipStream_t s);
 hipError_t launch_multi_map(const MultiDesc* table, int count, int32_t* map, int blocks, hipStream_t s);
+hipError_t launch_multi_scalars(const MultiScalarArgs& a, hipStream_t s);
 hipError_t launch_multi_step(const MultiArgs& a, hipStream_t s);
 hipError_t launch_grad_table(const GradDescArgs& a, hipStream_t s);
 hipError_t launch_grad_map(const GradDesc* table, int count, int32_t* map, int blocks, hipStream_t s);

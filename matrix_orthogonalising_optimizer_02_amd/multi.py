@@ -182,16 +182,31 @@ class AdamWMulti:
                                       B.raw_stream(stream, self.device))
         B._check(rc, "adamw_multi_plan")
 
-    def step(self, step: int, grad_scale=None, stream=None, grads=None):
-        """One step at 0-based `step`. grad_scale: optional one-element float32 device tensor."""
+    def step(self, step, grad_scale=None, stream=None, grads=None, lr=None):
+        """One step. step: the 0-based step number, or, for steps in a captured graph, a
+        one-element int64 device tensor that holds it and is increased by the call, so each
+        AdamWMulti has its own (a number would stay as it was at the capture, and with it
+        the bias corrections and the rounding bits). grad_scale: optional one-element float32 device tensor. lr: with a
+        counter, an optional one-element float32 device tensor in place of hp.lr."""
         if grads is not None:
             self.set_grads(grads, stream)
         if self.grads is None:
             raise ValueError("the step has no gradients")
+        torch, lib = B._torch(), B.load_library()
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
+        counted = isinstance(step, torch.Tensor)
+        if counted:
+            if step.dtype != torch.int64 or step.numel() != 1 or step.device != self.device:
+                raise ValueError(f"a step counter must be an int64 tensor of one element on {self.device}")
+        elif lr is not None:
+            raise ValueError("lr as a tensor goes with a step counter; otherwise set hp.lr")
+        rate = _scalar_ptr(lr, "lr", self.device)
         with B.device_and_stream(self.device, stream):
-            rc = B.load_library().adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale,
-                                                   B.raw_stream(stream, self.device))
+            handle = B.raw_stream(stream, self.device)
+            if counted:
+                rc = lib.adamw_multi_step_device(self._plan, self.hp, step.data_ptr(), rate, self.seed, scale, handle)
+            else:
+                rc = lib.adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale, handle)
         B._check(rc, "adamw_multi_step")
 
     def moments(self, i: int):

@@ -325,6 +325,52 @@ def test_captured_clip_and_step_replay_bitwise(torch_dev, bits):
         assert float(torch.randn(1 << 18, device=dev).sum()) != 0.0
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_captured_step_with_a_counter_on_the_device(torch_dev, bits):
+    """A captured step whose counter and learning rate are on the device: each replay is the
+    next step, with other rounding bits, as a host loop of steps (the bias corrections, made
+    in double on either side, may differ in fp32's last place: u of the update, 4 u with
+    the update's own roundings)."""
+    torch, dev = torch_dev
+    shapes = [(5000,), (64, 130), (9,)]
+    g = tensors(torch, dev, 750, WL.ROLE_G, shapes, 1e-3)
+
+    def fresh():
+        w = tensors(torch, dev, 750, WL.ROLE_W, shapes, 0.02)
+        return w, muon.AdamWMulti(w, g, state_bits=bits, seed=1 << 33)
+
+    w1, eager = fresh()
+    w2, counted = fresh()
+    counter, lr = torch.tensor([3], device=dev), torch.tensor([1e-4], device=dev)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        counted.step(counter, lr=lr)
+    assert int(counter) == 3
+    for r in range(4):
+        for i, t in enumerate(g):
+            t.copy_(tensors(torch, dev, 751 + r, WL.ROLE_G, shapes, 1e-3)[i])
+        rate = float(np.float32(1e-4 * (r + 1)))
+        lr.fill_(rate)
+        eager.hp.lr = rate
+        eager.step(3 + r)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(counter) == 4 + r
+        for a, b in zip(eager.exp_avg + eager.exp_avg_sq, counted.exp_avg + counted.exp_avg_sq):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), r
+        for a, b in zip(w1, w2):
+            # updates of at most 4 lr a step so far, 4 u of each, and W's own rounding
+            assert float((a - b).abs().max()) <= (r + 1) * (4 * U * 4 * rate * 4 + 2 * U * 0.2), r
+        assert float(torch.randn(1 << 18, device=dev).sum()) != 0.0
+    with pytest.raises(ValueError):
+        counted.step(torch.tensor([3.0], device=dev))
+    with pytest.raises(ValueError):
+        counted.step(3, lr=lr)
+
+
 def test_side_stream_step(torch_dev):
     torch, dev = torch_dev
     shapes = [(50000,), (77,)]

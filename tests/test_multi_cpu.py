@@ -90,6 +90,11 @@ def test_adamw_step_refusals(lib):  # noqa: F811
     for over in (dict(beta1=1.0), dict(beta2=-0.1), dict(eps=0.0), dict(eps=1e-39), dict(lr=float("nan")),
                  dict(weight_decay=float("inf"))):
         assert lib.adamw_multi_step(empty, B.adamw_default_hparams(**over), 0, 0, None, None) == INVALID, over
+    assert lib.adamw_multi_step_device(empty, hp, BASE, None, 0, None, None) == B.MUON_OK
+    assert lib.adamw_multi_step_device(empty, hp, None, None, 0, None, None) == INVALID
+    assert lib.adamw_multi_step_device(empty, hp, BASE + 4, None, 0, None, None) == ALIGN
+    assert lib.adamw_multi_step_device(empty, hp, BASE, BASE + 2, 0, None, None) == ALIGN
+    assert lib.adamw_multi_step_device(B.TensorPlan(), hp, BASE, None, 0, None, None) == INVALID
     grads = B.TensorPlan()
     assert lib.grad_norm_plan(None, 0, None, 0, grads, None) == B.MUON_OK
     assert lib.adamw_multi_step(grads, hp, 0, 0, None, None) == INVALID  # another call's plan
