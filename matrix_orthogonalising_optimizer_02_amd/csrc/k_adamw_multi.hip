@@ -48,14 +48,16 @@ struct Hyper {
 };
 
 // sqrt(v): r = 1/sqrt(v) from the hardware (1 ulp), s = v r, and one Newton step on s
-// whose residual is exact; seven operations where sqrtf has about sixteen. The same bits
-// as sqrtf on 3e8 values between 2^-97 and 2^127; nearer to 2^-126 the residual loses
-// digits and one value in fifty is an ulp off, and a v below 2^-126 (a gradient below
-// 4e-18) gets a root up to 2 times too small, nowhere near any eps in use.
+// whose residual is exact; with the factor below twelve operations where sqrtf has about
+// sixteen. The same bits as sqrtf on 3e8 values between 2^-97 and 2^127. Nearer to 2^-126
+// the residual loses digits, and the hardware's root takes no number below it: a v below
+// 2^-96 is multiplied by 2^64 first and its root by 2^-32 after, both exact.
 __device__ __forceinline__ float root(float v) {
-    const float r = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
-    const float s = v * r;
-    const float u = fmaf(fmaf(-s, s, v), 0.5f * r, s);
+    const bool small = v < 0x1p-96f;
+    const float x = v * (small ? 0x1p64f : 1.f);
+    const float r = __builtin_amdgcn_rsqf(fmaxf(x, 0x1p-126f));  // finite for 0
+    const float s = x * r;
+    const float u = fmaf(fmaf(-s, s, x), 0.5f * r, s) * (small ? 0x1p-32f : 1.f);
     return v == __builtin_inff() ? v : u;
 }
 

@@ -549,3 +549,52 @@ def test_overflowing_second_moment(torch_dev):
         opt.step(1)
         bad = ~torch.isfinite(w[0])
         assert int(bad.sum()) == (256 if bits == 8 else 0)
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1e-18, 2.0 ** -126])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_second_moments_and_small_eps(torch_dev, bits, eps):
+    """Gradients of 1e-20 to 1e-17: v is a subnormal fp32 number, and eps no cover for its root.
+
+    v is off by at most 2^-149 besides 8 u of itself (g'^2, its product, the decoded root's
+    square and b2 times it each round to a multiple of 2^-149 there, to half a step, the
+    first and the third times a factor below 1), so its root lies between those of v - e and
+    v + e; the update is off by 16 u besides that and m's own error (the module's text)."""
+    torch, dev = torch_dev
+    ohp, hp = as_hp(lr=1e-3, eps=eps, weight_decay=0.0)
+    sizes, n = [1e-17, 1e-18, 1e-19, 3e-20, 1e-20], 700
+    rng = np.random.default_rng(5)
+    w = [torch.zeros(n, device=dev) for _ in sizes]
+    opt = muon.AdamWMulti(w, [torch.zeros(n, device=dev) for _ in sizes], hp, state_bits=bits, seed=9)
+    for step in range(3):
+        g = [torch.from_numpy((s * rng.uniform(0.9, 1.1, n) * rng.choice([-1.0, 1.0], n)).astype(np.float32)).to(dev)
+             for s in sizes]
+        if bits == 8:
+            scales = [(host(opt.exp_avg_scale[i]), host(opt.exp_avg_sq_scale[i])) for i in range(len(sizes))]
+            md = [O8.decode(codes(opt.exp_avg[i])) * np.repeat(s[0], O8.BLOCK)[:n] for i, s in enumerate(scales)]
+            vd = [(O8.decode(codes(opt.exp_avg_sq[i])) * np.repeat(s[1], O8.BLOCK)[:n]) ** 2 for i, s in enumerate(scales)]
+        else:
+            md, vd = [host(t) for t in opt.exp_avg], [host(t) for t in opt.exp_avg_sq]
+        before = [host(t) for t in w]
+        opt.step(step, grads=g)
+        torch.cuda.synchronize()
+        for i, size in enumerate(sizes):
+            gv, t = host(g[i]), step + 1
+            _, rm, rv = A.adamw_step(before[i], gv, md[i], vd[i], step, ohp)
+            ev = 1.5 * 2.0 ** -149 + 8 * U * rv
+            em = 5 * U * (np.abs(ohp.beta1 * md[i]) + np.abs((1 - ohp.beta1) * gv)) + 2.0 ** -148
+            lo, hi = np.sqrt(np.maximum(rv - ev, 0.0)), np.sqrt(rv + ev)
+            k, bc = ohp.lr / (1 - ohp.beta1 ** t), np.sqrt(1 - ohp.beta2 ** t)
+            least = k * np.maximum(np.abs(rm) - em, 0.0) / (hi / bc + ohp.eps) * (1 - 16 * U)
+            most = k * (np.abs(rm) + em) / (lo / bc + ohp.eps) * (1 + 16 * U)
+            got = (before[i] - host(w[i])) * np.sign(rm)
+            tol = U * (np.abs(before[i]) + np.abs(host(w[i])))
+            ok = (got >= least - tol) & (got <= most + tol)
+            assert ok.all(), (size, step, float((got / most).max()), float((got / np.maximum(least, 1e-300)).min()))
+            if bits == 32:
+                assert (np.abs(host(opt.exp_avg_sq[i]) - rv) <= ev).all(), (size, step)
+            else:  # the stored root: a code's step (1/8, or 2^-9 of the scale) either way
+                top = np.repeat(host(opt.exp_avg_sq_scale[i]), O8.BLOCK)[:n]
+                u1 = O8.decode(codes(opt.exp_avg_sq[i])) * top
+                assert (u1 >= lo * 0.87 - top * 2.0 ** -9).all() and (u1 <= hi * 1.13 + top * 2.0 ** -9).all(), (size, step)
+        log(f"{bits} bits, eps {eps:.1e}, step {step}: largest update {max(float(np.abs(host(t)).max()) for t in w):.2e}")
