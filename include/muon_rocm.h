@@ -182,6 +182,12 @@ int ns5_plan(const int64_t* rows, const int64_t* cols, int32_t count, int32_t* o
 int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step,
               void* workspace, size_t workspace_bytes, float* update_rms, void* stream);
 
+/* muon_step's checks alone: the status that it would refuse the same arguments with, or
+ * MUON_OK. Host only. For a caller that has to know before it writes anything (a clipped
+ * step scales the gradients in place first). Errors: muon_step's, but HIP. */
+int muon_step_check(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step, void* workspace,
+                    size_t workspace_bytes, float* update_rms);
+
 /* Newton-Schulz orthogonalisation alone ("Muon is Scalable", Sec. 2.1 Eq. 2):
  * o_out[i] = NS_N(m_in[i]) with X0 = M / max(||M||_F, eps), for [rows[i], cols[i]]
  * fp32 device matrices; the output has the input's shape and orientation. bf16 MFMA

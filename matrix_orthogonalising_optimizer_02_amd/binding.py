@@ -33,7 +33,7 @@ KCLASS_NAMES = ("cast", "frob", "gram", "poly", "apply", "apply_final", "rownorm
                 "tensor_plan", "adamw_multi", "grad_norm", "grad_total", "grad_scale")
 
 EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_default_hparams",
-            "muon_workspace_bytes", "ns5_plan", "muon_step", "ns5_batched", "rownorm_update",
+            "muon_workspace_bytes", "ns5_plan", "muon_step", "muon_step_check", "ns5_batched", "rownorm_update",
             "rownorm_update_noalloc",
             "adamw_default_hparams", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy",
             "rownorm_shard_workspace_bytes", "rownorm_shard_colsq", "rownorm_shard_apply",
@@ -140,6 +140,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ns5_plan.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64), i32,
                              ctypes.POINTER(ctypes.c_int32), i32, ctypes.POINTER(ctypes.c_int32)]
     lib.muon_step.argtypes = [ctypes.POINTER(MuonMatrix), i32, ctypes.POINTER(MuonHParams), i64, vp, sz, vp, vp]
+    lib.muon_step_check.argtypes = [ctypes.POINTER(MuonMatrix), i32, ctypes.POINTER(MuonHParams), i64, vp, sz, vp]
     lib.ns5_batched.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(ctypes.c_int64), i32, ctypes.POINTER(MuonHParams), vp, sz, vp]
     lib.rownorm_update.argtypes = [ctypes.POINTER(MuonMatrix), i32, ctypes.POINTER(MuonHParams), vp, sz, vp, vp]
@@ -173,7 +174,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.muon_ceiling_mfma.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
     lib.muon_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
-    for name in ("muon_step", "ns5_batched", "rownorm_update", "rownorm_update_noalloc", "muon_workspace_bytes",
+    for name in ("muon_step", "muon_step_check", "ns5_batched", "rownorm_update", "rownorm_update_noalloc", "muon_workspace_bytes",
                  "ns5_plan", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
@@ -387,6 +388,15 @@ def muon_step(weights, momenta, grads, step: int, hp: Optional[MuonHParams] = No
     ws, wsb, _owner = _ws(workspace, [tuple(w.shape) for w in weights], dev, stream)
     rc = load_library().muon_step(arr, len(weights), ctypes.byref(hp), int(step), ws, wsb,
                                   _monitor_ptr(update_rms, len(weights)), _stream_handle(stream, dev))
+    _check(rc, "muon_step")
+
+
+def muon_step_check(weights, momenta, grads, step: int, hp: MuonHParams, workspace, update_rms=None):
+    """Raises what muon_step would refuse these arguments with; enqueues nothing."""
+    arr = _matrices(weights, momenta, grads)
+    rc = load_library().muon_step_check(arr, len(weights), ctypes.byref(hp), int(step),
+                                        ctypes.c_void_p(workspace.data_ptr()), ctypes.c_size_t(workspace.numel()),
+                                        _monitor_ptr(update_rms, len(weights)))
     _check(rc, "muon_step")
 
 

@@ -1312,26 +1312,40 @@ MUON_API int ns5_plan(const int64_t* rows, const int64_t* cols, int32_t count, i
     return MUON_OK;
 }
 
-MUON_API int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step,
-                       void* workspace, size_t workspace_bytes, float* update_rms, void* stream) {
-    g_last_error.clear();
+// Every check of a step on either kind, and its plan.
+static int check_muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step, void* workspace,
+                           size_t workspace_bytes, float* update_rms, Plan* plan) {
     if (step < 0) return fail(MUON_ERR_INVALID_ARG, "step < 0");
     int rc = check_hparams(hp, true);
     if (rc) return rc;
-    if (step % hp->period_k != 0)
-        return do_rownorm(mats, count, hp, workspace, workspace_bytes, update_rms, stream, true);
     std::vector<int64_t> rows, cols;
     std::vector<Range> ranges;
     rc = check_matrices(mats, count, rows, cols, ranges);
     if (rc) return rc;
     rc = check_monitor(update_rms, count, ranges);
     if (rc) return rc;
+    rc = make_plan(rows.data(), cols.data(), count, plan);
+    if (rc) return rc;
+    rc = check_workspace(*plan, workspace, workspace_bytes, ranges);
+    if (rc) return rc;
+    return check_overlaps(ranges);
+}
+
+MUON_API int muon_step_check(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step, void* workspace,
+                             size_t workspace_bytes, float* update_rms) {
+    return guarded([&]() -> int {
+        Plan plan;
+        return check_muon_step(mats, count, hp, step, workspace, workspace_bytes, update_rms, &plan);
+    });
+}
+
+MUON_API int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, int64_t step,
+                       void* workspace, size_t workspace_bytes, float* update_rms, void* stream) {
+    g_last_error.clear();
+    if (step >= 0 && hp && hp->period_k >= 1 && step % hp->period_k != 0)
+        return do_rownorm(mats, count, hp, workspace, workspace_bytes, update_rms, stream, true);
     Plan plan;
-    rc = make_plan(rows.data(), cols.data(), count, &plan);
-    if (rc) return rc;
-    rc = check_workspace(plan, workspace, workspace_bytes, ranges);
-    if (rc) return rc;
-    rc = check_overlaps(ranges);
+    int rc = check_muon_step(mats, count, hp, step, workspace, workspace_bytes, update_rms, &plan);
     if (rc) return rc;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     for (const GroupPlan& gp : plan.groups) {

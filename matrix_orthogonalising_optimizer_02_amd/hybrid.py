@@ -145,35 +145,45 @@ class HybridOptimizer:
         self.step_count = 0
 
     def step(self, grads: Dict[str, "object"], stream=None, update_rms=None):
-        factor = None
-        if self.max_grad_norm is not None and self.names:
-            factor = self._clip(grads, stream)
+        """One step. What either half refuses is refused before anything is written: weights,
+        states, gradients and step_count are then as they were."""
+        gm, ga = [grads[n] for n in self.muon_names], [grads[n] for n in self.adamw_names]
+        muon = [self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names], gm
         if self.muon_names:
-            B.muon_step([self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names],
-                        [grads[n] for n in self.muon_names], self.step_count, self.muon_hp, self.workspace,
-                        stream, update_rms)
-        if self.adamw_names:
-            g = [grads[n] for n in self.adamw_names]
-            if self.adamw_state_bits is not None:
-                self._adamw.step(self.step_count, factor, stream, g)
-            elif self._adamw is None:
-                self._adamw = B.AdamWGroup([self.params[n] for n in self.adamw_names], g,
-                                           [self.exp_avg[n] for n in self.adamw_names],
-                                           [self.exp_avg_sq[n] for n in self.adamw_names], self.adamw_hp)
-                self._adamw.step(self.step_count, stream)
-            else:
-                same = all(a is b for a, b in zip(g, self._adamw.tensors[1]))
-                self._adamw.step(self.step_count, stream, None if same else g)
+            B.muon_step_check(*muon, self.step_count, self.muon_hp, self.workspace, update_rms)
+        factor = None
+        if self.adamw_state_bits is None:
+            # adamw_step checks all of its tensors before its first launch, so it goes first
+            if self.adamw_names:
+                self._adamw_step(ga, stream)
+        else:
+            if self.adamw_names:
+                self._adamw.check_hparams(self.step_count)
+                self._adamw.set_grads(ga, stream)
+            if self.max_grad_norm is not None and self.names:
+                factor = self._clip([grads[n] for n in self.names], gm, stream)
+            if self.adamw_names:
+                self._adamw.step(self.step_count, factor, stream)
+        if self.muon_names:
+            B.muon_step(*muon, self.step_count, self.muon_hp, self.workspace, stream, update_rms)
         self.step_count += 1
 
-    def _clip(self, grads, stream):
+    def _adamw_step(self, g, stream):
+        if self._adamw is None:
+            self._adamw = B.AdamWGroup([self.params[n] for n in self.adamw_names], g,
+                                       [self.exp_avg[n] for n in self.adamw_names],
+                                       [self.exp_avg_sq[n] for n in self.adamw_names], self.adamw_hp)
+            self._adamw.step(self.step_count, stream)
+        else:
+            same = all(a is b for a, b in zip(g, self._adamw.tensors[1]))
+            self._adamw.step(self.step_count, stream, None if same else g)
+
+    def _clip(self, g, gm, stream):
         """Measures all gradients, scales Muon's; the factor for AdamW's (device tensor)."""
-        g, gm = [grads[n] for n in self.names], [grads[n] for n in self.muon_names]
-        for n, t in zip(self.muon_names, gm):  # what muon_step refuses is not scaled first
-            B._check_tensor(t, f"gradient of {n}")
         if self._norm is None:
-            self._norm = GradNorm(g, stream)
+            norm = GradNorm(g, stream)
             self._muon_norm = GradNorm(gm, stream) if gm else None
+            self._norm = norm
         else:
             self._norm.set_grads(g, stream)
             if gm:

@@ -120,6 +120,8 @@ class AdamWMulti:
                 self.exp_avg_sq_scale[i].data_ptr() or None if small else None, 0,
                 codes[c.dtype] if c is not None else 0, state_bits, lr_scales[i], wd_scales[i])
         self._plan = B.TensorPlan()
+        self._empty = B.TensorPlan()
+        B._check(B.load_library().adamw_multi_plan(None, 0, None, 0, self._empty, None), "adamw_multi_plan")
         self._table = None
         self.grads = self._ptrs = None
         if grads is not None:
@@ -207,6 +209,11 @@ class AdamWMulti:
                 rc = lib.adamw_multi_step_device(self._plan, self.hp, step.data_ptr(), rate, self.seed, scale, handle)
             else:
                 rc = lib.adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale, handle)
+        B._check(rc, "adamw_multi_step")
+
+    def check_hparams(self, step: int = 0):
+        """Raises where step() would refuse hp or the step's number; enqueues nothing."""
+        rc = B.load_library().adamw_multi_step(self._empty, self.hp, int(step), self.seed, None, None)
         B._check(rc, "adamw_multi_step")
 
     def moments(self, i: int):

@@ -1,0 +1,110 @@
+"""The hybrid optimizer as a training loop drives it: refused steps, gradients that come
+and go, steps captured with a counter on the device, and checkpoints.
+
+Comparisons are to the bit, with the same calls on other buffers or with a run that was
+not disturbed; where a tolerance stands, its test derives it.
+"""
+import sys
+import weakref
+
+import numpy as np
+import pytest
+
+import matrix_orthogonalising_optimizer_02_amd as muon
+from matrix_orthogonalising_optimizer_02_amd import binding as B
+from matrix_orthogonalising_optimizer_02_amd import hybrid as H
+from matrix_orthogonalising_optimizer_02_amd import workloads as WL
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = {"blocks.0.q.weight": (96, 64), "blocks.0.q.bias": (96,), "blocks.0.q_norm.weight": (96,), "blocks.0.up.weight": (64, 64),
+          "head.weight": (37, 5), "head.bias": (1,)}
+
+
+@pytest.fixture(scope="module")
+def torch_dev():
+    import torch
+    assert torch.cuda.is_available(), "the gpu tests need a visible GPU"
+    B.load_library()
+    return torch, torch.device("cuda:0")
+
+
+def log(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def draws(torch, dev, key, std, step=0, names=SHAPES):
+    order = list(SHAPES)
+    return {n: torch.from_numpy(WL.host_normal(key, WL.ROLE_G, order.index(n), SHAPES[n], std, step)).to(dev) for n in names}
+
+
+def fresh(torch, dev, bits, clip=0.01, names=SHAPES, **more):
+    return H.HybridOptimizer(draws(torch, dev, 940, 0.05, names=names), adamw_state_bits=bits,
+                             max_grad_norm=clip if bits is not None else None, **more)
+
+
+def everything(opt, grads):
+    """Copies of all that a step may write."""
+    t = list(opt.params.values()) + list(opt.momenta.values()) + list(opt.exp_avg.values()) + list(opt.exp_avg_sq.values())
+    if opt.adamw_state_bits is not None:
+        t += opt._adamw.exp_avg + opt._adamw.exp_avg_sq
+    return [x.clone() for x in t + list(grads.values())]
+
+
+def same(torch, a, b):
+    return len(a) == len(b) and all(torch.equal(x.reshape(-1).view(torch.uint8), y.reshape(-1).view(torch.uint8)) for x, y in zip(a, b))
+
+
+def off_by_one_element(torch, g):
+    """The same values at an address that is no multiple of 16 bytes."""
+    flat = torch.empty(g.numel() + 1, dtype=g.dtype, device=g.device)
+    flat[1:].copy_(g.flatten())
+    return flat[1:].view(g.shape)
+
+
+def refused_calls(torch, opt, g):
+    """(what, gradients, more arguments) of steps that have to be refused; opt's fields are set back by the caller."""
+    yield "an AdamW gradient off 16 bytes", dict(g, **{"blocks.0.q.bias": off_by_one_element(torch, g["blocks.0.q.bias"])}), {}
+    yield "an AdamW gradient of another size", dict(g, **{"head.bias": torch.zeros(2, device=g["head.bias"].device)}), {}
+    yield "an AdamW gradient of another type", dict(g, **{"head.weight": g["head.weight"].double()}), {}
+    yield "an AdamW gradient that is missing", {n: t for n, t in g.items() if n != "head.bias"}, {}
+    yield "an AdamW gradient on its weight", dict(g, **{"head.weight": opt.params["head.weight"]}), {}
+    yield "a Muon gradient off 16 bytes", dict(g, **{"blocks.0.up.weight": off_by_one_element(torch, g["blocks.0.up.weight"])}), {}
+    yield "a Muon gradient of another shape", dict(g, **{"blocks.0.up.weight": torch.zeros(64, 60, device=g["head.bias"].device)}), {}
+    yield "a Muon gradient on its momentum", dict(g, **{"blocks.0.up.weight": opt.momenta["blocks.0.up.weight"]}), {}
+    yield "a monitor of another size", g, {"update_rms": torch.zeros(7, device=g["head.bias"].device)}
+
+
+@pytest.mark.parametrize("bits", [8, 32, None])
+def test_a_refused_step_changes_nothing(torch_dev, bits):
+    """Weights, momenta, moments, gradients and the step's number stay, and the next good
+    step is that of an optimizer that saw no refusal."""
+    torch, dev = torch_dev
+    opt, clean = fresh(torch, dev, bits), fresh(torch, dev, bits)
+    for step in range(2):  # a first step, and one with all tables written
+        g = draws(torch, dev, 941, 1e-2, step)
+        wrong = list(refused_calls(torch, opt, g))
+        for field, bad in (("adamw_hp", dict(beta1=1.0)), ("adamw_hp", dict(eps=0.0)), ("muon_hp", dict(eps=0.0))):
+            wrong.append((f"{field} {bad}", g, {"set": (field, bad)}))
+        for what, given, more in wrong:
+            more = dict(more)
+            field, bad = more.pop("set", (None, {}))
+            kept = everything(opt, given)
+            was = {k: getattr(getattr(opt, field), k) for k in bad} if field else {}
+            for k, v in bad.items():
+                setattr(getattr(opt, field), k, v)
+            with pytest.raises((B.MuonError, ValueError, KeyError)):
+                opt.step(given, **more)
+            for k, v in was.items():
+                setattr(getattr(opt, field), k, v)
+            torch.cuda.synchronize()
+            unchanged = same(torch, everything(opt, given), kept)
+            assert unchanged, (step, what)
+            assert opt.step_count == step, what
+        h = {n: t.clone() for n, t in g.items()}
+        opt.step(g)
+        clean.step(h)
+        torch.cuda.synchronize()
+        equal = same(torch, everything(opt, g), everything(clean, h))
+        assert equal, step
