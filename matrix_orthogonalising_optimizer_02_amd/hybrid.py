@@ -110,6 +110,9 @@ class HybridOptimizer:
     max_grad_norm: clip all gradients together to this l2 norm (needs 32 or 8 above). The
     factor stays on the device: Muon's gradients are scaled in place, AdamW's where they
     are read. `grad_norm` then holds the last step's norm and factor (float32 [2]).
+
+    With adamw_state_bits no gradient is kept after the step that it was given to; who
+    captures a step into a graph keeps its gradients for the replays.
     """
 
     def __init__(self, named_params: Dict[str, "object"], muon_hp: Optional[B.MuonHParams] = None,
@@ -151,22 +154,29 @@ class HybridOptimizer:
         muon = [self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names], gm
         if self.muon_names:
             B.muon_step_check(*muon, self.step_count, self.muon_hp, self.workspace, update_rms)
-        factor = None
         if self.adamw_state_bits is None:
             # adamw_step checks all of its tensors before its first launch, so it goes first
             if self.adamw_names:
                 self._adamw_step(ga, stream)
         else:
-            if self.adamw_names:
-                self._adamw.check_hparams(self.step_count)
-                self._adamw.set_grads(ga, stream)
-            if self.max_grad_norm is not None and self.names:
-                factor = self._clip([grads[n] for n in self.names], gm, stream)
-            if self.adamw_names:
-                self._adamw.step(self.step_count, factor, stream)
+            try:
+                self._multi_step([grads[n] for n in self.names], gm, ga, stream)
+            finally:
+                for held in (self._adamw, self._norm, self._muon_norm):
+                    if held is not None:
+                        held.release_grads()
         if self.muon_names:
             B.muon_step(*muon, self.step_count, self.muon_hp, self.workspace, stream, update_rms)
         self.step_count += 1
+
+    def _multi_step(self, g, gm, ga, stream):
+        """AdamW's half over all tensors at once, and the clipping of both."""
+        if self.adamw_names:
+            self._adamw.check_hparams(self.step_count)
+            self._adamw.set_grads(ga, stream)
+        factor = self._clip(g, gm, stream) if self.max_grad_norm is not None and g else None
+        if self.adamw_names:
+            self._adamw.step(self.step_count, factor, stream)
 
     def _adamw_step(self, g, stream):
         if self._adamw is None:

@@ -52,10 +52,24 @@ def _per_tensor(values, n, name):
     return values
 
 
-def _unchanged(grads, before, ptrs, plan):
-    """Whether the same tensors at the same addresses were given last, and their table written."""
-    return plan.kind != 0 and before is not None and len(grads) == len(before) \
-        and all(map(operator.is_, grads, before)) and [g.data_ptr() for g in grads] == ptrs
+_dtype = operator.attrgetter("dtype")
+
+
+def _unchanged(grads, ptrs, numels, dtypes, plan):
+    """Whether gradients are placed as those of the last table, and that was written."""
+    if plan.kind == 0 or ptrs is None:
+        return False
+    t = B._torch().Tensor
+    try:
+        return list(map(t.data_ptr, grads)) == ptrs and list(map(t.numel, grads)) == numels \
+            and list(map(_dtype, grads)) == dtypes and all(map(t.is_contiguous, grads))
+    except (TypeError, AttributeError):  # not tensors: the checks say which
+        return False
+
+
+def _need_grads(grads):
+    if grads is None:
+        raise ValueError("there are no gradients: give them first")
 
 
 def _scalar_ptr(t, name, device):
@@ -74,7 +88,8 @@ class AdamWMulti:
     """AdamW over a list of fp32 parameters of any shapes, in one launch a step.
 
     The gradient tensors given here, or to set_grads() or step() later (float32, bfloat16
-    or float16), are read at every step until others are given. Their addresses stand in a
+    or float16), are kept and read at every step until others are given or
+    release_grads() lets go of them. Their addresses stand in a
     table on the device that is written when they change, which cannot be captured into a
     graph: give the gradients before a capture. Replayed steps read the table too, so new
     gradients are new for them as well.
@@ -123,7 +138,7 @@ class AdamWMulti:
         self._empty = B.TensorPlan()
         B._check(B.load_library().adamw_multi_plan(None, 0, None, 0, self._empty, None), "adamw_multi_plan")
         self._table = None
-        self.grads = self._ptrs = None
+        self.grads = self._ptrs = self._dtypes = None
         if grads is not None:
             self.set_grads(grads, stream)
 
@@ -159,7 +174,8 @@ class AdamWMulti:
         one differs from before; steps that follow on the stream read them."""
         torch = B._torch()
         grads = list(grads)
-        if _unchanged(grads, self.grads, self._ptrs, self._plan):
+        if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
+            self.grads = grads
             return
         if len(grads) != self.n:
             raise ValueError("one gradient per parameter")
@@ -170,7 +186,7 @@ class AdamWMulti:
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.g_dtype == code
             d.g, d.g_dtype = ptr, code
-        self.grads, self._ptrs = grads, [g.data_ptr() for g in grads]
+        self.grads, self._ptrs, self._dtypes = grads, [g.data_ptr() for g in grads], [g.dtype for g in grads]
         if same:
             return
         lib = B.load_library()
@@ -184,6 +200,11 @@ class AdamWMulti:
                                       B.raw_stream(stream, self.device))
         B._check(rc, "adamw_multi_plan")
 
+    def release_grads(self):
+        """Lets go of the gradient tensors: the next step needs some given first. Tensors at
+        the same addresses then need no new table."""
+        self.grads = None
+
     def step(self, step, grad_scale=None, stream=None, grads=None, lr=None):
         """One step. step: the 0-based step number, or, for steps in a captured graph, a
         one-element int64 device tensor that holds it and is increased by the call, so each
@@ -192,8 +213,7 @@ class AdamWMulti:
         counter, an optional one-element float32 device tensor in place of hp.lr."""
         if grads is not None:
             self.set_grads(grads, stream)
-        if self.grads is None:
-            raise ValueError("the step has no gradients")
+        _need_grads(self.grads)
         torch, lib = B._torch(), B.load_library()
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
         counted = isinstance(step, torch.Tensor)
@@ -260,7 +280,7 @@ class GradNorm:
         self.device = _device_of(grads, "grads")
         self._arr = (B.GradTensor * max(self.n, 1))()
         self._plan = B.TensorPlan()
-        self._table = self._numels = self.grads = self._ptrs = None
+        self._table = self._numels = self.grads = self._ptrs = self._dtypes = None
         self.set_grads(grads, stream)
         with B.device_and_stream(self.device, stream):
             self.total = torch.empty(2, dtype=torch.float32, device=self.device)
@@ -271,7 +291,8 @@ class GradNorm:
         """New gradient tensors of the same sizes; written to the table where an address differs."""
         torch = B._torch()
         grads = list(grads)
-        if _unchanged(grads, self.grads, self._ptrs, self._plan):
+        if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
+            self.grads = grads
             return
         if len(grads) != self.n:
             raise ValueError(f"{self.n} gradients are expected")
@@ -283,7 +304,7 @@ class GradNorm:
             ptr, code = g.data_ptr() or None, codes[g.dtype]
             same = same and d.g == ptr and d.dtype == code
             d.g, d.numel, d.dtype = ptr, g.numel(), code
-        self.grads, self._ptrs = grads, [g.data_ptr() for g in grads]
+        self.grads, self._ptrs, self._dtypes = grads, [g.data_ptr() for g in grads], [g.dtype for g in grads]
         if same:
             return
         lib = B.load_library()
@@ -297,9 +318,15 @@ class GradNorm:
                                     B.raw_stream(stream, self.device))
         B._check(rc, "grad_norm_plan")
 
+    def release_grads(self):
+        """Lets go of the gradient tensors: the next call needs some given first. Tensors at
+        the same addresses then need no new table."""
+        self.grads = None
+
     def measure(self, max_norm: float, stream=None):
         """(total, norms): total[0] the norm over all gradients, total[1] the factor
         min(1, max_norm / (norm + 1e-6)), norms[i] the norm of gradient i."""
+        _need_grads(self.grads)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_norm(self._plan, max_norm, self.total.data_ptr(), self.norms.data_ptr() or None,
                                             B.raw_stream(stream, self.device))
@@ -309,6 +336,7 @@ class GradNorm:
     def scale_(self, factor=None, stream=None):
         """The gradients times `factor` in place (one-element float32 device tensor; by
         default the last measure()'s clip factor). Nothing is read or written where it is 1."""
+        _need_grads(self.grads)
         ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_scale(self._plan, ptr, B.raw_stream(stream, self.device))

@@ -108,3 +108,37 @@ def test_a_refused_step_changes_nothing(torch_dev, bits):
         torch.cuda.synchronize()
         equal = same(torch, everything(opt, g), everything(clean, h))
         assert equal, step
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_gradients_are_not_kept_after_the_step(torch_dev, bits):
+    """The gradients' memory is free once the caller drops them, and tensors at the same
+    addresses as the last step's need no new tables."""
+    torch, dev = torch_dev
+    opt, straight = fresh(torch, dev, bits), fresh(torch, dev, bits)
+    for step in range(3):
+        g = draws(torch, dev, 942, 1e-2, step)
+        straight.step({n: t.clone() for n, t in g.items()})
+        opt.step(g)
+        alive = [weakref.ref(t) for t in g.values()]
+        del g
+        assert not any(r() is not None for r in alive), step
+    equal = same(torch, everything(opt, {}), everything(straight, {}))
+    assert equal
+    held = draws(torch, dev, 942, 1e-2, 3)
+    opt.step(held)
+    B.timing_read()
+    B.timing_enable()
+    for step in range(4, 6):  # other tensor objects, the same memory, as a caching allocator gives them
+        opt.step({n: t.view(t.shape) for n, t in held.items()})
+    counts = B.timing_read()
+    B.timing_enable(False)
+    assert counts["adamw_multi"][1] == 2 and counts["grad_norm"][1] == 2
+    assert counts["tensor_plan"][1] == 0, counts["tensor_plan"]
+    # by hand, a step without gradients reads those given last, and needs some
+    with pytest.raises(ValueError, match="no gradients"):
+        opt._adamw.step(6)
+    with pytest.raises(ValueError, match="no gradients"):
+        opt._norm.measure(1.0)
+    with pytest.raises(ValueError, match="no gradients"):
+        opt._norm.scale_()

@@ -598,3 +598,34 @@ def test_small_second_moments_and_small_eps(torch_dev, bits, eps):
                 u1 = O8.decode(codes(opt.exp_avg_sq[i])) * top
                 assert (u1 >= lo * 0.87 - top * 2.0 ** -9).all() and (u1 <= hi * 1.13 + top * 2.0 ** -9).all(), (size, step)
         log(f"{bits} bits, eps {eps:.1e}, step {step}: largest update {max(float(np.abs(host(t)).max()) for t in w):.2e}")
+
+
+def test_gradients_changed_in_place_are_seen(torch_dev):
+    """The same tensor objects with another size or layout are checked again, and other
+    objects at the same addresses need no new table."""
+    torch, dev = torch_dev
+    g = [torch.zeros(1000, device=dev), torch.zeros(8, 4, device=dev)]
+    w = [torch.zeros(1000, device=dev), torch.zeros(8, 4, device=dev)]
+    opt, norm = muon.AdamWMulti(w, g), muon.GradNorm(g)
+    opt.step(0, grads=g)
+    B.timing_read()
+    B.timing_enable()
+    opt.step(1, grads=[t.view(t.shape) for t in g])
+    norm.set_grads([t.view(t.shape) for t in g])
+    plans = B.timing_read()["tensor_plan"][1]
+    B.timing_enable(False)
+    assert plans == 0
+    opt.set_grads(g)
+    g[0].resize_(500)
+    for call in (lambda: opt.step(2, grads=g), lambda: norm.set_grads(g)):
+        with pytest.raises(ValueError, match="1000 elements"):
+            call()
+    g[0].resize_(1000)
+    g[1].t_()
+    for call in (lambda: opt.step(2, grads=g), lambda: norm.set_grads(g)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    g[1].t_()
+    opt.step(2, grads=g)
+    with pytest.raises(TypeError):
+        opt.step(3, grads=[None, g[1]])
