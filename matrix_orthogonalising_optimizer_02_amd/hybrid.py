@@ -147,9 +147,23 @@ class HybridOptimizer:
         self.grad_norm = None
         self.step_count = 0
 
-    def step(self, grads: Dict[str, "object"], stream=None, update_rms=None):
+    def step(self, grads: Dict[str, "object"], stream=None, update_rms=None, counter=None, lr=None):
         """One step. What either half refuses is refused before anything is written: weights,
-        states, gradients and step_count are then as they were."""
+        states, gradients and step_count are then as they were.
+
+        counter, lr: AdamW's step number and learning rate on the device (AdamWMulti.step), for
+        steps that are captured into a graph. With the host's step_count a replay would repeat
+        the bias corrections of the captured step and, with 8-bit states, its rounding bits, and
+        rounding would no longer be unbiased. Every run of the step increases the counter (it is
+        left alone where AdamW has no elements).
+        Muon's schedule stays the host's: capture a whole cycle of period_k steps (or a graph for
+        each kind of step), and set step_count by the counter before state_dict()."""
+        if counter is not None and self.adamw_state_bits is None:
+            raise ValueError("a counter needs adamw_state_bits 8 or 32")
+        if isinstance(counter, int):
+            raise ValueError("a counter is a tensor on the device; otherwise set step_count")
+        if counter is None and lr is not None:
+            raise ValueError("lr as a tensor goes with a counter; otherwise set adamw_hp.lr")
         gm, ga = [grads[n] for n in self.muon_names], [grads[n] for n in self.adamw_names]
         muon = [self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names], gm
         if self.muon_names:
@@ -160,7 +174,7 @@ class HybridOptimizer:
                 self._adamw_step(ga, stream)
         else:
             try:
-                self._multi_step([grads[n] for n in self.names], gm, ga, stream)
+                self._multi_step([grads[n] for n in self.names], gm, ga, stream, counter, lr)
             finally:
                 for held in (self._adamw, self._norm, self._muon_norm):
                     if held is not None:
@@ -169,14 +183,14 @@ class HybridOptimizer:
             B.muon_step(*muon, self.step_count, self.muon_hp, self.workspace, stream, update_rms)
         self.step_count += 1
 
-    def _multi_step(self, g, gm, ga, stream):
+    def _multi_step(self, g, gm, ga, stream, counter, lr):
         """AdamW's half over all tensors at once, and the clipping of both."""
         if self.adamw_names:
-            self._adamw.check_hparams(self.step_count)
+            self._adamw.check_step(self.step_count if counter is None else counter, lr)
             self._adamw.set_grads(ga, stream)
         factor = self._clip(g, gm, stream) if self.max_grad_norm is not None and g else None
         if self.adamw_names:
-            self._adamw.step(self.step_count, factor, stream)
+            self._adamw.step(self.step_count if counter is None else counter, factor, stream, None, lr)
 
     def _adamw_step(self, g, stream):
         if self._adamw is None:

@@ -214,27 +214,33 @@ class AdamWMulti:
         if grads is not None:
             self.set_grads(grads, stream)
         _need_grads(self.grads)
-        torch, lib = B._torch(), B.load_library()
+        lib = B.load_library()
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
-        counted = isinstance(step, torch.Tensor)
-        if counted:
-            if step.dtype != torch.int64 or step.numel() != 1 or step.device != self.device:
-                raise ValueError(f"a step counter must be an int64 tensor of one element on {self.device}")
-        elif lr is not None:
-            raise ValueError("lr as a tensor goes with a step counter; otherwise set hp.lr")
-        rate = _scalar_ptr(lr, "lr", self.device)
+        counter, rate = self._scalars(step, lr)
         with B.device_and_stream(self.device, stream):
             handle = B.raw_stream(stream, self.device)
-            if counted:
-                rc = lib.adamw_multi_step_device(self._plan, self.hp, step.data_ptr(), rate, self.seed, scale, handle)
+            if counter is not None:
+                rc = lib.adamw_multi_step_device(self._plan, self.hp, counter, rate, self.seed, scale, handle)
             else:
                 rc = lib.adamw_multi_step(self._plan, self.hp, int(step), self.seed, scale, handle)
         B._check(rc, "adamw_multi_step")
 
-    def check_hparams(self, step: int = 0):
-        """Raises where step() would refuse hp or the step's number; enqueues nothing."""
-        rc = B.load_library().adamw_multi_step(self._empty, self.hp, int(step), self.seed, None, None)
+    def check_step(self, step=0, lr=None):
+        """Raises where step() would refuse hp, the step's number or counter, or lr; enqueues nothing."""
+        counter, _ = self._scalars(step, lr)
+        rc = B.load_library().adamw_multi_step(self._empty, self.hp, 0 if counter else int(step), self.seed, None, None)
         B._check(rc, "adamw_multi_step")
+
+    def _scalars(self, step, lr):
+        """(address of the step's counter, of its learning rate), None where they are the host's."""
+        torch = B._torch()
+        if not isinstance(step, torch.Tensor):
+            if lr is not None:
+                raise ValueError("lr as a tensor goes with a step counter; otherwise set hp.lr")
+            return None, None
+        if step.dtype != torch.int64 or step.numel() != 1 or step.device != self.device:
+            raise ValueError(f"a step counter must be an int64 tensor of one element on {self.device}")
+        return step.data_ptr(), _scalar_ptr(lr, "lr", self.device)
 
     def moments(self, i: int):
         """The fp32 values of parameter i's first and second moment, in its shape."""

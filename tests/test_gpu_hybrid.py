@@ -142,3 +142,83 @@ def test_gradients_are_not_kept_after_the_step(torch_dev, bits):
         opt._norm.measure(1.0)
     with pytest.raises(ValueError, match="no gradients"):
         opt._norm.scale_()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_captured_cycle_with_a_counter_on_the_device(torch_dev, bits):
+    """A whole Periodic cycle, three steps, in one graph with AdamW's counter and learning
+    rate on the device: every replay does the next three steps, as an eager loop does them
+    by number. Muon's half and AdamW's moments (with 8-bit states their rounding) to the
+    bit. AdamW's weights: the bias corrections, made in double on either side, may differ in
+    fp32's last place, so an update of at most 4 lr may by 4 u of itself, and W by its own
+    rounding, u of 0.25."""
+    torch, dev = torch_dev
+    period = 3
+
+    def make():
+        return fresh(torch, dev, bits, muon_hp=muon.default_hparams(period_k=period), seed=(3 << 32) + 1)
+
+    eager, counted = make(), make()
+    g = draws(torch, dev, 943, 1e-2)
+    fixed = [{n: torch.empty_like(t) for n, t in g.items()} for _ in range(period)]
+    counter, lr = torch.zeros(1, dtype=torch.int64, device=dev), torch.tensor([1e-4], device=dev)
+    static, own = ({n: torch.empty_like(t) for n, t in g.items()} for _ in range(2))
+
+    def cycle(opt, **more):
+        for s in range(period):
+            for n, t in static.items():
+                t.copy_(fixed[s][n])
+            opt.step(static, **more)
+
+    def load(base):
+        for s in range(period):
+            for n, t in draws(torch, dev, 943, 1e-2, base + s).items():
+                fixed[s][n].copy_(t)
+
+    def eager_cycle():
+        for s in range(period):
+            for n, t in own.items():
+                t.copy_(fixed[s][n])
+            eager.adamw_hp.lr = float(lr)
+            eager.step(own)
+
+    load(0)  # the first cycle eagerly, so that every table is written
+    cycle(counted, counter=counter, lr=lr)
+    eager_cycle()
+    torch.cuda.synchronize()
+    assert int(counter) == period
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        cycle(counted, counter=counter, lr=lr)
+    assert int(counter) == period  # nothing has run yet
+    done = period
+    for r in range(4):
+        load(done)
+        lr.fill_(1e-4 * (r + 1))
+        eager_cycle()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        done += period
+        assert int(counter) == done
+        a, b = eager._adamw, counted._adamw
+        assert same(torch, a.exp_avg + a.exp_avg_sq, b.exp_avg + b.exp_avg_sq), r
+        assert same(torch, list(eager.momenta.values()), list(counted.momenta.values())), r
+        assert torch.equal(eager.grad_norm, counted.grad_norm)
+        for n in eager.params:
+            if n in eager.muon_names:
+                assert torch.equal(eager.params[n], counted.params[n]), (r, n)
+            else:
+                off = float((eager.params[n] - counted.params[n]).abs().max())
+                assert off <= done * (4 * 2.0 ** -24 * 4 * 4e-4 + 2 * 2.0 ** -24 * 0.25), (r, n, off)
+        assert float(torch.randn(1 << 18, device=dev).sum()) != 0.0
+    with pytest.raises(ValueError, match="counter"):
+        counted.step(own, lr=lr)
+    with pytest.raises(ValueError, match="counter"):
+        counted.step(own, counter=torch.zeros(1, device=dev))
+    with pytest.raises(ValueError, match="counter"):
+        counted.step(own, counter=5)
+    plain = fresh(torch, dev, None)
+    with pytest.raises(ValueError, match="adamw_state_bits"):
+        plain.step(own, counter=counter)
