@@ -222,16 +222,43 @@ class HybridOptimizer:
         if self.adamw_state_bits is None:
             state["exp_avg"] = {n: t.clone() for n, t in self.exp_avg.items()}
             state["exp_avg_sq"] = {n: t.clone() for n, t in self.exp_avg_sq.items()}
+        elif self._adamw is None:
+            state["adamw"] = None
         else:
-            state["adamw"] = self._adamw.state_dict() if self._adamw is not None else None
+            state["adamw"] = {"names": list(self.adamw_names), **self._adamw.state_dict()}
         return state
 
     def load_state_dict(self, state):
+        """The saved states, by parameter name; nothing is changed where one does not fit. The
+        rounding bits of 8-bit states go by an AdamW parameter's position in this optimizer."""
         if (self.adamw_state_bits is None) != ("exp_avg" in state):
             raise ValueError("the saved AdamW states are of another kind than this optimizer's")
+        step = int(state["step"])
+        groups = [("momenta", self.momenta), ("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)]
+        for key, dst in groups:
+            for n, t in dst.items():
+                if state[key][n].shape != t.shape:
+                    raise ValueError(f"{key} of {n} has another shape")
         if self.adamw_state_bits is not None and self._adamw is not None:
-            self._adamw.load_state_dict(state["adamw"])
-        self.step_count = int(state["step"])
-        for key, dst in (("momenta", self.momenta), ("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
+            self._adamw.load_state_dict(self._by_name(state["adamw"]))  # checks all before it copies
+        self.step_count = step
+        for key, dst in groups:
             for n, t in dst.items():
                 t.copy_(state[key][n])
+
+    def _by_name(self, saved):
+        """AdamW's saved lists in this optimizer's order. Without names (as an earlier version
+        saved them) they are in that order already."""
+        if saved is None:
+            raise ValueError("the saved state has no AdamW parameters")
+        names = saved.get("names")
+        if names is None:
+            return saved
+        if sorted(names) != sorted(self.adamw_names):
+            raise ValueError("the saved AdamW states are those of other parameters")
+        at = {n: i for i, n in enumerate(names)}
+        lists = {k: v for k, v in saved.items() if isinstance(v, (list, tuple)) and k != "names"}
+        for k, v in lists.items():
+            if len(v) != len(names):
+                raise ValueError(f"one {k} per parameter")
+        return {**saved, **{k: [v[at[n]] for n in self.adamw_names] for k, v in lists.items()}}

@@ -259,13 +259,14 @@ class AdamWMulti:
     def load_state_dict(self, state):
         if state["state_bits"] != self.state_bits:
             raise ValueError(f"the saved states have {state['state_bits']} bits, these {self.state_bits}")
+        seed = int(state["seed"])
         for name in self._state_names:
             if len(state[name]) != self.n:
                 raise ValueError(f"one {name} per parameter")
             for dst, src in zip(getattr(self, name), state[name]):
                 if dst.shape != src.shape or dst.dtype != src.dtype:
                     raise ValueError(f"{name} does not fit the parameters")
-        self.seed = int(state["seed"])
+        self.seed = seed
         for name in self._state_names:
             for dst, src in zip(getattr(self, name), state[name]):
                 dst.copy_(src)
