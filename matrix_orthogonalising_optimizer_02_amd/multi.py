@@ -67,6 +67,16 @@ def _unchanged(grads, ptrs, numels, dtypes, plan):
         return False
 
 
+def _copy(arr):
+    return type(arr).from_buffer_copy(arr)
+
+
+def _next_plan(rc, new, old):
+    """The plan to go on with after a plan call: the new one, or the old one where the call was
+    refused before it wrote anything (a launch that failed leaves a plan that steps refuse)."""
+    return old if rc and not new.device else new
+
+
 def _need_grads(grads):
     if grads is None:
         raise ValueError("there are no gradients: give them first")
@@ -171,7 +181,8 @@ class AdamWMulti:
 
     def set_grads(self, grads, stream=None):
         """New gradient tensors. Their addresses are written to the table on `stream` where
-        one differs from before; steps that follow on the stream read them."""
+        one differs from before; steps that follow on the stream read them. Tensors that are
+        refused leave those given before."""
         torch = B._torch()
         grads = list(grads)
         if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
@@ -181,24 +192,21 @@ class AdamWMulti:
             raise ValueError("one gradient per parameter")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
         codes = B.dtype_codes()
-        same = self._plan.kind != 0
-        for d, g in zip(self._arr, grads):
-            ptr, code = g.data_ptr() or None, codes[g.dtype]
-            same = same and d.g == ptr and d.g_dtype == code
-            d.g, d.g_dtype = ptr, code
-        self.grads, self._ptrs, self._dtypes = grads, [g.data_ptr() for g in grads], [g.dtype for g in grads]
-        if same:
-            return
+        arr, ptrs, dtypes = _copy(self._arr), [g.data_ptr() for g in grads], [g.dtype for g in grads]
+        for d, ptr, dtype in zip(arr, ptrs, dtypes):
+            d.g, d.g_dtype = ptr or None, codes[dtype]
         lib = B.load_library()
-        self._plan.kind = 0  # no step with a table that was not written
         with B.device_and_stream(self.device, stream):
             if self._table is None:
                 need = ctypes.c_size_t(0)
-                B._check(lib.adamw_multi_plan_bytes(self._arr, self.n, need), "adamw_multi_plan_bytes")
+                B._check(lib.adamw_multi_plan_bytes(arr, self.n, need), "adamw_multi_plan_bytes")
                 self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
-            rc = lib.adamw_multi_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
+            plan = B.TensorPlan()
+            rc = lib.adamw_multi_plan(arr, self.n, self._table.data_ptr(), self._table.numel(), plan,
                                       B.raw_stream(stream, self.device))
+        self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "adamw_multi_plan")
+        self.grads, self._arr, self._ptrs, self._dtypes = grads, arr, ptrs, dtypes
 
     def release_grads(self):
         """Lets go of the gradient tensors: the next step needs some given first. Tensors at
@@ -304,26 +312,23 @@ class GradNorm:
         if len(grads) != self.n:
             raise ValueError(f"{self.n} gradients are expected")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
-        self._numels = [g.numel() for g in grads]
         codes = B.dtype_codes()
-        same = self._plan.kind != 0
-        for d, g in zip(self._arr, grads):
-            ptr, code = g.data_ptr() or None, codes[g.dtype]
-            same = same and d.g == ptr and d.dtype == code
-            d.g, d.numel, d.dtype = ptr, g.numel(), code
-        self.grads, self._ptrs, self._dtypes = grads, [g.data_ptr() for g in grads], [g.dtype for g in grads]
-        if same:
-            return
+        arr, ptrs, dtypes = _copy(self._arr), [g.data_ptr() for g in grads], [g.dtype for g in grads]
+        numels = [g.numel() for g in grads]
+        for d, ptr, numel, dtype in zip(arr, ptrs, numels, dtypes):
+            d.g, d.numel, d.dtype = ptr or None, numel, codes[dtype]
         lib = B.load_library()
-        self._plan.kind = 0
         with B.device_and_stream(self.device, stream):
             if self._table is None:
                 need = ctypes.c_size_t(0)
-                B._check(lib.grad_norm_plan_bytes(self._arr, self.n, need), "grad_norm_plan_bytes")
+                B._check(lib.grad_norm_plan_bytes(arr, self.n, need), "grad_norm_plan_bytes")
                 self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
-            rc = lib.grad_norm_plan(self._arr, self.n, self._table.data_ptr(), self._table.numel(), self._plan,
+            plan = B.TensorPlan()
+            rc = lib.grad_norm_plan(arr, self.n, self._table.data_ptr(), self._table.numel(), plan,
                                     B.raw_stream(stream, self.device))
+        self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "grad_norm_plan")
+        self.grads, self._arr, self._numels, self._ptrs, self._dtypes = grads, arr, numels, ptrs, dtypes
 
     def release_grads(self):
         """Lets go of the gradient tensors: the next call needs some given first. Tensors at

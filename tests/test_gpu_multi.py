@@ -629,3 +629,57 @@ def test_gradients_changed_in_place_are_seen(torch_dev):
     opt.step(2, grads=g)
     with pytest.raises(TypeError):
         opt.step(3, grads=[None, g[1]])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_refused_gradients_leave_those_given_before(torch_dev, bits):
+    """A list that set_grads or a step refuses (off 16 bytes, on a weight, within a capture)
+    changes nothing: the earlier gradients are kept, and steps and replays go on with them."""
+    torch, dev = torch_dev
+    shapes = [(1000,), (64, 9)]
+    flat = torch.zeros(1001, device=dev)
+    g = tensors(torch, dev, 760, WL.ROLE_G, shapes, 1e-3)
+    want = [t.clone() for t in g]
+
+    def fresh(grads):
+        w = tensors(torch, dev, 760, WL.ROLE_W, shapes, 0.02)
+        return w, muon.AdamWMulti(w, grads, state_bits=bits), muon.GradNorm(grads)
+
+    w1, straight, norm1 = fresh(want)
+    w2, opt, norm2 = fresh(g)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        norm2.measure(1.0)
+        opt.step(0, norm2.factor)
+    bad = [flat[1:], w2[0]]
+    other = [t.clone() for t in g]
+    del g
+    for step in range(3):
+        for first in bad:
+            with pytest.raises(B.MuonError):
+                opt.step(step, grads=[first, opt.grads[1]])
+        with pytest.raises(B.MuonError):
+            norm2.set_grads([other[0], other[0].view(-1)[:576].view(64, 9)])
+        with pytest.raises(ValueError):
+            norm2.set_grads(other[:1])
+        if step == 1:
+            second = torch.cuda.CUDAGraph()
+            with pytest.raises(B.MuonError, match="captured"):
+                with torch.cuda.graph(second, stream=side):
+                    opt.step(step, grads=other)
+            torch.cuda.synchronize()
+        straight.step(step, norm1.measure(1.0)[0][1:])
+        opt.step(step, norm2.measure(1.0)[0][1:])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(w1 + [norm1.total, norm1.norms], w2 + [norm2.total, norm2.norms])), step
+    norm1.measure(1.0)
+    straight.step(0, norm1.factor)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(w1, w2))
+    opt.step(4, grads=other)
+    straight.step(4)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(w1, w2))
