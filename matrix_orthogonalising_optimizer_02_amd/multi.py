@@ -67,6 +67,36 @@ def _unchanged(grads, ptrs, numels, dtypes, plan):
         return False
 
 
+def _moved(tensors, ptrs):
+    """Index of the first tensor that is no longer at its address, or None."""
+    now = list(map(B._torch().Tensor.data_ptr, tensors))
+    return None if now == ptrs else next(i for i, (a, b) in enumerate(zip(now, ptrs)) if a != b)
+
+
+class _Watch:
+    """Tensors (by list, in `parts`) whose addresses stand in a table, and those addresses."""
+
+    def __init__(self, parts):
+        self.parts = parts
+        self.tensors = [t for tensors in parts.values() for t in tensors]
+        self.data_ptr = B._torch().Tensor.data_ptr
+        self.ptrs = list(map(self.data_ptr, self.tensors))
+
+    def check(self):
+        if list(map(self.data_ptr, self.tensors)) == self.ptrs:
+            return
+        i = _moved(self.tensors, self.ptrs)
+        for name, tensors in self.parts.items():
+            if i < len(tensors):
+                raise ValueError(f"{name}[{i}] has other memory than when it was given")
+            i -= len(tensors)
+
+
+def _need_grads(grads):
+    if grads is None:
+        raise ValueError("there are no gradients: give them first")
+
+
 def _copy(arr):
     return type(arr).from_buffer_copy(arr)
 
@@ -75,11 +105,6 @@ def _next_plan(rc, new, old):
     """The plan to go on with after a plan call: the new one, or the old one where the call was
     refused before it wrote anything (a launch that failed leaves a plan that steps refuse)."""
     return old if rc and not new.device else new
-
-
-def _need_grads(grads):
-    if grads is None:
-        raise ValueError("there are no gradients: give them first")
 
 
 def _scalar_ptr(t, name, device):
@@ -102,7 +127,10 @@ class AdamWMulti:
     release_grads() lets go of them. Their addresses stand in a
     table on the device that is written when they change, which cannot be captured into a
     graph: give the gradients before a capture. Replayed steps read the table too, so new
-    gradients are new for them as well.
+    gradients are new for them as well. The parameters', copies' and states' addresses are
+    those of the construction: a step refuses parameters and copies that have got other
+    memory since (`p.data = ...`, a module moved or converted). Of a gradient the memory
+    that it had when it was given is kept and read.
     state_bits: 32, or 8 for moments in e4m3 with one scale for every 256 elements (a
     quarter of the memory), rounded stochastically from `seed`, the step and the position.
     copies: optional 16-bit tensors that receive the updated weights.
@@ -144,6 +172,11 @@ class AdamWMulti:
                 self.exp_avg_scale[i].data_ptr() or None if small else None,
                 self.exp_avg_sq_scale[i].data_ptr() or None if small else None, 0,
                 codes[c.dtype] if c is not None else 0, state_bits, lr_scales[i], wd_scales[i])
+        # The kernel writes to all of these. The first are looked at in every step; the states, whose
+        # memory is kept, where they are read or replaced by name.
+        self._fixed = _Watch({"params": self.params, **({"copies": self.copies} if self.copies is not None else {})})
+        self._states = _Watch({name: getattr(self, name) for name in self._state_names})
+        self._states.memory = [t.untyped_storage() for t in self._states.tensors]
         self._plan = B.TensorPlan()
         self._empty = B.TensorPlan()
         B._check(B.load_library().adamw_multi_plan(None, 0, None, 0, self._empty, None), "adamw_multi_plan")
@@ -186,11 +219,13 @@ class AdamWMulti:
         torch = B._torch()
         grads = list(grads)
         if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
-            self.grads = grads
+            if self.grads is None or not all(map(operator.is_, grads, self.grads)):
+                self._take(grads)
             return
         if len(grads) != self.n:
             raise ValueError("one gradient per parameter")
         _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
+        self._fixed.check()
         codes = B.dtype_codes()
         arr, ptrs, dtypes = _copy(self._arr), [g.data_ptr() for g in grads], [g.dtype for g in grads]
         for d, ptr, dtype in zip(arr, ptrs, dtypes):
@@ -206,12 +241,16 @@ class AdamWMulti:
                                       B.raw_stream(stream, self.device))
         self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "adamw_multi_plan")
-        self.grads, self._arr, self._ptrs, self._dtypes = grads, arr, ptrs, dtypes
+        self._arr, self._ptrs, self._dtypes = arr, ptrs, dtypes
+        self._take(grads)
+
+    def _take(self, grads):
+        self.grads, self._memory = grads, [g.untyped_storage() for g in grads]
 
     def release_grads(self):
         """Lets go of the gradient tensors: the next step needs some given first. Tensors at
         the same addresses then need no new table."""
-        self.grads = None
+        self.grads = self._memory = None
 
     def step(self, step, grad_scale=None, stream=None, grads=None, lr=None):
         """One step. step: the 0-based step number, or, for steps in a captured graph, a
@@ -222,6 +261,7 @@ class AdamWMulti:
         if grads is not None:
             self.set_grads(grads, stream)
         _need_grads(self.grads)
+        self._fixed.check()
         lib = B.load_library()
         scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
         counter, rate = self._scalars(step, lr)
@@ -234,7 +274,9 @@ class AdamWMulti:
         B._check(rc, "adamw_multi_step")
 
     def check_step(self, step=0, lr=None):
-        """Raises where step() would refuse hp, the step's number or counter, or lr; enqueues nothing."""
+        """Raises where step() would refuse the parameters, hp, the step's number or counter, or
+        lr; enqueues nothing."""
+        self._fixed.check()
         counter, _ = self._scalars(step, lr)
         rc = B.load_library().adamw_multi_step(self._empty, self.hp, 0 if counter else int(step), self.seed, None, None)
         B._check(rc, "adamw_multi_step")
@@ -252,6 +294,7 @@ class AdamWMulti:
 
     def moments(self, i: int):
         """The fp32 values of parameter i's first and second moment, in its shape."""
+        self._states.check()
         p = self.params[i]
         if self.state_bits == 32:
             return self.exp_avg[i].view(p.shape).clone(), self.exp_avg_sq[i].view(p.shape).clone()
@@ -261,10 +304,12 @@ class AdamWMulti:
         return out[0], out[1].square()
 
     def state_dict(self):
+        self._states.check()
         return {"state_bits": self.state_bits, "seed": self.seed,
                 **{name: [t.clone() for t in getattr(self, name)] for name in self._state_names}}
 
     def load_state_dict(self, state):
+        self._states.check()
         if state["state_bits"] != self.state_bits:
             raise ValueError(f"the saved states have {state['state_bits']} bits, these {self.state_bits}")
         seed = int(state["seed"])
@@ -283,7 +328,8 @@ class AdamWMulti:
 class GradNorm:
     """l2 norms of a list of gradients, their total and the clip factor, on the device.
 
-    The gradients' addresses are kept in a table, as AdamWMulti's (not within a capture).
+    The gradients' addresses are kept in a table, as AdamWMulti's (not within a capture);
+    scale_() refuses gradients that have got other memory than when they were given.
     `total` (float32 [2]: the norm, the factor) and `norms` (float32 [count]) belong to the
     object and are overwritten by every measure(); calls on one object must not overlap.
     """
@@ -307,7 +353,8 @@ class GradNorm:
         torch = B._torch()
         grads = list(grads)
         if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
-            self.grads = grads
+            if self.grads is None or not all(map(operator.is_, grads, self.grads)):
+                self._take(grads)
             return
         if len(grads) != self.n:
             raise ValueError(f"{self.n} gradients are expected")
@@ -328,12 +375,16 @@ class GradNorm:
                                     B.raw_stream(stream, self.device))
         self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "grad_norm_plan")
-        self.grads, self._arr, self._numels, self._ptrs, self._dtypes = grads, arr, numels, ptrs, dtypes
+        self._arr, self._numels, self._ptrs, self._dtypes = arr, numels, ptrs, dtypes
+        self._take(grads)
+
+    def _take(self, grads):
+        self.grads, self._memory = grads, [g.untyped_storage() for g in grads]
 
     def release_grads(self):
         """Lets go of the gradient tensors: the next call needs some given first. Tensors at
         the same addresses then need no new table."""
-        self.grads = None
+        self.grads = self._memory = None
 
     def measure(self, max_norm: float, stream=None):
         """(total, norms): total[0] the norm over all gradients, total[1] the factor
@@ -349,6 +400,9 @@ class GradNorm:
         """The gradients times `factor` in place (one-element float32 device tensor; by
         default the last measure()'s clip factor). Nothing is read or written where it is 1."""
         _need_grads(self.grads)
+        i = _moved(self.grads, self._ptrs)
+        if i is not None:
+            raise ValueError(f"grads[{i}] has other memory than when it was given")
         ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_scale(self._plan, ptr, B.raw_stream(stream, self.device))

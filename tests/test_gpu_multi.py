@@ -683,3 +683,39 @@ def test_refused_gradients_leave_those_given_before(torch_dev, bits):
     straight.step(4)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(w1, w2))
+
+
+def test_tensors_that_got_other_memory_are_refused(torch_dev):
+    """p.data = ... after the construction: a step would write where the tensor was."""
+    torch, dev = torch_dev
+    shapes = [(1000,), (64, 9)]
+    for bits in (8, 32):
+        w, g = tensors(torch, dev, 770, WL.ROLE_W, shapes, 0.02), tensors(torch, dev, 770, WL.ROLE_G, shapes, 1e-3)
+        copies = [t.bfloat16() for t in w]
+        opt, norm = muon.AdamWMulti(w, g, state_bits=bits, copies=copies), muon.GradNorm(g)
+        opt.step(0)
+        norm.measure(1.0)
+        saved = opt.state_dict()
+        for moved, calls in ((w[1], [lambda: opt.step(1), lambda: opt.step(1, grads=g), lambda: opt.check_step(1)]),
+                             (copies[0], [lambda: opt.step(1)]),
+                             (g[0], [lambda: norm.scale_()]),
+                             (opt.exp_avg[0], [opt.state_dict, lambda: opt.moments(0), lambda: opt.load_state_dict(saved)])):
+            old, kept = moved.data, [t.clone() for t in w + copies + opt.exp_avg]
+            new = old.clone()
+            moved.data = new
+            for call in calls:
+                with pytest.raises(ValueError, match="other memory"):
+                    call()
+            torch.cuda.synchronize()
+            moved.data = old
+            assert all(torch.equal(a, b) for a, b in zip([t.view(torch.uint8) for t in w + copies + opt.exp_avg],
+                                                         [t.view(torch.uint8) for t in kept]))
+        # a gradient's memory is the one that it had, and kept, until it is given again
+        first = norm.measure(1.0)[1].clone()
+        g[0].data = g[0].data * 3.0
+        junk = torch.full((1000,), float("nan"), device=dev)
+        assert torch.equal(norm.measure(1.0)[1], first)
+        norm.set_grads(g)
+        assert abs(float(norm.measure(1.0)[1][0] / first[0]) - 3.0) < 1e-5
+        opt.step(1, grads=g)
+        del junk

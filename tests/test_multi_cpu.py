@@ -180,3 +180,21 @@ def test_rounding_bits_are_spread_and_apart():
         assert abs(np.corrcoef(a, x)[0, 1]) < 5 / np.sqrt(n)
     far = O8.rounding_bits(123, 7, 0, np.array([5, 5 + (1 << 32)]))[0]
     assert far[0] != far[1]
+
+
+def test_moved_tensors_are_found():
+    import torch
+    from matrix_orthogonalising_optimizer_02_amd import multi
+    t = [torch.zeros(8) for _ in range(3)]
+    ptrs = [x.data_ptr() for x in t]
+    assert multi._moved(t, ptrs) is None and multi._moved([], []) is None
+    watch = multi._Watch({"params": t[:2], "copies": t[2:]})
+    watch.check()
+    for i, name in ((0, r"params\[0\]"), (1, r"params\[1\]"), (2, r"copies\[0\]")):
+        old = t[i].data
+        t[i].data = torch.ones(8)
+        assert multi._moved(t, ptrs) == i
+        with pytest.raises(ValueError, match=name + " has other memory"):
+            watch.check()
+        t[i].data = old
+        watch.check()
