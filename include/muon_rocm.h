@@ -399,7 +399,8 @@ int adamw_multi_plan(const adamw_tensor* tensors, int32_t count, void* device, s
                      void* stream);
 
 /* One step at 0-based step `step` over the plan's tensors: one launch.
- * grad_scale: DEVICE float (the clip factor of grad_norm, or one over a loss scale), NULL = 1.
+ * grad_scale: DEVICE float (the clip factor of grad_norm, or one over a loss scale), NULL = 1;
+ * outside the plan's w, copy, m, v and scales (not checked: the plan's addresses are on the device).
  * seed: of the stochastic rounding; without effect on 32-bit states. Two calls on one plan
  * at the same time race, as on the states themselves.
  * Errors: INVALID_ARG (as adamw_step, eps below 2^-126, a plan of another kind), ALIGN,
@@ -412,7 +413,8 @@ int adamw_multi_step(const tensor_plan* plan, const adamw_hparams* hp, int64_t s
  * (with it the bias corrections and the rounding bits of 8-bit states, which have to change
  * from step to step). counter: DEVICE int64, 8-byte aligned: the 0-based step, not below 0;
  * the call uses its value and then adds one, so that every plan needs its own; a plan without
- * elements launches nothing and leaves it. lr: DEVICE float, NULL = hp->lr. Two launches.
+ * elements launches nothing and leaves it. lr: DEVICE float, NULL = hp->lr; both outside the
+ * plan's tensors (not checked). Two launches.
  * Errors: as adamw_multi_step, INVALID_ARG for a NULL counter. */
 int adamw_multi_step_device(const tensor_plan* plan, const adamw_hparams* hp, int64_t* counter, const float* lr,
                             uint64_t seed, const float* grad_scale, void* stream);
@@ -439,13 +441,15 @@ int grad_norm_plan(const grad_tensor* grads, int32_t count, void* device, size_t
                    void* stream);
 
 /* total[0] = the norm over all of the plan's tensors, total[1] = the clip factor; norms[i] =
- * tensor i's norm, NULL = not wanted. DEVICE arrays of 2 and `count` floats. A NaN gradient
+ * tensor i's norm, NULL = not wanted. DEVICE arrays of 2 and `count` floats outside the
+ * plan's tensors (not checked). A NaN gradient
  * gives NaN for both, an infinite one an infinite norm and the factor 0. Two launches.
  * Errors: INVALID_ARG (NULL plan or total, another plan's kind, max_norm not > 0 and
  * finite), ALIGN, ALIAS (total and norms overlap each other or the table), HIP. */
 int grad_norm(const tensor_plan* plan, float max_norm, float* total, float* norms, void* stream);
 
-/* g <- factor g in place, rounded to g's type, for the plan's tensors; factor: DEVICE float.
+/* g <- factor g in place, rounded to g's type, for the plan's tensors; factor: DEVICE float
+ * outside these tensors (not checked).
  * Nothing is read or written where factor is 1. One launch. Errors: INVALID_ARG, ALIGN, HIP. */
 int grad_scale(const tensor_plan* plan, const float* factor, void* stream);
 

@@ -186,8 +186,8 @@ class HybridOptimizer:
     def _multi_step(self, g, gm, ga, stream, counter, lr):
         """AdamW's half over all tensors at once, and the clipping of both."""
         if self.adamw_names:
-            self._adamw.check_step(self.step_count if counter is None else counter, lr)
             self._adamw.set_grads(ga, stream)
+            self._adamw.check_step(self.step_count if counter is None else counter, lr)
         factor = self._clip(g, gm, stream) if self.max_grad_norm is not None and g else None
         if self.adamw_names:
             self._adamw.step(self.step_count if counter is None else counter, factor, stream, None, lr)

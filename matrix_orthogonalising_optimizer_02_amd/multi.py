@@ -7,6 +7,7 @@ gradients' norms and the clip factor that feeds it.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import operator
 from typing import Optional
@@ -92,6 +93,23 @@ class _Watch:
             i -= len(tensors)
 
 
+class _Spans:
+    """The bytes of tensors, as disjoint address ranges in order."""
+
+    def __init__(self, tensors):
+        self.starts, self.ends = [], []
+        for lo, hi in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors):
+            if self.ends and lo <= self.ends[-1]:
+                self.ends[-1] = max(self.ends[-1], hi)
+            elif hi > lo:
+                self.starts.append(lo)
+                self.ends.append(hi)
+
+    def touch(self, ptr, nbytes):
+        i = bisect.bisect_left(self.starts, ptr + nbytes) - 1
+        return i >= 0 and self.ends[i] > ptr
+
+
 def _need_grads(grads):
     if grads is None:
         raise ValueError("there are no gradients: give them first")
@@ -107,8 +125,8 @@ def _next_plan(rc, new, old):
     return old if rc and not new.device else new
 
 
-def _scalar_ptr(t, name, device):
-    """Device pointer of an optional one-element float32 tensor."""
+def _scalar_ptr(t, name, device, written):
+    """Device pointer of an optional one-element float32 tensor outside the spans that the call writes."""
     if t is None:
         return None
     torch = B._torch()
@@ -116,7 +134,10 @@ def _scalar_ptr(t, name, device):
         raise ValueError(f"{name} must be a float32 tensor of one element")
     if t.device != device:
         raise ValueError(f"{name} must live on {device}")
-    return t.data_ptr()
+    ptr = t.data_ptr()
+    if written.touch(ptr, 4):
+        raise ValueError(f"{name} lies within the tensors that the call writes")
+    return ptr
 
 
 class AdamWMulti:
@@ -176,12 +197,13 @@ class AdamWMulti:
         # memory is kept, where they are read or replaced by name.
         self._fixed = _Watch({"params": self.params, **({"copies": self.copies} if self.copies is not None else {})})
         self._states = _Watch({name: getattr(self, name) for name in self._state_names})
+        self._written = _Spans(self._fixed.tensors + self._states.tensors)
         self._states.memory = [t.untyped_storage() for t in self._states.tensors]
         self._plan = B.TensorPlan()
         self._empty = B.TensorPlan()
         B._check(B.load_library().adamw_multi_plan(None, 0, None, 0, self._empty, None), "adamw_multi_plan")
         self._table = None
-        self.grads = self._ptrs = self._dtypes = None
+        self.grads = self._ptrs = self._dtypes = self._read = None
         if grads is not None:
             self.set_grads(grads, stream)
 
@@ -241,7 +263,7 @@ class AdamWMulti:
                                       B.raw_stream(stream, self.device))
         self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "adamw_multi_plan")
-        self._arr, self._ptrs, self._dtypes = arr, ptrs, dtypes
+        self._arr, self._ptrs, self._dtypes, self._read = arr, ptrs, dtypes, None
         self._take(grads)
 
     def _take(self, grads):
@@ -250,7 +272,84 @@ class AdamWMulti:
     def release_grads(self):
         """Lets go of the gradient tensors: the next step needs some given first. Tensors at
         the same addresses then need no new table."""
-        self.grads = self._memory = None
+        self.grads = self._memory = self._read = None
+
+    def step(self, step, grad_scale=None, stream=None, grads=None, lr=None):
+        """One step. step: the 0-based step number, or, for steps in a captured graph, a
+        one-element int64 device tensor that holds it and is increased by the call, so each
+        AdamWMulti has its own (a number would stay as it was at the capture, and with it
+        the bias corrections and the rounding bits). grad_scale: optional one-element float32
+        device tensor. lr: with a counter, an optional one-element float32 device tensor in
+        place of hp.lr. None of the three may lie within what the step writes."""
+        if grads is not None:
+            self.set_grads(grads, stream)
+
+    def _make_states(self, states):
+        torch = B._torch()
+        small = self.state_bits == 8
+        dtype = torch.float8_e4m3fn if small else torch.float32
+        scales = [-(-k // STATE_BLOCK) for k in self._numels]
+        names = {"exp_avg": self._numels, "exp_avg_sq": self._numels}
+        if small:
+            names.update(exp_avg_scale=scales, exp_avg_sq_scale=scales)
+        for name, sizes in names.items():
+            kind = torch.float32 if name.endswith("scale") else dtype
+            if states is not None:
+                tensors = list(states[name])
+                if len(tensors) != self.n:
+                    raise ValueError(f"one {name} per parameter")
+                _check_list(tensors, name, self.device, (kind,), sizes)
+            else:
+                # one zeroed buffer, every tensor at a multiple of 256 bytes
+                size = torch.empty(0, dtype=kind).element_size()
+                starts, at = [], 0
+                for k in sizes:
+                    starts.append(at)
+                    at += -(-k * size // 256) * 256
+                flat = torch.zeros(at, dtype=torch.uint8, device=self.device)
+                tensors = [flat[a:a + k * size].view(kind) for a, k in zip(starts, sizes)]
+            setattr(self, name, tensors)
+        self._state_names = tuple(names)
+
+    def set_grads(self, grads, stream=None):
+        """New gradient tensors. Their addresses are written to the table on `stream` where
+        one differs from before; steps that follow on the stream read them. Tensors that are
+        refused leave those given before."""
+        torch = B._torch()
+        grads = list(grads)
+        if _unchanged(grads, self._ptrs, self._numels, self._dtypes, self._plan):
+            if self.grads is None or not all(map(operator.is_, grads, self.grads)):
+                self._take(grads)
+            return
+        if len(grads) != self.n:
+            raise ValueError("one gradient per parameter")
+        _check_list(grads, "grads", self.device, (torch.float32, torch.bfloat16, torch.float16), self._numels)
+        self._fixed.check()
+        codes = B.dtype_codes()
+        arr, ptrs, dtypes = _copy(self._arr), [g.data_ptr() for g in grads], [g.dtype for g in grads]
+        for d, ptr, dtype in zip(arr, ptrs, dtypes):
+            d.g, d.g_dtype = ptr or None, codes[dtype]
+        lib = B.load_library()
+        with B.device_and_stream(self.device, stream):
+            if self._table is None:
+                need = ctypes.c_size_t(0)
+                B._check(lib.adamw_multi_plan_bytes(arr, self.n, need), "adamw_multi_plan_bytes")
+                self._table = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+            plan = B.TensorPlan()
+            rc = lib.adamw_multi_plan(arr, self.n, self._table.data_ptr(), self._table.numel(), plan,
+                                      B.raw_stream(stream, self.device))
+        self._plan = _next_plan(rc, plan, self._plan)
+        B._check(rc, "adamw_multi_plan")
+        self._arr, self._ptrs, self._dtypes, self._read = arr, ptrs, dtypes, None
+        self._take(grads)
+
+    def _take(self, grads):
+        self.grads, self._memory = grads, [g.untyped_storage() for g in grads]
+
+    def release_grads(self):
+        """Lets go of the gradient tensors: the next step needs some given first. Tensors at
+        the same addresses then need no new table."""
+        self.grads = self._memory = self._read = None
 
     def step(self, step, grad_scale=None, stream=None, grads=None, lr=None):
         """One step. step: the 0-based step number, or, for steps in a captured graph, a
@@ -263,7 +362,7 @@ class AdamWMulti:
         _need_grads(self.grads)
         self._fixed.check()
         lib = B.load_library()
-        scale = _scalar_ptr(grad_scale, "grad_scale", self.device)
+        scale = _scalar_ptr(grad_scale, "grad_scale", self.device, self._written)
         counter, rate = self._scalars(step, lr)
         with B.device_and_stream(self.device, stream):
             handle = B.raw_stream(stream, self.device)
@@ -290,7 +389,12 @@ class AdamWMulti:
             return None, None
         if step.dtype != torch.int64 or step.numel() != 1 or step.device != self.device:
             raise ValueError(f"a step counter must be an int64 tensor of one element on {self.device}")
-        return step.data_ptr(), _scalar_ptr(lr, "lr", self.device)
+        ptr = step.data_ptr()
+        if self._read is None:
+            self._read = _Spans(self.grads or [])
+        if self._written.touch(ptr, 8) or self._read.touch(ptr, 8):
+            raise ValueError("the step counter lies within other tensors of the step")
+        return ptr, _scalar_ptr(lr, "lr", self.device, self._written)
 
     def moments(self, i: int):
         """The fp32 values of parameter i's first and second moment, in its shape."""
@@ -375,7 +479,7 @@ class GradNorm:
                                     B.raw_stream(stream, self.device))
         self._plan = _next_plan(rc, plan, self._plan)
         B._check(rc, "grad_norm_plan")
-        self._arr, self._numels, self._ptrs, self._dtypes = arr, numels, ptrs, dtypes
+        self._arr, self._numels, self._ptrs, self._dtypes, self._written = arr, numels, ptrs, dtypes, None
         self._take(grads)
 
     def _take(self, grads):
@@ -398,12 +502,15 @@ class GradNorm:
 
     def scale_(self, factor=None, stream=None):
         """The gradients times `factor` in place (one-element float32 device tensor; by
-        default the last measure()'s clip factor). Nothing is read or written where it is 1."""
+        default the last measure()'s clip factor; not an element of the gradients). Nothing is
+        read or written where it is 1."""
         _need_grads(self.grads)
         i = _moved(self.grads, self._ptrs)
         if i is not None:
             raise ValueError(f"grads[{i}] has other memory than when it was given")
-        ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device)
+        if self._written is None:
+            self._written = _Spans(self.grads)
+        ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device, self._written)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_scale(self._plan, ptr, B.raw_stream(stream, self.device))
         B._check(rc, "grad_scale")

@@ -719,3 +719,39 @@ def test_tensors_that_got_other_memory_are_refused(torch_dev):
         assert abs(float(norm.measure(1.0)[1][0] / first[0]) - 3.0) < 1e-5
         opt.step(1, grads=g)
         del junk
+
+
+def test_scalars_within_the_tensors_are_refused(torch_dev):
+    """A factor inside the gradients that it scales, or inside the weights, would be read by
+    some blocks before and by others after it is written; beside them is fine."""
+    torch, dev = torch_dev
+    flat = torch.ones(4096, device=dev)
+    g = [flat[:1000], flat[1024:2048]]
+    norm = muon.GradNorm(g)
+    norm.measure(1.0)
+    for i in (0, 999, 1024, 2047):
+        with pytest.raises(ValueError, match="within the tensors"):
+            norm.scale_(flat[i:i + 1])
+    torch.cuda.synchronize()
+    assert bool((flat == 1.0).all())
+    flat[1000] = 0.5
+    norm.scale_(flat[1000:1001])
+    assert bool((g[0] == 0.5).all()) and bool((g[1] == 0.5).all()) and float(flat[1001]) == 1.0 and float(flat[2048]) == 1.0
+    for bits in (8, 32):
+        w = [torch.ones(1000, device=dev), torch.ones(1, device=dev)]
+        gw = [torch.ones(1000, device=dev), torch.ones(1, device=dev)]
+        opt = muon.AdamWMulti(w, gw, state_bits=bits)
+        ok, count = torch.ones(1, device=dev), torch.zeros(1, dtype=torch.int64, device=dev)
+        wrong = [dict(grad_scale=w[1]), dict(grad_scale=w[0][7:8])]
+        wrong += [dict(grad_scale=opt.exp_avg_scale[0][2:3])] if bits == 8 else [dict(grad_scale=opt.exp_avg[0][3:4])]
+        for more in wrong:
+            with pytest.raises(ValueError, match="within the tensors"):
+                opt.step(0, **more)
+        for step, lr in ((gw[0].view(torch.int64)[3:4], None), (w[0].view(torch.int64)[0:1], None), (count, w[0][1:2])):
+            with pytest.raises(ValueError, match="within"):
+                opt.step(step, lr=lr)
+        torch.cuda.synchronize()
+        assert bool((w[0] == 1.0).all()) and bool((gw[0] == 1.0).all()) and int(count) == 0
+        opt.step(0, grad_scale=gw[1])  # a gradient is only read
+        opt.step(count, grad_scale=ok, lr=ok)
+        assert int(count) == 1
