@@ -124,6 +124,8 @@ def _param(t, name, cols, groups, x, dtypes):
     n = t.numel() // cols if cols else 1
     if groups is not None and n != groups:
         raise ValueError(f"{name} must have {groups} rows, as the weight")
+    if n > 1 and x.dim() > 2:
+        _check_leading(t, n, name, x)
     stride = cols
     if not t.is_contiguous():
         levels = _row_levels(t, name)
@@ -131,6 +133,18 @@ def _param(t, name, cols, groups, x, dtypes):
             raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
         stride = levels[0][1] if levels else cols
     return n, _pack_param(t.data_ptr(), stride)
+
+
+def _check_leading(t, n, name, x):
+    """t's n rows belong to x's leading dimensions, one or several of them in order."""
+    lead = list(t.shape[:-1])
+    while lead[-1] == 1:
+        lead.pop()
+    products = [1]
+    for size in x.shape[:-1]:
+        products.append(products[-1] * size)
+    if n not in products or (len(lead) > 1 and lead != list(x.shape[:len(lead)])):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} has no row for each of the leading dimensions of x, {tuple(x.shape)}")
 
 
 def _desc(x, rows, cols, weight, bias, kind, eps, weight_offset, inner):
@@ -161,7 +175,8 @@ def norm_forward(x, weight=None, bias=None, *, kind: str = "layer", eps: float =
 
     kind "rms" takes no mean away (mean is None). weight and bias: float32 or x's dtype,
     [cols] for all rows, or one row for each of `groups` equal runs of x's rows (adaLN's
-    scale and shift of each sample, e.g. [samples, cols], with weight_offset 1). x's rows
+    scale and shift of each sample, e.g. [samples, cols], with weight_offset 1); where x has
+    more than two dimensions, a run is what one or several leading ones number. x's rows
     may be strided (a slice of a fused projection). mean and rstd: float32 [rows], for
     norm_backward; neither is computed into memory with stats=False (both None then). out:
     receives y, and may be x.

@@ -210,3 +210,29 @@ def test_oracle_gradients_are_the_differences(kind):
             down = loss()
             arr[at] = keep
             assert abs((up - down) / 2e-6 - grad[at]) < 1e-7 * max(1.0, abs(grad[at])) + 1e-8
+
+
+def test_weight_rows_that_are_no_leading_dimensions():
+    """A row a sample, a row a row of x, or one for all; a row a token of every sample would
+    be taken for equal runs of rows, and is refused."""
+    import torch
+    x = torch.zeros(6, 10, 32)
+
+    def groups(*shape, x=x):
+        return norms._param(torch.zeros(*shape), "weight", shape[-1], None, x, (torch.float32,))[0]
+
+    assert groups(32) == groups(1, 32) == groups(1, 1, 32) == 1
+    assert groups(6, 32) == groups(6, 1, 32) == groups(6, 1, 1, 32) == 6
+    assert groups(60, 32) == groups(6, 10, 32) == groups(60, 1, 32) == 60
+    for bad in ((10, 32), (1, 10, 32), (12, 32), (3, 32), (2, 32), (3, 2, 32), (10, 6, 32), (6, 2, 32), (30, 1, 32)):
+        with pytest.raises(ValueError, match="leading dimensions"):
+            groups(*bad)
+    square = torch.zeros(6, 6, 32)
+    assert groups(6, 32, x=square) == 6  # a row a sample
+    with pytest.raises(ValueError, match="leading dimensions"):
+        groups(1, 6, 32, x=square)
+    four = torch.zeros(2, 3, 10, 32)
+    assert groups(2, 32, x=four) == 2 and groups(6, 32, x=four) == groups(2, 3, 32, x=four) == groups(2, 3, 1, 32, x=four) == 6
+    assert groups(10, 32, x=torch.zeros(1, 10, 32)) == groups(1, 10, 32, x=torch.zeros(1, 10, 32)) == 10
+    # rows that have no dimensions of their own: equal runs, as many as divide them
+    assert groups(4, 32, x=torch.zeros(60, 32)) == groups(4, 1, 32, x=torch.zeros(60, 32)) == 4
