@@ -49,9 +49,10 @@ struct Hyper {
 
 // sqrt(v): r = 1/sqrt(v) from the hardware (1 ulp), s = v r, and one Newton step on s
 // whose residual is exact; with the factor below twelve operations where sqrtf has about
-// sixteen. The same bits as sqrtf on 3e8 values between 2^-97 and 2^127. Nearer to 2^-126
-// the residual loses digits, and the hardware's root takes no number below it: a v below
-// 2^-96 is multiplied by 2^64 first and its root by 2^-32 after, both exact.
+// sixteen. The same bits as sqrtf on all values below 2^-93 and 3e8 up to 2^127. Nearer to
+// 2^-126 the unscaled residual would lose digits, and the hardware's root takes no number
+// below it: a v below 2^-96 is multiplied by 2^64 first and its root by 2^-32 after, both
+// exact (8-bit states, 177 M elements: 521.7 us; 520 us without).
 __device__ __forceinline__ float root(float v) {
     const bool small = v < 0x1p-96f;
     const float x = v * (small ? 0x1p64f : 1.f);

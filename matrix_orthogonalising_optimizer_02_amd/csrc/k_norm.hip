@@ -666,9 +666,11 @@ hipError_t launch_type(bool rms, int dtype, const NormPlan& p, const NormArgs& a
 // 42 us with one vector a lane and 10 waves a row, 31 us with 40 waves a unit). Backward: one
 // vector of 16-bit elements up to 1024 vectors a row (so that a lane's eight columns leave
 // registers for two rows in advance), two of fp32 from 129 vectors on, blocks of 8 waves or
-// one row, and about 10 waves a unit: every block's partial sums are written and read once
-// more, so that fewer blocks win ([8192, 5120] bf16 52.9 us; 58 us with 20 waves, 66 us
-// with 30).
+// one row, and as many whole blocks a unit as 10 waves hold, one at least: 10 waves where a
+// row takes 10, 8 for rows that share a block of 8, 6 for rows of 6 (fp32 of 1153 columns).
+// Every block's partial sums are written and read once more, so that fewer blocks win
+// ([8192, 5120] bf16 52.9 us; 58 us with 20 waves, 66 us with 30; other widths were not
+// measured with more).
 constexpr int kForwardVectors = 256, kForwardBlockWaves = 4, kForwardWaves = 24;
 constexpr int kBackwardVectors = 1024, kBackwardVectors32 = 128, kBackwardBlockWaves = 8, kBackwardWaves = 10;
 constexpr int kComputeUnits = 256;

@@ -337,7 +337,9 @@ def _autograd_function():
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """norm_forward's y for torch.autograd: affine with weight and bias of [cols], adaLN
     with one row a sample and weight_offset 1, plain without either. To capture a backward
-    pass into a HIP graph, call norm_forward and norm_backward themselves."""
+    pass into a HIP graph, call norm_forward and norm_backward themselves: while an eager
+    graph of the same leaves lives, a capture of autograd's backward pass waits for that
+    graph's stream, which a capture does not allow, and torch ends the process."""
     return _autograd_function().apply(x, weight, bias, "layer", eps, weight_offset)
 
 
