@@ -94,16 +94,20 @@ class _Watch:
 
 
 class _Spans:
-    """The bytes of tensors, as disjoint address ranges in order."""
+    """The bytes at ptrs, as disjoint address ranges in order."""
 
-    def __init__(self, tensors):
+    def __init__(self, ptrs, sizes):
         self.starts, self.ends = [], []
-        for lo, hi in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors):
-            if self.ends and lo <= self.ends[-1]:
-                self.ends[-1] = max(self.ends[-1], hi)
-            elif hi > lo:
-                self.starts.append(lo)
-                self.ends.append(hi)
+        last = 0
+        for lo, size in sorted(zip(ptrs, sizes)):
+            hi = lo + size
+            if lo > last:
+                if size:
+                    self.starts.append(lo)
+                    self.ends.append(hi)
+                    last = hi
+            elif hi > last:
+                self.ends[-1] = last = hi
 
     def touch(self, ptr, nbytes):
         i = bisect.bisect_left(self.starts, ptr + nbytes) - 1
@@ -126,9 +130,7 @@ def _next_plan(rc, new, old):
 
 
 def _scalar_ptr(t, name, device, written):
-    """Device pointer of an optional one-element float32 tensor outside the spans that the call writes."""
-    if t is None:
-        return None
+    """Device pointer of a one-element float32 tensor outside the spans that the call writes."""
     torch = B._torch()
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != 1:
         raise ValueError(f"{name} must be a float32 tensor of one element")
@@ -197,8 +199,12 @@ class AdamWMulti:
         # memory is kept, where they are read or replaced by name.
         self._fixed = _Watch({"params": self.params, **({"copies": self.copies} if self.copies is not None else {})})
         self._states = _Watch({name: getattr(self, name) for name in self._state_names})
-        self._written = _Spans(self._fixed.tensors + self._states.tensors)
-        self._states.memory = [t.untyped_storage() for t in self._states.tensors]
+        sizes = [4 * k for k in self._numels] + [2 * k for k in self._numels if self.copies is not None]
+        sizes += [k if small else 4 * k for k in self._numels] * 2
+        sizes += [4 * -(-k // STATE_BLOCK) for k in self._numels if small] * 2
+        self._written = _Spans(self._fixed.ptrs + self._states.ptrs, sizes)
+        lists = self._states.parts.values()  # own states: a list has one memory
+        self._states.memory = [t.untyped_storage() for ts in lists for t in (ts if states is not None else ts[:1])]
         self._plan = B.TensorPlan()
         self._empty = B.TensorPlan()
         B._check(B.load_library().adamw_multi_plan(None, 0, None, 0, self._empty, None), "adamw_multi_plan")
@@ -362,7 +368,7 @@ class AdamWMulti:
         _need_grads(self.grads)
         self._fixed.check()
         lib = B.load_library()
-        scale = _scalar_ptr(grad_scale, "grad_scale", self.device, self._written)
+        scale = None if grad_scale is None else _scalar_ptr(grad_scale, "grad_scale", self.device, self._written)
         counter, rate = self._scalars(step, lr)
         with B.device_and_stream(self.device, stream):
             handle = B.raw_stream(stream, self.device)
@@ -390,11 +396,11 @@ class AdamWMulti:
         if step.dtype != torch.int64 or step.numel() != 1 or step.device != self.device:
             raise ValueError(f"a step counter must be an int64 tensor of one element on {self.device}")
         ptr = step.data_ptr()
-        if self._read is None:
-            self._read = _Spans(self.grads or [])
-        if self._written.touch(ptr, 8) or self._read.touch(ptr, 8):
+        if self._read is None and self.grads is not None:
+            self._read = _Spans(self._ptrs, [n * g.element_size() for n, g in zip(self._numels, self.grads)])
+        if self._written.touch(ptr, 8) or (self._read is not None and self._read.touch(ptr, 8)):
             raise ValueError("the step counter lies within other tensors of the step")
-        return ptr, _scalar_ptr(lr, "lr", self.device, self._written)
+        return ptr, None if lr is None else _scalar_ptr(lr, "lr", self.device, self._written)
 
     def moments(self, i: int):
         """The fp32 values of parameter i's first and second moment, in its shape."""
@@ -509,7 +515,7 @@ class GradNorm:
         if i is not None:
             raise ValueError(f"grads[{i}] has other memory than when it was given")
         if self._written is None:
-            self._written = _Spans(self.grads)
+            self._written = _Spans(self._ptrs, [n * g.element_size() for n, g in zip(self._numels, self.grads)])
         ptr = _scalar_ptr(self.factor if factor is None else factor, "factor", self.device, self._written)
         with B.device_and_stream(self.device, stream):
             rc = B.load_library().grad_scale(self._plan, ptr, B.raw_stream(stream, self.device))

@@ -206,11 +206,12 @@ def test_spans_of_tensors():
     from matrix_orthogonalising_optimizer_02_amd import multi
     base = torch.zeros(100)
     at = base.data_ptr()
-    s = multi._Spans([base[60:80], base[10:20], base[20:30], base[15:18], base[50:50]])
+    parts = [base[60:80], base[10:20], base[20:30], base[15:18], base[50:50], base[:0]]
+    s = multi._Spans([t.data_ptr() for t in parts], [4 * t.numel() for t in parts])
     inside = [i for i in range(100) if s.touch(at + 4 * i, 4)]
     assert inside == list(range(10, 30)) + list(range(60, 80))
     assert s.touch(at + 36, 8) and not s.touch(at + 32, 8)  # an 8-byte counter across the edge
     assert s.touch(at + 4 * 29, 8) and not s.touch(at + 120, 8)
     assert s.touch(at + 38, 4) and not s.touch(at + 36, 4)
-    assert not multi._Spans([]).touch(at, 4)
+    assert not multi._Spans([], []).touch(at, 4) and not multi._Spans([0, 0], [0, 0]).touch(at, 4)
     assert s.touch(at, 400)
