@@ -318,6 +318,9 @@ void adamw_default_hparams(adamw_hparams* hp);
 int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step,
                void* stream);
 
+/* adamw_step's checks alone, as muon_step_check's. Host only. */
+int adamw_step_check(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step);
+
 /* ---- Many tensors in one launch ------------------------------------------------------
  * The hybrid optimizer's AdamW side has hundreds of small tensors (238 in the 15B-scale
  * model). The calls below read their descriptors from a table in device memory that a

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -35,7 +36,7 @@ KCLASS_NAMES = ("cast", "frob", "gram", "poly", "apply", "apply_final", "rownorm
 EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_default_hparams",
             "muon_workspace_bytes", "ns5_plan", "muon_step", "muon_step_check", "ns5_batched", "rownorm_update",
             "rownorm_update_noalloc",
-            "adamw_default_hparams", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy",
+            "adamw_default_hparams", "adamw_step", "adamw_step_check", "svd_entropy_workspace_bytes", "svd_entropy",
             "rownorm_shard_workspace_bytes", "rownorm_shard_colsq", "rownorm_shard_apply",
             "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
             "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step", "adamw_multi_step_device",
@@ -147,6 +148,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.rownorm_update_noalloc.argtypes = [ctypes.POINTER(MuonMatrix), i32, ctypes.POINTER(MuonHParams), vp, vp]
     lib.adamw_default_hparams.argtypes = [ctypes.POINTER(AdamWHParams)]
     lib.adamw_default_hparams.restype = None
+    lib.adamw_step_check.argtypes = [ctypes.POINTER(AdamWParam), i32, ctypes.POINTER(AdamWHParams), i64]
     lib.adamw_step.argtypes = [ctypes.POINTER(AdamWParam), i32, ctypes.POINTER(AdamWHParams), i64, vp]
     lib.svd_entropy_workspace_bytes.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                                 i32, ctypes.POINTER(ctypes.c_size_t)]
@@ -175,7 +177,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
     lib.muon_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
     for name in ("muon_step", "muon_step_check", "ns5_batched", "rownorm_update", "rownorm_update_noalloc", "muon_workspace_bytes",
-                 "ns5_plan", "adamw_step", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
+                 "ns5_plan", "adamw_step", "adamw_step_check", "svd_entropy_workspace_bytes", "svd_entropy", "rownorm_shard_workspace_bytes",
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
                  "adamw_multi_step_device", "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
@@ -375,6 +377,26 @@ def _monitor_ptr(update_rms, count):
     return ctypes.c_void_p(update_rms.data_ptr() or None)
 
 
+class MuonCall:
+    """muon_step's arguments, checked and converted once: check() raises what the library would
+    refuse and enqueues nothing, run() is the step."""
+
+    def __init__(self, weights, momenta, grads, step: int, hp: Optional[MuonHParams] = None, workspace=None, stream=None,
+                 update_rms=None):
+        hp = hp or default_hparams()
+        arr = _matrices(weights, momenta, grads)
+        dev = weights[0].device if weights else None
+        ws, wsb, self._owner = _ws(workspace, [tuple(w.shape) for w in weights], dev, stream)
+        self._args = (arr, len(weights), ctypes.byref(hp), int(step), ws, wsb, _monitor_ptr(update_rms, len(weights)))
+        self._stream = _stream_handle(stream, dev)
+
+    def check(self):
+        _check(load_library().muon_step_check(*self._args), "muon_step")
+
+    def run(self):
+        _check(load_library().muon_step(*self._args, self._stream), "muon_step")
+
+
 def muon_step(weights, momenta, grads, step: int, hp: Optional[MuonHParams] = None,
               workspace=None, stream=None, update_rms=None):
     """One Periodic Row-wise Muon step (refresh iff step % period_k == 0), in place.
@@ -382,22 +404,7 @@ def muon_step(weights, momenta, grads, step: int, hp: Optional[MuonHParams] = No
     update_rms: optional float32 device tensor [len(weights)] that receives each
     matrix's update RMS (RMS of the scaled direction, before lr and weight decay).
     """
-    hp = hp or default_hparams()
-    arr = _matrices(weights, momenta, grads)
-    dev = weights[0].device if weights else None
-    ws, wsb, _owner = _ws(workspace, [tuple(w.shape) for w in weights], dev, stream)
-    rc = load_library().muon_step(arr, len(weights), ctypes.byref(hp), int(step), ws, wsb,
-                                  _monitor_ptr(update_rms, len(weights)), _stream_handle(stream, dev))
-    _check(rc, "muon_step")
-
-
-def muon_step_check(weights, momenta, grads, step: int, hp: MuonHParams, workspace, update_rms=None):
-    """Raises what muon_step would refuse these arguments with; enqueues nothing."""
-    arr = _matrices(weights, momenta, grads)
-    rc = load_library().muon_step_check(arr, len(weights), ctypes.byref(hp), int(step),
-                                        ctypes.c_void_p(workspace.data_ptr()), ctypes.c_size_t(workspace.numel()),
-                                        _monitor_ptr(update_rms, len(weights)))
-    _check(rc, "muon_step")
+    MuonCall(weights, momenta, grads, step, hp, workspace, stream, update_rms).run()
 
 
 def rownorm_update(weights, momenta, grads, hp: Optional[MuonHParams] = None, workspace=None,
@@ -473,6 +480,20 @@ def _check_flat(t, name):
         raise ValueError(f"{name} must live on a GPU")
 
 
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
+def plainly_right(tensors, dtypes, device):
+    """Whether all are contiguous tensors of one of dtypes on a GPU, `device`: the common case of a
+    long list in a quarter of the time that checking one by one for a message takes."""
+    t = _torch().Tensor
+    try:
+        return all(map(t.is_contiguous, tensors)) and dtypes.issuperset(map(_dtype, tensors)) \
+            and all(i == device.index for i in map(t.get_device, tensors))
+    except (TypeError, AttributeError):  # not tensors
+        return False
+
+
 class AdamWGroup:
     """Tensors for repeated AdamW steps, with the C descriptor array built once.
 
@@ -496,16 +517,23 @@ class AdamWGroup:
                                      v.data_ptr() or None, g.data_ptr() or None)
         self.n = n
         self.device = params[0].device if params else None
+        self.shapes = [w.shape for w in params]
 
     def set_grads(self, grads):
         if len(grads) != self.n:
             raise ValueError("one gradient per parameter")
-        for i, (g, w) in enumerate(zip(grads, self.tensors[0])):
-            _check_flat(g, f"grad[{i}]")
-            if g.shape != w.shape:
-                raise ValueError(f"shape mismatch at index {i}")
-            self.arr[i].g = g.data_ptr() or None
+        if not (plainly_right(grads, {_torch().float32}, self.device) and list(map(_shape, grads)) == self.shapes):
+            for i, (g, w) in enumerate(zip(grads, self.tensors[0])):
+                _check_flat(g, f"grad[{i}]")
+                if g.shape != w.shape:
+                    raise ValueError(f"shape mismatch at index {i}")
+        for d, ptr in zip(self.arr, map(_torch().Tensor.data_ptr, grads)):
+            d.g = ptr or None
         self.tensors = (self.tensors[0], list(grads), self.tensors[2], self.tensors[3])
+
+    def check_step(self, step: int):
+        """Raises what step() would refuse the present tensors and hp with; enqueues nothing."""
+        _check(load_library().adamw_step_check(self.arr, self.n, ctypes.byref(self.hp), int(step)), "adamw_step")
 
     def step(self, step: int, stream=None, grads=None):
         if grads is not None:

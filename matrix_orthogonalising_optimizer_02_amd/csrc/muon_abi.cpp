@@ -1418,9 +1418,8 @@ MUON_API void adamw_default_hparams(adamw_hparams* hp) {
     hp->weight_decay = 0.1f;
 }
 
-MUON_API int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step,
-                        void* stream) {
-    g_last_error.clear();
+// Every check of an AdamW step.
+static int check_adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step) {
     if (!hp) return fail(MUON_ERR_INVALID_ARG, "hparams is NULL");
     if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
         return fail(MUON_ERR_INVALID_ARG, "lr and weight_decay must be finite");
@@ -1445,7 +1444,17 @@ MUON_API int adamw_step(const adamw_param* params, int32_t count, const adamw_hp
         ranges.push_back({reinterpret_cast<uintptr_t>(p.v), reinterpret_cast<uintptr_t>(p.v) + bytes, true});
         ranges.push_back({reinterpret_cast<uintptr_t>(p.g), reinterpret_cast<uintptr_t>(p.g) + bytes, false});
     }
-    int rc = check_overlaps(ranges);
+    return check_overlaps(ranges);
+}
+
+MUON_API int adamw_step_check(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step) {
+    return guarded([&]() -> int { return check_adamw_step(params, count, hp, step); });
+}
+
+MUON_API int adamw_step(const adamw_param* params, int32_t count, const adamw_hparams* hp, int64_t step,
+                        void* stream) {
+    g_last_error.clear();
+    int rc = check_adamw_step(params, count, hp, step);
     if (rc) return rc;
     // bias corrections in double on the host (t = step + 1)
     const double t = double(step) + 1.0;

@@ -160,47 +160,48 @@ class HybridOptimizer:
         each kind of step), and set step_count by the counter before state_dict()."""
         if counter is not None and self.adamw_state_bits is None:
             raise ValueError("a counter needs adamw_state_bits 8 or 32")
-        if isinstance(counter, int):
+        if counter is not None and not isinstance(counter, B._torch().Tensor):
             raise ValueError("a counter is a tensor on the device; otherwise set step_count")
         if counter is None and lr is not None:
             raise ValueError("lr as a tensor goes with a counter; otherwise set adamw_hp.lr")
         gm, ga = [grads[n] for n in self.muon_names], [grads[n] for n in self.adamw_names]
-        muon = [self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names], gm
-        if self.muon_names:
-            B.muon_step_check(*muon, self.step_count, self.muon_hp, self.workspace, update_rms)
-        if self.adamw_state_bits is None:
-            # adamw_step checks all of its tensors before its first launch, so it goes first
+        at, factor = self.step_count if counter is None else counter, None
+        try:
             if self.adamw_names:
-                self._adamw_step(ga, stream)
-        else:
-            try:
-                self._multi_step([grads[n] for n in self.names], gm, ga, stream, counter, lr)
-            finally:
+                self._check_adamw(ga, stream, at, lr)
+            # muon_step checks all of its arguments before its first launch
+            muon = B.MuonCall([self.params[n] for n in self.muon_names], [self.momenta[n] for n in self.muon_names], gm,
+                              self.step_count, self.muon_hp, self.workspace, stream, update_rms) if gm else None
+            if self.max_grad_norm is not None and self.names:
+                if gm:
+                    muon.check()
+                factor = self._clip([grads[n] for n in self.names], gm, stream)
+            if gm:
+                muon.run()
+            if self.adamw_names and self.adamw_state_bits is None:
+                self._adamw.step(self.step_count, stream)
+            elif self.adamw_names:
+                self._adamw.step(at, factor, stream, None, lr)
+        finally:
+            if self.adamw_state_bits is not None:
                 for held in (self._adamw, self._norm, self._muon_norm):
                     if held is not None:
                         held.release_grads()
-        if self.muon_names:
-            B.muon_step(*muon, self.step_count, self.muon_hp, self.workspace, stream, update_rms)
         self.step_count += 1
 
-    def _multi_step(self, g, gm, ga, stream, counter, lr):
-        """AdamW's half over all tensors at once, and the clipping of both."""
-        if self.adamw_names:
-            self._adamw.set_grads(ga, stream)
-            self._adamw.check_step(self.step_count if counter is None else counter, lr)
-        factor = self._clip(g, gm, stream) if self.max_grad_norm is not None and g else None
-        if self.adamw_names:
-            self._adamw.step(self.step_count if counter is None else counter, factor, stream, None, lr)
-
-    def _adamw_step(self, g, stream):
+    def _check_adamw(self, g, stream, at, lr):
+        """Gives AdamW its gradients; all that its step refuses is refused here."""
+        if self.adamw_state_bits is not None:
+            self._adamw.set_grads(g, stream)
+            self._adamw.check_step(at, lr)
+            return
         if self._adamw is None:
             self._adamw = B.AdamWGroup([self.params[n] for n in self.adamw_names], g,
                                        [self.exp_avg[n] for n in self.adamw_names],
                                        [self.exp_avg_sq[n] for n in self.adamw_names], self.adamw_hp)
-            self._adamw.step(self.step_count, stream)
-        else:
-            same = all(a is b for a, b in zip(g, self._adamw.tensors[1]))
-            self._adamw.step(self.step_count, stream, None if same else g)
+        elif not all(a is b for a, b in zip(g, self._adamw.tensors[1])):
+            self._adamw.set_grads(g)
+        self._adamw.check_step(at)
 
     def _clip(self, g, gm, stream):
         """Measures all gradients, scales Muon's; the factor for AdamW's (device tensor)."""

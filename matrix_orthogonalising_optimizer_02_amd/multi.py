@@ -19,6 +19,9 @@ STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
 
 def _check_list(tensors, name, device=None, dtypes=None, numels=None):
     torch = B._torch()
+    if device is not None and device.type == "cuda" and dtypes is not None and B.plainly_right(tensors, set(dtypes), device) \
+            and (numels is None or list(map(torch.Tensor.numel, tensors)) == numels):
+        return
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")

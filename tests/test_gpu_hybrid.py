@@ -301,3 +301,16 @@ def test_a_refused_checkpoint_changes_nothing(torch_dev, bits):
     if bits is not None:  # saved without names, as an earlier version did: by position
         opt.load_state_dict(dict(good, adamw=without(good["adamw"], "names")))
         assert same(torch, opt._adamw.exp_avg_sq, other._adamw.exp_avg_sq)
+
+
+def test_a_refused_list_leaves_the_group_its_gradients(torch_dev):
+    """AdamWGroup: a list that is refused half way through is not taken up in part."""
+    torch, dev = torch_dev
+    w, g = [torch.zeros(100, device=dev) for _ in range(2)], [torch.full((100,), v, device=dev) for v in (1.0, 2.0)]
+    m, v = [torch.zeros_like(t) for t in w], [torch.zeros_like(t) for t in w]
+    group = B.AdamWGroup(w, g, m, v)
+    with pytest.raises(ValueError, match="shape"):
+        group.step(0, grads=[torch.full((100,), -5.0, device=dev), torch.zeros(99, device=dev)])
+    group.step(0)
+    torch.cuda.synchronize()
+    assert float(m[0][0]) > 0 and float(m[1][0]) == pytest.approx(2.0 * float(m[0][0]))

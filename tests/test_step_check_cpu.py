@@ -60,3 +60,27 @@ def test_the_check_passes_what_is_whole(lib):  # noqa: F811
     assert lib.muon_workspace_bytes(*shape, 1, need) == B.MUON_OK
     assert both(lib, [matrix(0)], bytes_=need.value)[0] == B.MUON_OK
     assert both(lib, [matrix(0)], bytes_=need.value - 1)[0] == B.MUON_ERR_WORKSPACE
+
+
+def param(i=0, **over):
+    p = BASE + 8 * i * GIB
+    f = dict(numel=1000, w=p, m=p + GIB, v=p + 2 * GIB, g=p + 3 * GIB)
+    f.update(over)
+    return B.AdamWParam(*f.values())
+
+
+@fake_only
+def test_the_adamw_check_refuses_what_its_step_refuses(lib):  # noqa: F811
+    hp = B.adamw_default_hparams()
+    ok = (B.AdamWParam * 3)(param(0), param(1, numel=0), param(2))
+    assert lib.adamw_step_check(ok, 3, hp, 0) == B.MUON_OK and lib.adamw_step_check(None, 0, hp, 0) == B.MUON_OK
+    for over, status in ((dict(numel=-1), B.MUON_ERR_INVALID_ARG), (dict(g=None), B.MUON_ERR_INVALID_ARG),
+                         (dict(g=BASE + 3 * GIB + 4), B.MUON_ERR_ALIGN), (dict(v=BASE + GIB), B.MUON_ERR_ALIAS),
+                         (dict(g=BASE + 16 * GIB), B.MUON_ERR_ALIAS), (dict(numel=(1 << 40) + 1), B.MUON_ERR_TOO_LARGE)):
+        arr = (B.AdamWParam * 2)(param(2), param(0, **over))
+        assert lib.adamw_step_check(arr, 2, hp, 0) == status == lib.adamw_step(arr, 2, hp, 0, None), over
+    for over in (dict(beta1=1.0), dict(eps=0.0), dict(lr=float("nan"))):
+        bad = B.adamw_default_hparams(**over)
+        assert lib.adamw_step_check(ok, 3, bad, 0) == B.MUON_ERR_INVALID_ARG == lib.adamw_step(ok, 3, bad, 0, None)
+    assert lib.adamw_step_check(ok, 3, hp, -1) == lib.adamw_step_check(ok, 3, None, 0) == B.MUON_ERR_INVALID_ARG
+    assert lib.adamw_step_check(ok, -1, hp, 0) == lib.adamw_step_check(None, 1, hp, 0) == B.MUON_ERR_INVALID_ARG
