@@ -119,7 +119,14 @@ typedef struct muon_matrix {
 #define MUON_KCLASS_GRAD_NORM 24       /* sums of squares of the gradients, block by block */
 #define MUON_KCLASS_GRAD_TOTAL 25      /* the tensors' norms, their total and the clip factor */
 #define MUON_KCLASS_GRAD_SCALE 26      /* gradients scaled in place */
-#define MUON_KCLASS_COUNT 27
+#define MUON_KCLASS_QUANTISE8 27       /* matrices to 8 bits with a power of two a block */
+#define MUON_KCLASS_DEQUANTISE8 28     /* and back */
+#define MUON_KCLASS_MATMUL8 29         /* products of such matrices */
+#define MUON_KCLASS_MATMUL8_JOIN 30    /* the sum of a product's parts along k */
+#define MUON_KCLASS_ADD_NORM_FORWARD 31   /* residual addition, RMS norm and quantising */
+#define MUON_KCLASS_ADD_NORM_BACKWARD 32  /* its gradients (the weight's sums count as 21) */
+#define MUON_KCLASS_ROTARY 33          /* rotary positions */
+#define MUON_KCLASS_COUNT 34
 
 /* Returns MUON_ABI_VERSION. Host only. */
 int muon_abi_version(void);
@@ -523,6 +530,66 @@ int norm_backward_workspace_bytes(const norm_desc* desc, size_t* bytes);
 int norm_backward(const norm_desc* desc, const norm_rows* dy, const norm_rows* x, const norm_param* w,
                   const float* mean, const float* rstd, const norm_rows* dx, const norm_param* dw,
                   const norm_param* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Matrices in 8 bits and their products ------------------------------------------------
+ * For the layers whose weights Muon steps: activations, weights and gradients as e4m3 codes
+ * (1 sign, 4 exponent, 3 mantissa bits, largest value 448) with a power of two for every block
+ * of MUON_BLOCK8 = 128 elements of a row, or for every 128 x 128 elements (`tiles`, for
+ * weights: the transposed matrix then has the same codes and powers). A block's power is the
+ * least 2^e with max |x| <= 448 2^e over its finite elements (e >= -127), kept as the byte
+ * e + 127 (255 stands for NaN and is never written); its codes are x 2^-e rounded to nearest,
+ * ties to even. Infinities and NaN become NaN codes, each for itself. A value is
+ * code 2^(byte - 127); in blocks below 2^-118 it may be taken for 0. */
+#define MUON_BLOCK8 128
+#define MUON_BLOCKS8_MAX_COLS (1 << 22)
+
+typedef struct blocks8 {
+    int64_t rows, cols;
+    uint8_t* codes;    /* DEVICE, 16-byte aligned: row r at codes + r ld, cols codes and zeros up
+                          to the next multiple of 128 (quantise8 writes them, products take
+                          them for zeros) */
+    uint8_t* scales;   /* DEVICE, 4-byte aligned: byte j of row r (of row block r / 128 with
+                          tiles) at scales + r scale_ld + j, one for each 128 columns; read in
+                          fours, the rest of the last four without effect */
+    int64_t ld;        /* multiple of 16, at least cols rounded up to 128 */
+    int64_t scale_ld;  /* multiple of 4, at least cols / 128 rounded up */
+    int32_t tiles;     /* 0: a power for 1 x 128 elements, 1: for 128 x 128 */
+    int32_t reserved;
+} blocks8;
+
+/* direct [rows, cols] and / or transposed [cols, rows] (either NULL = not wanted) from x
+ * [rows, cols] of `dtype` with rows `stride` elements apart (aligned to its element, stride
+ * >= 0). Blocks run along each result's own rows: the transposed one's are 128 rows of x. Both
+ * have the same `tiles`. One read of x, one launch. rows == 0 or cols == 0 is a no-op.
+ * Errors: INVALID_ARG, ALIGN, ALIAS (an output overlaps another buffer, by spans), TOO_LARGE
+ * (rows or cols above 2^30, a row of a result above MUON_BLOCKS8_MAX_COLS, a span above 2^46
+ * elements, 2^24 blocks of 128 x 128 and more), HIP. */
+int quantise8(const void* x, int64_t rows, int64_t cols, int64_t stride, int32_t dtype, const blocks8* direct,
+              const blocks8* transposed, void* stream);
+
+/* y [rows, cols] of `dtype`, rows `stride` elements apart: the values of q, rounded to dtype
+ * (exact in fp32 and bf16 but for the smallest blocks). Errors: as quantise8. */
+int dequantise8(const blocks8* q, void* y, int64_t stride, int32_t dtype, void* stream);
+
+/* c[i][j] = sum_k a[i][k] b[j][k] for a [m, k], b [n, k], c [m, n] of `dtype`, rows ldc
+ * elements apart; plus the old c with accumulate != 0. Sums are fp32, rounded to dtype once;
+ * parts of k that blocks of the launch took are added in their order: identical calls give
+ * identical bits. m == 0 or n == 0 is a no-op, k == 0 gives zeros. With
+ *   y = x w^T           a = x (direct),             b = w (direct)
+ *   dx = dy w           a = dy (direct),            b = w (transposed)
+ *   dw = dy^T x         a = dy (transposed),        b = x (transposed)
+ * products: 8 = by the 8-bit matrix instructions, which round inside: the sum of 64 products
+ *   is off by up to 2^-12 of the sum of their magnitudes (2^-16 of the result, root mean
+ *   square, on normally distributed values); 16 = the codes are widened to bf16, exactly, and
+ *   the sums are those of fp32 additions, at half the rate; 0 = 16 for an fp32 c, 8 for others.
+ * Workspace (matmul8_workspace_bytes, 256-byte aligned; none needed where that gives 0): the
+ * partial sums of products with few tiles.
+ * Errors: INVALID_ARG (and a->cols != b->cols), ALIGN, ALIAS (c or the workspace overlaps
+ * another buffer, rows of c overlap), WORKSPACE, TOO_LARGE (as quantise8, 2^21 tiles of 128 x
+ * 128 of c and more, 2^35 elements of c and more), HIP. */
+int matmul8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t products, size_t* bytes);
+int matmul8(const blocks8* a, const blocks8* b, void* c, int64_t ldc, int32_t dtype, int32_t products,
+            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- Singular-spectrum diagnostic ----------------------------------------------------
  * SVD entropy of "Muon is Scalable for LLM Training", Sec. 3.4 (Dynamics of Singular

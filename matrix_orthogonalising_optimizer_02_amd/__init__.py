@@ -34,6 +34,12 @@ from .binding import (  # noqa: F401
     timing_read,
     workspace_bytes,
 )
+from .blocks8 import (  # noqa: F401
+    Blocks8,
+    matmul8,
+    matmul8_workspace_bytes,
+    quantise8,
+)
 from .multi import (  # noqa: F401
     AdamWMulti,
     GradNorm,

@@ -31,7 +31,8 @@ KCLASS_NAMES = ("cast", "frob", "gram", "poly", "apply", "apply_final", "rownorm
                 "colnorm_partial", "colnorm_finalize", "colnorm_apply", "rms_finalize",
                 "scaled_update", "adamw", "spec_gram", "spec_house", "spec_pass", "spec_reduce",
                 "spec_bisect", "spec_entropy", "norm_forward", "norm_backward", "norm_wgrad",
-                "tensor_plan", "adamw_multi", "grad_norm", "grad_total", "grad_scale")
+                "tensor_plan", "adamw_multi", "grad_norm", "grad_total", "grad_scale", "quantise8", "dequantise8",
+                "matmul8", "matmul8_join", "add_norm_forward", "add_norm_backward", "rotary")
 
 EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_default_hparams",
             "muon_workspace_bytes", "ns5_plan", "muon_step", "muon_step_check", "ns5_batched", "rownorm_update",
@@ -41,6 +42,7 @@ EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_defa
             "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
             "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step", "adamw_multi_step_device",
             "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
+            "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
 
@@ -104,6 +106,12 @@ class AdamWTensor(ctypes.Structure):
 class GradTensor(ctypes.Structure):
     _fields_ = [("g", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Blocks8Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scale_ld", ctypes.c_int64),
+                ("tiles", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -172,6 +180,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.grad_norm_plan.argtypes = [ctypes.POINTER(GradTensor), i32, vp, sz, plan, vp]
     lib.grad_norm.argtypes = [plan, ctypes.c_float, vp, vp, vp]
     lib.grad_scale.argtypes = [plan, vp, vp]
+    blocks = ctypes.POINTER(Blocks8Desc)
+    lib.quantise8.argtypes = [vp, i64, i64, i64, i32, blocks, blocks, vp]
+    lib.dequantise8.argtypes = [blocks, vp, i64, i32, vp]
+    lib.matmul8_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, size]
+    lib.matmul8.argtypes = [blocks, blocks, vp, i64, i32, i32, i32, vp, sz, vp]
     lib.muon_ceiling_copy.argtypes = [vp, vp, i64, vp]
     lib.muon_ceiling_mfma.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
@@ -181,6 +194,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
                  "adamw_multi_step_device", "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
+                 "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
                  "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):
         getattr(lib, name).restype = ctypes.c_int

@@ -1,0 +1,258 @@
+"""Matrices in 8 bits with a power of two for every 128 elements, and their products.
+
+The 8-bit path of the linear layers whose weights Muon steps: `quantise8` turns
+activations, gradients and fp32 weights into e4m3 codes, `matmul8` multiplies them on the
+scaled matrix instructions, and `linear8` is the layer with both gradients for
+torch.autograd. The norm before a projection can write its output in this form itself
+(`add_rms_norm_forward`).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+from . import binding as B
+
+BLOCK = 128
+_pack = struct.Struct("@2q2P2q2i").pack  # the C struct blocks8
+_calls = None
+
+
+def _entry_points():
+    """quantise8, dequantise8, matmul8 and the workspace query with plain pointer arguments."""
+    global _calls
+    if _calls is None:
+        lib = B.load_library()
+        vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+        quantise, dequantise, product = lib["quantise8"], lib["dequantise8"], lib["matmul8"]
+        size = lib["matmul8_workspace_bytes"]
+        quantise.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
+        dequantise.argtypes = [vp, vp, i64, i32, vp]
+        product.argtypes = [vp, vp, vp, i64, i32, i32, i32, vp, ctypes.c_size_t, vp]
+        size.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+        _calls = quantise, dequantise, product, size
+    return _calls
+
+
+def _up(n, to):
+    return -(-n // to) * to
+
+
+class Blocks8:
+    """A matrix [rows, cols] as codes and powers of two.
+
+    codes: float8_e4m3fn [rows, at least cols rounded up to 128], zeros from cols to there.
+    scales: uint8 [rows, at least cols / 128 rounded up, to a multiple of 4], the power of
+    each 1 x 128 elements as its exponent + 127; with `tiles` a row for each 128 rows, the
+    power of 128 x 128 elements. A value is code * 2^(scale - 127). Rows may lie further
+    apart than they are long.
+    """
+
+    __slots__ = ("codes", "scales", "rows", "cols", "tiles")
+
+    def __init__(self, codes, scales, cols: int, tiles: bool = False):
+        torch = B._torch()
+        for t, name, dtype in ((codes, "codes", torch.float8_e4m3fn), (scales, "scales", torch.uint8)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != dtype or t.dim() != 2:
+                raise ValueError(f"{name} must be a 2-D {dtype} tensor")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must live on a GPU")
+            if t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError(f"{name} must have adjacent elements in its last dimension")
+        if scales.device != codes.device:
+            raise ValueError(f"scales must live on {codes.device}")
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols, self.tiles = int(codes.shape[0]), int(cols), bool(tiles)
+        blocks, high = -(-self.cols // BLOCK), -(-self.rows // BLOCK) if tiles else self.rows
+        if self.cols < 0 or codes.shape[1] < blocks * BLOCK:
+            raise ValueError(f"codes must have {blocks * BLOCK} columns for a matrix of {cols}")
+        if scales.shape[0] != high or scales.shape[1] < _up(blocks, 4):
+            raise ValueError(f"scales must have shape [{high}, {_up(blocks, 4)}] for a matrix [{self.rows}, {cols}]")
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _packed(self):
+        c, s = self.codes, self.scales
+        # the stride of a single row is of no account
+        ld = c.stride(0) if self.rows > 1 else _up(self.cols, BLOCK)
+        scale_ld = s.stride(0) if s.shape[0] > 1 else _up(-(-self.cols // BLOCK), 4)
+        return _pack(self.rows, self.cols, c.data_ptr(), s.data_ptr(), ld, scale_ld, self.tiles, 0)
+
+    def dequantise(self, dtype=None, out=None, stream=None):
+        """The values [rows, cols] in dtype (default float32; exact there and in bfloat16)."""
+        torch = B._torch()
+        device = self.device
+        with B.device_and_stream(device, stream):
+            if out is None:
+                out = torch.empty((self.rows, self.cols), dtype=dtype or torch.float32, device=device)
+            else:
+                _check_out(out, (self.rows, self.cols), dtype, device)
+            if out.dtype not in B.dtype_codes():
+                raise ValueError("dtype must be float32, bfloat16 or float16")
+            rc = _entry_points()[1](self._packed(), out.data_ptr(), out.stride(0), B.dtype_codes()[out.dtype],
+                                    B.raw_stream(stream, device))
+        if rc:
+            B._check(rc, "dequantise8")
+        return out
+
+
+def _check_out(out, shape, dtype, device):
+    torch = B._torch()
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    if tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"out must have shape {tuple(shape)} and live on {device}")
+    if dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must have dtype {dtype}")
+    if out.shape[-1] > 1 and out.stride(-1) != 1:
+        raise ValueError("out must have adjacent elements in its last dimension")
+
+
+def _new(like, rows, cols, tiles):
+    """Memory for a matrix [rows, cols] in 8 bits, beside the tensor `like`."""
+    torch = B._torch()
+    q = Blocks8.__new__(Blocks8)
+    blocks = -(-cols // BLOCK)
+    q.codes = like.new_empty((rows, blocks * BLOCK), dtype=torch.float8_e4m3fn)
+    q.scales = like.new_empty((-(-rows // BLOCK) if tiles else rows, _up(blocks, 4)), dtype=torch.uint8)
+    q.rows, q.cols, q.tiles = rows, cols, tiles
+    return q
+
+
+def _rows_of(x, name):
+    """(rows, cols, stride) of a tensor as a matrix of its last dimension."""
+    torch = B._torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must live on a GPU")
+    if x.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    if x.dtype not in B.dtype_codes():
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    cols = x.shape[-1]
+    rows = 1
+    for size in x.shape[:-1]:
+        rows *= size
+    if x.is_contiguous() or rows == 0 or cols == 0:
+        return rows, cols, cols
+    if cols > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    stride = span = None
+    for size, step in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride, span = step, size * step
+        elif step != span:
+            raise ValueError(f"{name} has rows at more than one stride; make it contiguous")
+        else:
+            span *= size
+    return rows, cols, cols if stride is None else stride
+
+
+def _given(q, name, rows, cols, tiles, device):
+    if not isinstance(q, Blocks8):
+        raise TypeError(f"{name} must be a Blocks8")
+    if (q.rows, q.cols, q.tiles) != (rows, cols, tiles) or q.device != device:
+        raise ValueError(f"{name} must be a Blocks8 of [{rows}, {cols}] with tiles={tiles} on {device}")
+
+
+def quantise8(x, *, tiles: bool = False, direct: bool = True, transposed: bool = False, out=None, out_transposed=None,
+              stream=None):
+    """(q, qt): x [..., cols] as Blocks8 [rows, cols] and its transpose [cols, rows], each None
+    where not asked for, from one read of x.
+
+    Each block of 128 elements along a result's rows (tiles: of 128 x 128) gets the least power
+    of two that brings its largest finite magnitude to 448 or less; codes are rounded to
+    nearest. Infinities and NaN become NaN, each for itself. x: float32, bfloat16 or float16,
+    its rows at one stride. out, out_transposed: Blocks8 that are written in place of new ones.
+    """
+    rows, cols, stride = _rows_of(x, "x")
+    device = x.device
+    tiles = bool(tiles)
+    if out is not None:
+        _given(out, "out", rows, cols, tiles, device)
+    if out_transposed is not None:
+        _given(out_transposed, "out_transposed", cols, rows, tiles, device)
+    if not (direct or transposed or out is not None or out_transposed is not None):
+        raise ValueError("neither direct nor transposed is asked for")
+    with B.device_and_stream(device, stream):
+        q, qt = out, out_transposed
+        if q is None and direct:
+            q = _new(x, rows, cols, tiles)
+        if qt is None and transposed:
+            qt = _new(x, cols, rows, tiles)
+        rc = _entry_points()[0](x.data_ptr(), rows, cols, stride, B.dtype_codes()[x.dtype], q and q._packed(),
+                                qt and qt._packed(), B.raw_stream(stream, device))
+    if rc:
+        B._check(rc, "quantise8")
+    return q, qt
+
+
+def matmul8_workspace_bytes(m: int, n: int, k: int, dtype=None, products=None) -> int:
+    """Bytes of matmul8's workspace for [m, k] times [n, k] into dtype (default bfloat16)."""
+    size = ctypes.c_size_t(0)
+    dtype = B.dtype_codes()[dtype or B._torch().bfloat16]
+    B._check(_entry_points()[3](m, n, k, dtype, products or 0, size), "matmul8_workspace_bytes")
+    return size.value
+
+
+def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = False, products=None, workspace=None,
+            stream=None):
+    """out[i, j] = sum_k a[i, k] b[j, k] (plus the old out with accumulate), fp32 sums rounded
+    once to dtype (float32, bfloat16 or float16; default out's, or bfloat16).
+
+    With quantise8's results of a layer's x, weight and dy: y = (x, weight), dx = (dy, weight
+    transposed), dweight = (dy transposed, x transposed). products 8: by the 8-bit matrix
+    instructions, which round inside (2^-16 of the result on normally distributed values); 16:
+    widened to bfloat16, exactly, with sums as of fp32 additions, at half the rate; None: 16 for
+    a float32 result, 8 for others. workspace: optional uint8 buffer of
+    matmul8_workspace_bytes().
+    """
+    torch = B._torch()
+    for q, name in ((a, "a"), (b, "b")):
+        if not isinstance(q, Blocks8):
+            raise TypeError(f"{name} must be a Blocks8")
+    device = a.device
+    if b.device != device:
+        raise ValueError(f"b must live on {device}")
+    if a.cols != b.cols:
+        raise ValueError(f"a and b must have the same number of columns, {a.cols} and {b.cols}")
+    if products not in (None, 8, 16):
+        raise ValueError("products must be None, 8 or 16")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None:
+        _check_out(out, (a.rows, b.rows), dtype, device)
+    dtype = out.dtype if out is not None else dtype or torch.bfloat16
+    code = B.dtype_codes().get(dtype)
+    if code is None:
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    with B.device_and_stream(device, stream):
+        if out is None:
+            out = a.codes.new_empty((a.rows, b.rows), dtype=dtype)
+        ws, wsb = None, 0
+        if workspace is not None:
+            if workspace.device != device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+                raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+            ws, wsb = workspace.data_ptr(), workspace.numel()
+        else:
+            wsb = matmul8_workspace_bytes(a.rows, b.rows, a.cols, dtype, products)
+            if wsb:
+                workspace = a.codes.new_empty(wsb, dtype=torch.uint8)
+                ws = workspace.data_ptr()
+        ldc = out.stride(0) if out.shape[0] > 1 else out.shape[1]
+        rc = _entry_points()[2](a._packed(), b._packed(), out.data_ptr(), ldc, code, products or 0, bool(accumulate), ws, wsb,
+                                B.raw_stream(stream, device))
+    if rc:
+        B._check(rc, "matmul8")
+    return out

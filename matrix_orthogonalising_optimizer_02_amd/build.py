@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["k_elementwise.hip", "k_gemm.hip", "k_adamw.hip", "k_spectrum.hip", "noalloc.hip", "k_ceiling.hip",
-           "k_norm.hip", "k_adamw_multi.hip", "k_grad_norm.hip", "muon_abi.cpp", "abi_norm.cpp", "abi_multi.cpp"]
+           "k_norm.hip", "k_adamw_multi.hip", "k_grad_norm.hip", "k_blocks8.hip", "k_matmul8.hip", "muon_abi.cpp", "abi_norm.cpp",
+           "abi_multi.cpp", "abi_blocks8.cpp"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -1,0 +1,107 @@
+// Matrices in 8 bits with a power of two for every 128 elements: kernel descriptors, the rule
+// that gives a block its power, and the conversion. A block is 1 x 128 elements of a row, or
+// 128 x 128. Its power is the least 2^e that brings its largest finite magnitude to 448, e4m3's
+// largest value, or less. Dividing by it is exact, so an element is rounded once, by the
+// conversion; and the matrix instructions of gfx950 take such powers (a byte, e + 127) beside
+// their 8-bit operands, so that a product needs no arithmetic for its scales. Against a scale
+// of amax / 448 at most half of the largest binade stays unused: e4m3 is a floating format, so
+// that costs no precision but for magnitudes 2^-14 below the block's largest.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+#include "train.hpp"
+
+namespace muon {
+
+constexpr int kBlock8 = 128;
+
+// Codes [rows, ld] with zeros from the matrix's last column to a multiple of 128, powers
+// [rows or row blocks, scale_ld]. codes == nullptr: not wanted.
+struct Blocks8Ptr {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t ld, scale_ld;
+};
+
+struct Quant8Args {
+    const void* x;
+    int64_t stride;
+    int32_t rows, cols;
+    int32_t col_blocks;
+    Blocks8Ptr direct, transposed;
+};
+
+struct Dequant8Args {
+    Blocks8Ptr q;
+    void* y;
+    int64_t stride;
+    uint32_t total;        // chunks of 16 codes
+    int32_t cols;
+    uint32_t per_row;      // chunks of a row
+    uint32_t mul;          // i / per_row = (mulhi(i, mul) + i) >> shift, 33-bit sum, for per_row > 1
+    int32_t shift;
+    int32_t row_shift;     // 7 for 128 x 128 blocks
+    int32_t dtype;
+};
+
+// C[i][j] = sum_k A[i][k] B[j][k]
+struct Mat8Args {
+    const uint8_t *a, *b;      // codes
+    const uint8_t *as, *bs;    // powers
+    int64_t lda, ldb, lsa, lsb;
+    int32_t sha, shb;          // row i's powers are row i >> sh
+    int32_t m, n;
+    int32_t steps;             // blocks of 128 along k
+    int32_t dtype;             // of c
+    int32_t accumulate;
+    void* c;
+    int64_t ldc;
+    int32_t tiles_m, tiles_n;
+    int32_t splits;            // parts of k, each a multiple of 4 steps but for the last
+    float* partial;            // [splits][m][n], used when splits > 1
+};
+
+// How a product is cut: `few` rows in one pass over B, or tiles of side `tile`.
+struct Mat8Plan {
+    int few;                   // 0, or the 16-row groups of A that a wave holds
+    int waves;                 // few: of a block, which share k
+    int tile;                  // 128 or 256
+    int splits;
+    size_t partial_bytes;
+};
+Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide);
+
+hipError_t launch_quantise8(int dtype, bool tiles, const Quant8Args& a, hipStream_t s);
+hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s);
+hipError_t launch_matmul8(const Mat8Plan& p, bool wide, const Mat8Args& a, hipStream_t s);
+hipError_t launch_matmul8_join(const Mat8Args& a, hipStream_t s);
+
+// Bits of f's magnitude, 0 where it is infinite or NaN.
+__device__ __forceinline__ unsigned finite_bits(float f) {
+    const unsigned u = __float_as_uint(f) & 0x7FFFFFFFu;
+    return u >= 0x7F800000u ? 0u : u;
+}
+
+// The byte e + 127 of a block with largest magnitude `top` (bits): 448 is 1.75 2^8, so a
+// mantissa up to 1.75 (0x600000) takes the exponent less 8 and a larger one carries into the
+// next. At least 0: a block below 2^-118 loses what lies under 2^-136.
+__device__ __forceinline__ unsigned block_power(unsigned top) {
+    const unsigned e = (top + 0x1FFFFFu) >> 23;
+    return e > 8u ? e - 8u : 0u;
+}
+
+// 2^-e and 2^e of the byte (a byte of 0 gives 0 for the latter: its block holds zeros, or
+// magnitudes below 2^-118).
+__device__ __forceinline__ float power_inverse(unsigned byte) { return __uint_as_float((254u - byte) << 23); }
+__device__ __forceinline__ float power_value(unsigned byte) { return __uint_as_float(byte << 23); }
+
+// Four values of at most 448 to four codes, ties to even; an infinity or NaN gives NaN.
+__device__ __forceinline__ unsigned pack_codes(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+}  // namespace muon

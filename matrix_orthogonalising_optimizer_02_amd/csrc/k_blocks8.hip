@@ -1,0 +1,195 @@
+// Quantising a matrix to 8 bits with a power of two for every 128 elements, and reading it
+// back (blocks8.hpp has the rule).
+#include "blocks8.hpp"
+#include "rows.hpp"
+
+namespace muon {
+namespace {
+
+// Largest of the four 16-lane rows of a wave, lane by lane of a row.
+__device__ __forceinline__ unsigned rows_max(unsigned v) {
+    auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = s[0] > s[1] ? s[0] : s[1];
+    s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return s[0] > s[1] ? s[0] : s[1];
+}
+
+__device__ __forceinline__ void put_power(uint8_t* row, int at, int blocks, unsigned byte) {
+    row[at] = (uint8_t)byte;
+    if (at == blocks - 1)  // the rest of the last four, which products read and do not use
+        for (int i = blocks; i & 3; ++i) row[i] = 0;
+}
+
+// A block of 256 threads takes 128 x 128 elements, a thread 8 x 8 of them in registers: 16
+// threads share a row (its largest magnitude is a reduction over 16 lanes, its codes leave as
+// 128 contiguous bytes), and the 8 rows of a thread are 8 contiguous bytes of the transposed
+// matrix, which is put together in 16 KB of LDS. So both forms cost one read of x.
+// HBM-bound: [8192, 5120] bf16 into both forms, see the launcher.
+template <int T, bool kTiles, bool kDirect, bool kTransposed>
+__global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
+    typedef Elem<T> E;
+    typedef typename E::type elem;
+    __shared__ unsigned tops[4][kBlock8];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kTransposed ? kBlock8 * kBlock8 : 16];
+    const int br = blockIdx.x / a.col_blocks, bc = blockIdx.x - br * a.col_blocks;
+    const int row_blocks = (a.rows + kBlock8 - 1) / kBlock8;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+    const int row0 = br * kBlock8 + rg * 8, col0 = bc * kBlock8 + cg * 8;
+    float v[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const elem* x = reinterpret_cast<const elem*>(a.x) + (int64_t)(row0 + p) * a.stride + col0;
+        if (row0 + p < a.rows && col0 + 8 <= a.cols) {
+#pragma unroll
+            for (int q = 0; q < 8 / E::kVec; ++q) E::unpack(load16(x + q * E::kVec), v[p] + q * E::kVec);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[p][e] = row0 + p < a.rows && col0 + e < a.cols ? (float)x[e] : 0.f;
+        }
+    }
+    unsigned row_top[8], col_top[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) row_top[e] = col_top[e] = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const unsigned u = finite_bits(v[p][e]);
+            row_top[p] = max(row_top[p], u);
+            col_top[e] = max(col_top[e], u);
+        }
+    if constexpr (kTiles) {
+        unsigned top = row_top[0];
+#pragma unroll
+        for (int p = 1; p < 8; ++p) top = max(top, row_top[p]);
+        top = lanes_max<64>(top);
+        if ((threadIdx.x & 63) == 0) tops[wave][0] = top;
+        __syncthreads();
+        top = max(max(tops[0][0], tops[1][0]), max(tops[2][0], tops[3][0]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) row_top[e] = col_top[e] = top;
+    } else {
+        if constexpr (kDirect) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) row_top[p] = lanes_max<16>(row_top[p]);
+        }
+        if constexpr (kTransposed) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned t = rows_max(col_top[e]);
+                if ((threadIdx.x & 48) == 0) tops[wave][cg * 8 + e] = t;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = cg * 8 + e;
+                col_top[e] = max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c]));
+            }
+        }
+    }
+    if constexpr (kDirect) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            if (row0 + p >= a.rows) break;
+            const unsigned byte = block_power(row_top[p]);
+            const float s = power_inverse(byte);
+            u32x2 w;
+            w.x = pack_codes(v[p][0] * s, v[p][1] * s, v[p][2] * s, v[p][3] * s);
+            w.y = pack_codes(v[p][4] * s, v[p][5] * s, v[p][6] * s, v[p][7] * s);
+            *reinterpret_cast<u32x2*>(a.direct.codes + (int64_t)(row0 + p) * a.direct.ld + col0) = w;
+            if (cg == 0 && (!kTiles || (rg == 0 && p == 0)))
+                put_power(a.direct.scales + (int64_t)(kTiles ? br : row0 + p) * a.direct.scale_ld, bc, a.col_blocks, byte);
+        }
+    }
+    if constexpr (kTransposed) {
+        // eight rows of a column are an 8-byte slot of the turned tile's row; slot g of row c
+        // sits at g ^ (c / 8), so that the 16 column groups of a write meet 16 slots
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = power_inverse(block_power(col_top[e]));
+            u32x2 w;
+            w.x = pack_codes(v[0][e] * s, v[1][e] * s, v[2][e] * s, v[3][e] * s);
+            w.y = pack_codes(v[4][e] * s, v[5][e] * s, v[6][e] * s, v[7][e] * s);
+            *reinterpret_cast<u32x2*>(turned + (cg * 8 + e) * kBlock8 + ((rg ^ cg) & 15) * 8) = w;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int c = q * 32 + (threadIdx.x >> 3), j = threadIdx.x & 7, g = c >> 3;
+            const u32x4 r = *reinterpret_cast<const u32x4*>(turned + c * kBlock8 + ((j ^ (g >> 1)) & 7) * 16);
+            const u32x4 w = g & 1 ? u32x4{r.z, r.w, r.x, r.y} : r;
+            if (bc * kBlock8 + c < a.cols)
+                *reinterpret_cast<u32x4*>(a.transposed.codes + (int64_t)(bc * kBlock8 + c) * a.transposed.ld + br * kBlock8 +
+                                          j * 16) = w;
+        }
+        if constexpr (kTiles) {
+            if (threadIdx.x == 0)
+                put_power(a.transposed.scales + (int64_t)bc * a.transposed.scale_ld, br, row_blocks, block_power(col_top[0]));
+        } else if (threadIdx.x < kBlock8 && bc * kBlock8 + (int)threadIdx.x < a.cols) {
+            const int c = threadIdx.x;
+            const unsigned top = max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c]));
+            put_power(a.transposed.scales + (int64_t)(bc * kBlock8 + c) * a.transposed.scale_ld, br, row_blocks,
+                      block_power(top));
+        }
+    }
+}
+
+// 16 codes a thread; HBM-bound.
+template <int T>
+__global__ __launch_bounds__(256) void k_dequantise8(Dequant8Args a) {
+    typedef Elem<T> E;
+    typedef typename E::type elem;
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;
+    if (i >= a.total) return;
+    unsigned row = i;
+    if (a.per_row > 1) row = (unsigned)(((uint64_t)__umulhi(i, a.mul) + i) >> a.shift);
+    const int col = (int)(i - row * a.per_row) * 16;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(a.q.codes + (int64_t)row * a.q.ld + col);
+    const float s = power_value(a.q.scales[(int64_t)(row >> a.row_shift) * a.q.scale_ld + col / kBlock8]);
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], true);
+        f[4 * k] = lo[0] * s;
+        f[4 * k + 1] = lo[1] * s;
+        f[4 * k + 2] = hi[0] * s;
+        f[4 * k + 3] = hi[1] * s;
+    }
+    elem* y = reinterpret_cast<elem*>(a.y) + (int64_t)row * a.stride + col;
+    if (col + 16 <= a.cols) {
+#pragma unroll
+        for (int k = 0; k < 16 / E::kVec; ++k) put_stream16(y + k * E::kVec, E::pack(f + k * E::kVec));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (col + k < a.cols) y[k] = (elem)f[k];
+    }
+}
+
+template <int T, bool kTiles>
+hipError_t launch_sides(const Quant8Args& a, hipStream_t s) {
+    const int64_t blocks = int64_t((a.rows + kBlock8 - 1) / kBlock8) * a.col_blocks;
+    const dim3 grid((unsigned)blocks), block(256);
+    if (a.direct.codes && a.transposed.codes) hipLaunchKernelGGL((k_quantise8<T, kTiles, true, true>), grid, block, 0, s, a);
+    else if (a.direct.codes) hipLaunchKernelGGL((k_quantise8<T, kTiles, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_quantise8<T, kTiles, false, true>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantise8(int dtype, bool tiles, const Quant8Args& a, hipStream_t s) {
+    if (dtype == kF32) return tiles ? launch_sides<kF32, true>(a, s) : launch_sides<kF32, false>(a, s);
+    if (dtype == kBF16) return tiles ? launch_sides<kBF16, true>(a, s) : launch_sides<kBF16, false>(a, s);
+    return tiles ? launch_sides<kF16, true>(a, s) : launch_sides<kF16, false>(a, s);
+}
+
+hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s) {
+    const dim3 grid((a.total + 255) / 256), block(256);
+    if (a.dtype == kF32) hipLaunchKernelGGL(k_dequantise8<kF32>, grid, block, 0, s, a);
+    else if (a.dtype == kBF16) hipLaunchKernelGGL(k_dequantise8<kBF16>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_dequantise8<kF16>, grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace muon
