@@ -591,6 +591,98 @@ int matmul8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dtype, int3
 int matmul8(const blocks8* a, const blocks8* b, void* c, int64_t ldc, int32_t dtype, int32_t products,
             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Residual addition with RMS norm ----------------------------------------------------
+ * The step between two layers of a pre-norm block. For rows of `cols` elements:
+ *   h = x + residual, rounded to the residual's type;  rstd = 1 / sqrt((1/cols) sum h^2 + eps)
+ *   y = h rstd (weight_offset + w)
+ * with y in x's type and / or in 8 bits for matmul8, both from the same fp32 values. Without a
+ * residual h is x and is not written. Backward, from dy and the gradient dh of h itself (what
+ * comes down the residual stream; NULL = 0), with n = h rstd and a = dy (weight_offset + w):
+ *   d = dh + rstd (a - n (1/cols) sum a n)        the gradient of x and of the residual
+ *   dw = sum over rows of dy n
+ * Quantising y counts as the identity there. Arithmetic is fp32, each output rounded once;
+ * sums run in a fixed order. */
+typedef struct add_norm_desc {
+    int64_t rows, cols;
+    int32_t dtype;        /* of x, y, dy, dx */
+    int32_t rdtype;       /* of residual, h, dh, dr: MUON_DTYPE_F32 or dtype */
+    int32_t wdtype;       /* of w, dw: MUON_DTYPE_F32 or dtype */
+    float eps;            /* finite, > 0 */
+    float weight_offset;  /* finite; without effect where w is NULL */
+    int32_t reserved;
+} add_norm_desc;
+
+/* norm_rows here: row r at data + r stride0 (stride1 is not used); norm_param: one row. h may
+ * be residual or x (same pointer, stride and type). residual, w, y, codes, rstd: NULL (or data
+ * NULL) = absent or not wanted; h goes with residual. codes: [rows, cols], tiles 0. One launch.
+ * rows == 0 or cols == 0 is a no-op.
+ * Errors: INVALID_ARG, ALIGN, ALIAS (an output overlaps another buffer, by spans), TOO_LARGE
+ * (cols above MUON_NORM_MAX_COLS, rows above 2^30, a span above 2^46 elements), HIP. */
+int add_rms_norm_forward(const add_norm_desc* desc, const norm_rows* x, const norm_rows* residual, const norm_param* w,
+                         const norm_rows* h, const norm_rows* y, const blocks8* codes, float* rstd, void* stream);
+
+/* Workspace in bytes of add_rms_norm_backward with dw. Host only. */
+int add_rms_norm_backward_workspace_bytes(const add_norm_desc* desc, size_t* bytes);
+
+/* dr [rows, cols] of rdtype receives d; dx, wanted only where dtype is not rdtype, d in dtype.
+ * dr and dx may be dy, dh or h where pointer, stride and type are the same. dw is overwritten
+ * (zeros where rows == 0), NULL = not wanted; dw without w is INVALID_ARG. desc->eps is not
+ * used. One launch, and a second for dw where the rows took several blocks.
+ * Errors: as add_rms_norm_forward, and WORKSPACE (256-byte aligned; none needed without dw). */
+int add_rms_norm_backward(const add_norm_desc* desc, const norm_rows* dy, const norm_rows* dh, const norm_rows* h,
+                          const norm_param* w, const float* rstd, const norm_rows* dr, const norm_rows* dx,
+                          const norm_param* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Rotary positions over several axes ---------------------------------------------------
+ * For the query and key heads, after their RMS norms: time, height and width of an image or
+ * video token, or one axis for text. Each head has `dim` elements, of which 2 pairs are turned:
+ * pair i is elements (i, i + pairs) under MUON_ROTARY_HALVES and (2 i, 2 i + 1) under
+ * MUON_ROTARY_ADJACENT, turned by the angle 2 pi freq[i] position[axis[i]] of its token:
+ *   p' = p cos - q sin,  q' = p sin + q cos
+ * elements from 2 pairs on are copied. inverse != 0 turns back, which is also the gradient.
+ * The angle's fraction of a turn is fp64, its sine and cosine and the products are fp32,
+ * rounded once. */
+#define MUON_ROTARY_HALVES 0
+#define MUON_ROTARY_ADJACENT 1
+#define MUON_ROTARY_MAX_DIM 1024
+#define MUON_ROTARY_MAX_HEADS 65536
+#define MUON_POSITION_I32 0
+#define MUON_POSITION_I64 1
+#define MUON_POSITION_F32 2
+
+typedef struct rotary_desc {
+    int64_t batch, tokens, heads, dim;
+    int32_t pairs, axes;     /* >= 1; 2 pairs <= dim */
+    int32_t dtype;           /* of x and y */
+    int32_t layout;          /* MUON_ROTARY_* */
+    int32_t position_type;   /* MUON_POSITION_* */
+    int32_t inverse;
+} rotary_desc;
+
+/* Head h of token t of batch b at data + b stride_batch + t stride_token + h stride_head
+ * elements, its elements adjacent. Strides are >= 0. */
+typedef struct rotary_rows {
+    void* data;
+    int64_t stride_batch, stride_token, stride_head;
+} rotary_rows;
+
+/* The token's `axes` positions, adjacent, at data + b stride_batch + t stride_token elements
+ * (stride_batch 0: the same for every batch). */
+typedef struct rotary_positions {
+    const void* data;
+    int64_t stride_batch, stride_token;
+} rotary_positions;
+
+/* freq (DEVICE, pairs doubles): turns per unit of position, theta^(-i / n) / (2 pi) for a
+ * ladder of n pairs. axis (DEVICE, pairs ints in 0 .. axes - 1; others are taken for the last).
+ * y may be x itself (same pointer and strides). One launch; batch, tokens, heads or dim == 0 is
+ * a no-op.
+ * Errors: INVALID_ARG, ALIGN (a pointer not aligned to its element), ALIAS (y overlaps another
+ * buffer, by spans, or itself), TOO_LARGE (dim above MUON_ROTARY_MAX_DIM, heads above
+ * MUON_ROTARY_MAX_HEADS, batch tokens above 2^30, a span above 2^46 elements), HIP. */
+int rotary_apply(const rotary_desc* desc, const rotary_rows* x, const rotary_positions* positions, const double* freq,
+                 const int32_t* axis, const rotary_rows* y, void* stream);
+
 /* ---- Singular-spectrum diagnostic ----------------------------------------------------
  * SVD entropy of "Muon is Scalable for LLM Training", Sec. 3.4 (Dynamics of Singular
  * Spectrum): for W [A, B] with singular values sigma_1..sigma_n, n = min(A, B),

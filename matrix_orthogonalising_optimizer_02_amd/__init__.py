@@ -34,6 +34,12 @@ from .binding import (  # noqa: F401
     timing_read,
     workspace_bytes,
 )
+from .add_norm import (  # noqa: F401
+    add_rms_norm,
+    add_rms_norm_backward,
+    add_rms_norm_backward_workspace_bytes,
+    add_rms_norm_forward,
+)
 from .blocks8 import (  # noqa: F401
     Blocks8,
     matmul8,
@@ -50,4 +56,9 @@ from .norms import (  # noqa: F401
     norm_backward_workspace_bytes,
     norm_forward,
     rms_norm,
+)
+from .rotary import (  # noqa: F401
+    RotaryAxes,
+    rotary,
+    rotary_apply,
 )

@@ -43,6 +43,7 @@ EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_defa
             "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step", "adamw_multi_step_device",
             "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
             "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
+            "add_rms_norm_forward", "add_rms_norm_backward_workspace_bytes", "add_rms_norm_backward", "rotary_apply",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
 
@@ -112,6 +113,27 @@ class Blocks8Desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scale_ld", ctypes.c_int64),
                 ("tiles", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AddNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("rdtype", ctypes.c_int32),
+                ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("position_type", ctypes.c_int32), ("inverse", ctypes.c_int32)]
+
+
+class RotaryRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64)]
+
+
+class RotaryPositions(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
 
 
 class MuonError(RuntimeError):
@@ -185,6 +207,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dequantise8.argtypes = [blocks, vp, i64, i32, vp]
     lib.matmul8_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, size]
     lib.matmul8.argtypes = [blocks, blocks, vp, i64, i32, i32, i32, vp, sz, vp]
+    add = ctypes.POINTER(AddNormDesc)
+    lib.add_rms_norm_forward.argtypes = [add, rows, rows, param, rows, rows, blocks, vp, vp]
+    lib.add_rms_norm_backward_workspace_bytes.argtypes = [add, size]
+    lib.add_rms_norm_backward.argtypes = [add, rows, rows, rows, param, vp, rows, rows, param, vp, sz, vp]
+    turned = ctypes.POINTER(RotaryRows)
+    lib.rotary_apply.argtypes = [ctypes.POINTER(RotaryDesc), turned, ctypes.POINTER(RotaryPositions), vp, vp, turned, vp]
     lib.muon_ceiling_copy.argtypes = [vp, vp, i64, vp]
     lib.muon_ceiling_mfma.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_double), vp]
     lib.muon_timing_enable.argtypes = [ctypes.c_int]
@@ -195,6 +223,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
                  "adamw_multi_step_device", "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
                  "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
+                 "add_rms_norm_forward", "add_rms_norm_backward_workspace_bytes", "add_rms_norm_backward", "rotary_apply",
                  "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):
         getattr(lib, name).restype = ctypes.c_int

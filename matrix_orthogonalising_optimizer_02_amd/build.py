@@ -19,8 +19,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["k_elementwise.hip", "k_gemm.hip", "k_adamw.hip", "k_spectrum.hip", "noalloc.hip", "k_ceiling.hip",
-           "k_norm.hip", "k_adamw_multi.hip", "k_grad_norm.hip", "k_blocks8.hip", "k_matmul8.hip", "muon_abi.cpp", "abi_norm.cpp",
-           "abi_multi.cpp", "abi_blocks8.cpp"]
+           "k_norm.hip", "k_adamw_multi.hip", "k_grad_norm.hip", "k_blocks8.hip", "k_matmul8.hip", "k_add_norm.hip",
+           "k_rotary.hip", "muon_abi.cpp", "abi_norm.cpp",
+           "abi_multi.cpp", "abi_blocks8.cpp", "abi_add_norm.cpp"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -74,6 +74,31 @@ struct Mat8Plan {
 };
 Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide);
 
+// ---- residual addition, RMS norm, 8-bit output ------------------------------------------
+// Rows of `cols` elements, a stride apart each.
+struct AddNormArgs {
+    const void* x;         // forward: the block's output; backward: dy
+    const void* r;         // forward: the residual, null = none; backward: dh, null = none
+    void* h;               // forward: x + r in the residual's type, null without one; backward: h, read
+    void* y;               // forward: the norm's output, null = not wanted; backward: d in x's type, null = not wanted
+    void* d;               // backward: d in the residual's type
+    int64_t x_stride, r_stride, h_stride, y_stride, d_stride;
+    const void* w;         // null: factor 1
+    float* rstd;
+    Blocks8Ptr q;          // forward: the norm's output in 8 bits
+    float* partial;        // backward: [chunks][cols]
+    void* dw;              // backward: null = not wanted
+    int32_t rows, cols;
+    int32_t wdtype;
+    int32_t chunks;        // blocks
+    int32_t team_waves, teams;
+    float eps, offset;
+    double inv_cols;
+};
+NormPlan plan_add_norm(bool forward, int dtype, int64_t cols, int64_t rows);
+hipError_t launch_add_norm_forward(int dtype, bool res32, const NormPlan& p, const AddNormArgs& a, hipStream_t s);
+hipError_t launch_add_norm_backward(int dtype, bool res32, const NormPlan& p, const AddNormArgs& a, hipStream_t s);
+
 hipError_t launch_quantise8(int dtype, bool tiles, const Quant8Args& a, hipStream_t s);
 hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s);
 hipError_t launch_matmul8(const Mat8Plan& p, bool wide, const Mat8Args& a, hipStream_t s);

@@ -52,8 +52,6 @@ struct Turn {
     }
 };
 
-constexpr int kSubThreads = 512;  // most threads of a block whose rows share a wave
-
 template <int T, bool kRms, int kLanes, int kN, bool kExact>
 __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_norm_forward(NormArgs a) {
     typedef Elem<T> E;

@@ -138,6 +138,7 @@ struct Team {
 };
 
 constexpr int kMaxWaves = 16;
+constexpr int kSubThreads = 512;  // most threads of a block whose rows share a wave
 
 // kCount sums over the row's lanes. Teams of several waves exchange them through `red`,
 // one slot a wave, behind one barrier of the whole block: every team runs the same number

@@ -69,6 +69,30 @@ hipError_t launch_norm_forward(bool rms, int dtype, const NormPlan& p, const Nor
 hipError_t launch_norm_backward(bool rms, int dtype, const NormPlan& p, const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_wgrad(const NormArgs& a, hipStream_t s);
 
+// ---- rotary positions ---------------------------------------------------------------
+struct RotaryRows {
+    void* data;
+    int64_t sb, st, sh;    // batch, token, head
+};
+
+struct RotaryArgs {
+    RotaryRows x, y;
+    const void* pos;       // axis adjacent
+    int64_t pb, pt;
+    const double* freq;    // turns per unit of position, a pair each
+    const int32_t* axis;   // of each pair
+    uint32_t rows;         // batch * tokens
+    uint32_t tokens;
+    int32_t heads, dim, pairs, axes;
+    int32_t pos_type;      // 0 int32, 1 int64, 2 float
+    int32_t block_rows;    // tokens of a block
+    uint32_t heads_mul;    // i / heads, as inner_mul above
+    int32_t heads_shift;
+    int32_t lane_bits;     // log2 of the threads that share a head
+    float sign;            // -1: turned back
+};
+hipError_t launch_rotary(int dtype, bool adjacent, const RotaryArgs& a, hipStream_t s);
+
 // ---- many tensors in one launch ----------------------------------------------------
 // A table in device memory holds the descriptors and, for every block, its tensor. Both
 // are written by kernels whose arguments carry the descriptors: no copy from host memory,
