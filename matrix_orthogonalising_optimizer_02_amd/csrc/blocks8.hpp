@@ -61,14 +61,16 @@ struct Mat8Args {
     int64_t ldc;
     int32_t tiles_m, tiles_n;
     int32_t splits;            // parts of k, each a multiple of 4 steps but for the last
+    int32_t share;             // few rows: waves that take turns along k
     float* partial;            // [splits][m][n], used when splits > 1
 };
 
-// How a product is cut: `few` rows in one pass over B, or tiles of side `tile`.
+// How a product is cut.
 struct Mat8Plan {
-    int few;                   // 0, or the 16-row groups of A that a wave holds
-    int waves;                 // few: of a block, which share k
-    int tile;                  // 128 or 256
+    int few;                   // groups of 16 rows of A, 0 where they are many
+    int stream;                // few: 1 = a large B, through LDS
+    int waves, share;          // few, a small B: of a block, and of those that take turns at the same rows of B
+    int tile;                  // many: side of a block's tile, 128 or 256
     int splits;
     size_t partial_bytes;
 };

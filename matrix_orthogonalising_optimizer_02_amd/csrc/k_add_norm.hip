@@ -101,10 +101,17 @@ __device__ __forceinline__ void load_weights(const AddNormArgs& a, int col, floa
 // block of 128.
 template <int kVec, int kGroup>
 __device__ __forceinline__ void put_codes(const AddNormArgs& a, int64_t row, int index, int skip, const float* y, bool mine) {
-    unsigned top = 0;
+    float most = 0.f;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) top = max(top, e >= skip ? finite_bits(y[e]) : 0u);
-    const unsigned byte = block_power(lanes_max<kGroup>(top));
+    for (int e = 0; e < kVec; ++e) most = fmaxf(most, e >= skip ? fabsf(y[e]) : 0.f);  // passes over NaN
+    unsigned top = lanes_max<kGroup>(__float_as_uint(most));
+    if (__any(top >= 0x7F800000u)) {  // an infinity: once more over what is finite
+        top = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) top = max(top, e >= skip ? finite_bits(y[e]) : 0u);
+        top = lanes_max<kGroup>(top);
+    }
+    const unsigned byte = block_power(top);
     const int at = index * kVec, blocks = (a.cols + kBlock8 - 1) / kBlock8;
     if (!mine || at >= blocks * kBlock8) return;
     const float s = power_inverse(byte);
@@ -191,13 +198,12 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_add_norm_forwar
         float sum[1] = {sq};
         row_sums<kLanes, 1>(sum, red[flip], t, a.team_waves);
         flip ^= 1;
-        // rstd and the products with it are fp64, at fp32's rate on this card: the fewer of y's
-        // bits rounding has moved, the fewer codes fall to the other side of a border. One
-        // Newton step from the fp32 root.
+        // rstd as the sum of two floats (one Newton step in fp64 from the fp32 root)
         const double var = (double)sum[0] * a.inv_cols + a.eps;
-        double rstd = 1.f / sqrtf((float)var);
-        rstd *= 1.5 - 0.5 * var * rstd * rstd;
-        if (mine && t.lane == 0 && a.rstd) a.rstd[row] = (float)rstd;
+        double rd = 1.f / sqrtf((float)var);
+        if (rd > 0.0) rd *= 1.5 - 0.5 * var * rd * rd;  // 0 where the sum is infinite
+        const float rstd = (float)rd, rest = (float)(rd - rstd);
+        if (mine && t.lane == 0 && a.rstd) a.rstd[row] = rstd;
         // All of the row was read before the sum above: h may lie where r or x lay.
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
@@ -207,7 +213,13 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_add_norm_forwar
             if (a.r && mine && any) h[k].store(reinterpret_cast<relem*>(a.h) + row * a.h_stride, sp.col, a.cols);
             float y[kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) y[e] = (float)((double)f[k][e] * (rstd * w[k][e]));
+            for (int e = 0; e < kVec; ++e) {
+                // rstd w with what its rounding lost: y is then off by little more than its own
+                // half step, and fewer codes fall to the other side of a border
+                const float p = rstd * w[k][e];
+                const float lost = fmaf(rstd, w[k][e], -p) + rest * w[k][e];
+                y[e] = fmaf(f[k][e], p, f[k][e] * lost);
+            }
             if (a.y && mine && any) {
                 Piece<T, kVec> o;
                 o.pack(y);

@@ -6,13 +6,45 @@
 namespace muon {
 namespace {
 
-// Largest of the four 16-lane rows of a wave, lane by lane of a row.
-__device__ __forceinline__ unsigned rows_max(unsigned v) {
-    auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = s[0] > s[1] ? s[0] : s[1];
-    s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return s[0] > s[1] ? s[0] : s[1];
-}
+// Magnitudes as unsigned integers, 16 bits each for the 16-bit types: `kWords` dwords for 8
+// elements, with 0 in the place of an infinity or NaN (the sum of such a magnitude and the
+// distance of the infinity from 2^15 or 2^31 has its top bit set).
+template <int T>
+struct Magnitudes {
+    static constexpr int kWords = T == kF32 ? 8 : 4;
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    typedef short i16x2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ unsigned of(unsigned w) {
+        if constexpr (T == kF32) {
+            const unsigned m = w & 0x7FFFFFFFu;
+            return m & ~(unsigned)((int)(m + 0x00800000u) >> 31);
+        } else {
+            const unsigned m = w & 0x7FFF7FFFu;
+            const unsigned short gap = T == kBF16 ? 0x0080 : 0x0400;
+            const u16x2 past = __builtin_bit_cast(u16x2, m) + (u16x2){gap, gap};
+            return m & ~__builtin_bit_cast(unsigned, __builtin_bit_cast(i16x2, past) >> (i16x2){15, 15});
+        }
+    }
+    static __device__ __forceinline__ unsigned most(unsigned a, unsigned b) {
+        if constexpr (T == kF32) return max(a, b);
+        else return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+    }
+    // the larger half of a dword of two, in fp32's bits
+    static __device__ __forceinline__ unsigned half_bits(unsigned m) {
+        if constexpr (T == kF32) return m;
+        else if constexpr (T == kBF16) return m << 16;
+        else return __float_as_uint((float)__builtin_bit_cast(_Float16, (unsigned short)m));
+    }
+    static __device__ __forceinline__ unsigned bits(unsigned m) {
+        if constexpr (T == kF32) return m;
+        else return half_bits(max(m & 0xFFFFu, m >> 16));
+    }
+    // element e's magnitude of `kWords` dwords, in fp32's bits
+    static __device__ __forceinline__ unsigned element(const unsigned* w, int e) {
+        if constexpr (T == kF32) return w[e];
+        else return half_bits((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+    }
+};
 
 __device__ __forceinline__ void put_power(uint8_t* row, int at, int blocks, unsigned byte) {
     row[at] = (uint8_t)byte;
@@ -35,34 +67,38 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     const int row_blocks = (a.rows + kBlock8 - 1) / kBlock8;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int row0 = br * kBlock8 + rg * 8, col0 = bc * kBlock8 + cg * 8;
-    float v[8][8];
+    typedef Magnitudes<T> M;
+    constexpr int kParts = 8 / E::kVec, kWords = M::kWords;
+    auto most = [](unsigned x, unsigned y) { return M::most(x, y); };
+    u32x4 raw[8][kParts];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const elem* x = reinterpret_cast<const elem*>(a.x) + (int64_t)(row0 + p) * a.stride + col0;
         if (row0 + p < a.rows && col0 + 8 <= a.cols) {
 #pragma unroll
-            for (int q = 0; q < 8 / E::kVec; ++q) E::unpack(load16(x + q * E::kVec), v[p] + q * E::kVec);
+            for (int q = 0; q < kParts; ++q) raw[p][q] = load16(x + q * E::kVec);
         } else {
+            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[p][e] = row0 + p < a.rows && col0 + e < a.cols ? (float)x[e] : 0.f;
+            for (int e = 0; e < 8; ++e) f[e] = row0 + p < a.rows && col0 + e < a.cols ? (float)x[e] : 0.f;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) raw[p][q] = E::pack(f + q * E::kVec);
         }
     }
-    unsigned row_top[8], col_top[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) row_top[e] = col_top[e] = 0;
+    unsigned row_top[8], cols_top[kWords], col_top[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const unsigned u = finite_bits(v[p][e]);
-            row_top[p] = max(row_top[p], u);
-            col_top[e] = max(col_top[e], u);
+        for (int i = 0; i < kWords; ++i) {
+            const unsigned m = M::of(raw[p][i >> 2][i & 3]);
+            row_top[p] = i ? most(row_top[p], m) : m;
+            cols_top[i] = p ? most(cols_top[i], m) : m;
         }
     if constexpr (kTiles) {
         unsigned top = row_top[0];
 #pragma unroll
-        for (int p = 1; p < 8; ++p) top = max(top, row_top[p]);
-        top = lanes_max<64>(top);
+        for (int p = 1; p < 8; ++p) top = most(top, row_top[p]);
+        top = lanes_max<64>(M::bits(top));
         if ((threadIdx.x & 63) == 0) tops[wave][0] = top;
         __syncthreads();
         top = max(max(tops[0][0], tops[1][0]), max(tops[2][0], tops[3][0]));
@@ -71,13 +107,19 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     } else {
         if constexpr (kDirect) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p) row_top[p] = lanes_max<16>(row_top[p]);
+            for (int p = 0; p < 8; ++p) row_top[p] = M::bits(lanes_reduce<16>(row_top[p], most));
         }
         if constexpr (kTransposed) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const unsigned t = rows_max(col_top[e]);
-                if ((threadIdx.x & 48) == 0) tops[wave][cg * 8 + e] = t;
+            for (int i = 0; i < kWords; ++i) {  // over the four 16-lane rows of the wave
+                auto s = __builtin_amdgcn_permlane16_swap(cols_top[i], cols_top[i], false, false);
+                const unsigned m = most(s[0], s[1]);
+                s = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+                cols_top[i] = most(s[0], s[1]);
+            }
+            if ((threadIdx.x & 48) == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) tops[wave][cg * 8 + e] = M::element(cols_top, e);
             }
             __syncthreads();
 #pragma unroll
@@ -87,15 +129,21 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
             }
         }
     }
+    auto row_of = [&](int p, float (&v)[8]) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) E::unpack(raw[p][q], v + q * E::kVec);
+    };
     if constexpr (kDirect) {
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
             if (row0 + p >= a.rows) break;
             const unsigned byte = block_power(row_top[p]);
             const float s = power_inverse(byte);
+            float v[8];
+            row_of(p, v);
             u32x2 w;
-            w.x = pack_codes(v[p][0] * s, v[p][1] * s, v[p][2] * s, v[p][3] * s);
-            w.y = pack_codes(v[p][4] * s, v[p][5] * s, v[p][6] * s, v[p][7] * s);
+            w.x = pack_codes(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+            w.y = pack_codes(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
             *reinterpret_cast<u32x2*>(a.direct.codes + (int64_t)(row0 + p) * a.direct.ld + col0) = w;
             if (cg == 0 && (!kTiles || (rg == 0 && p == 0)))
                 put_power(a.direct.scales + (int64_t)(kTiles ? br : row0 + p) * a.direct.scale_ld, bc, a.col_blocks, byte);
@@ -104,6 +152,9 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     if constexpr (kTransposed) {
         // eight rows of a column are an 8-byte slot of the turned tile's row; slot g of row c
         // sits at g ^ (c / 8), so that the 16 column groups of a write meet 16 slots
+        float v[8][8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) row_of(p, v[p]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float s = power_inverse(block_power(col_top[e]));
@@ -134,35 +185,48 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     }
 }
 
-// 16 codes a thread; HBM-bound.
+// kChunks times 16 codes a thread, all asked for before the first is written; HBM-bound.
+constexpr int kChunks = 1;
 template <int T>
 __global__ __launch_bounds__(256) void k_dequantise8(Dequant8Args a) {
     typedef Elem<T> E;
     typedef typename E::type elem;
-    const unsigned i = blockIdx.x * 256u + threadIdx.x;
-    if (i >= a.total) return;
-    unsigned row = i;
-    if (a.per_row > 1) row = (unsigned)(((uint64_t)__umulhi(i, a.mul) + i) >> a.shift);
-    const int col = (int)(i - row * a.per_row) * 16;
-    const u32x4 w = *reinterpret_cast<const u32x4*>(a.q.codes + (int64_t)row * a.q.ld + col);
-    const float s = power_value(a.q.scales[(int64_t)(row >> a.row_shift) * a.q.scale_ld + col / kBlock8]);
-    float f[16];
+    u32x4 w[kChunks];
+    float s[kChunks];
+    unsigned row[kChunks];
+    int col[kChunks];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], true);
-        f[4 * k] = lo[0] * s;
-        f[4 * k + 1] = lo[1] * s;
-        f[4 * k + 2] = hi[0] * s;
-        f[4 * k + 3] = hi[1] * s;
+    for (int k = 0; k < kChunks; ++k) {
+        const unsigned i = blockIdx.x * (256u * kChunks) + k * 256u + threadIdx.x;
+        row[k] = i;
+        if (a.per_row > 1) row[k] = (unsigned)(((uint64_t)__umulhi(i, a.mul) + i) >> a.shift);
+        col[k] = i < a.total ? (int)(i - row[k] * a.per_row) * 16 : a.cols;
+        if (i < a.total) {
+            w[k] = *reinterpret_cast<const u32x4*>(a.q.codes + (int64_t)row[k] * a.q.ld + col[k]);
+            s[k] = power_value(a.q.scales[(int64_t)(row[k] >> a.row_shift) * a.q.scale_ld + col[k] / kBlock8]);
+        }
     }
-    elem* y = reinterpret_cast<elem*>(a.y) + (int64_t)row * a.stride + col;
-    if (col + 16 <= a.cols) {
 #pragma unroll
-        for (int k = 0; k < 16 / E::kVec; ++k) put_stream16(y + k * E::kVec, E::pack(f + k * E::kVec));
-    } else {
+    for (int k = 0; k < kChunks; ++k) {
+        if (col[k] >= a.cols) break;
+        float f[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (col + k < a.cols) y[k] = (elem)f[k];
+        for (int q = 0; q < 4; ++q) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k][q], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k][q], true);
+            f[4 * q] = lo[0] * s[k];
+            f[4 * q + 1] = lo[1] * s[k];
+            f[4 * q + 2] = hi[0] * s[k];
+            f[4 * q + 3] = hi[1] * s[k];
+        }
+        elem* y = reinterpret_cast<elem*>(a.y) + (int64_t)row[k] * a.stride + col[k];
+        if (col[k] + 16 <= a.cols) {
+#pragma unroll
+            for (int q = 0; q < 16 / E::kVec; ++q) put_stream16(y + q * E::kVec, E::pack(f + q * E::kVec));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (col[k] + q < a.cols) y[q] = (elem)f[q];
+        }
     }
 }
 
@@ -185,7 +249,7 @@ hipError_t launch_quantise8(int dtype, bool tiles, const Quant8Args& a, hipStrea
 }
 
 hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s) {
-    const dim3 grid((a.total + 255) / 256), block(256);
+    const dim3 grid((a.total + (256 * kChunks - 1)) / (256 * kChunks)), block(256);
     if (a.dtype == kF32) hipLaunchKernelGGL(k_dequantise8<kF32>, grid, block, 0, s, a);
     else if (a.dtype == kBF16) hipLaunchKernelGGL(k_dequantise8<kBF16>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(k_dequantise8<kF16>, grid, block, 0, s, a);

@@ -41,11 +41,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* q) {
     return __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(q), (short)0, 0x7FFFFFFF, 0x00020000);
 }
 
-// The products of one fragment pair over 64 k. Narrow: one scaled 8-bit instruction. Wide: the
-// codes become bf16 (exact, powers included) and go through four bf16 instructions, whose sums
-// are as good as a sequence of fp32 additions; the 8-bit instruction rounds inside (the sum of
-// 64 products is off by 2^-16 of it on gaussian codes, 2^-12 of the sum of magnitudes at most
-// on codes of any size), which a 16-bit result does not show and an fp32 one does.
+// Two ways to multiply. Narrow: the scaled 8-bit instructions. They round inside (the sum of 64
+// products is off by 2^-16 of it on gaussian codes, 2^-12 of the sum of magnitudes at most on
+// codes of any size), which a 16-bit result does not show and an fp32 one does. Wide: eight codes
+// become bf16, exactly and with their powers, for bf16 instructions at half the rate, whose sums
+// are as good as a sequence of fp32 additions.
+__device__ __forceinline__ bf16x8 widen(unsigned lo, unsigned hi, float power) {
+    const bf162 w[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false),
+                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true),
+                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false),
+                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true)};
+    return bf16x8{w[0][0], w[0][1], w[1][0], w[1][1], w[2][0], w[2][1], w[3][0], w[3][1]};
+}
+
 constexpr int kRaster = 8;  // tile rows that are walked together, so that their B panels meet in L2
 
 struct TileAt {
@@ -222,11 +230,6 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
                 sa[f] = power_value((pa[f] >> sh) & 255u);
                 sb[f] = power_value((pb[f] >> sh) & 255u);
             }
-            auto widen = [](unsigned lo, unsigned hi, float s) {
-                const bf162 w[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true),
-                                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true)};
-                return bf16x8{w[0][0], w[0][1], w[1][0], w[1][1], w[2][0], w[2][1], w[3][0], w[3][1]};
-            };
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 bf16x8 wa[T], wb[T];
@@ -362,6 +365,255 @@ __global__ __launch_bounds__(256, kSide == 256 ? 1 : 2) void k_matmul8(Mat8Args 
     matmul8_tile<kSide, kWide>(a, smem);
 }
 
+// c[row][col] of one fp32 sum.
+__device__ __forceinline__ void put1(const Mat8Args& a, int row, int col, float f) {
+    const int64_t at = (int64_t)row * a.ldc + col;
+    if (a.dtype == kF32) {
+        float* c = reinterpret_cast<float*>(a.c) + at;
+        *c = a.accumulate ? *c + f : f;
+    } else if (a.dtype == kBF16) {
+        unsigned short* c = reinterpret_cast<unsigned short*>(a.c) + at;
+        *c = f2bf(a.accumulate ? bf2f(*c) + f : f);
+    } else {
+        _Float16* c = reinterpret_cast<_Float16*>(a.c) + at;
+        *c = (_Float16)(a.accumulate ? (float)*c + f : f);
+    }
+}
+
+// Few rows of A and a small B: bound by latency, in one launch. A wave takes 16 rows of B with all
+// rows of A (kM x 16) and goes along k, kSteps steps of 128 at a time, the next ones asked for
+// before the present ones are waited for.
+// `share` waves of a block take turns at the steps of the same rows where B has too few rows to
+// give every compute unit 8 waves; their sums meet in LDS, in the waves' order. The block's other
+// waves take other rows, and find the same pieces of A in the cache. Fragments come straight from
+// memory: a lane holds row l % 16, chunks l / 16 and 4 + l / 16 of the 128 bytes (the order of k
+// inside a block is free, as a block has one power), so that a load covers 64 contiguous bytes of
+// 16 rows.
+constexpr int kFewWaves = 8;  // most waves of a block
+constexpr int kUnits = 256;   // compute units
+
+template <int kM, bool kWide>
+__device__ __forceinline__ void matmul8_few(const Mat8Args& a, float* red) {
+    constexpr int kSteps = kM == 1 ? 4 : 2;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int share = a.share, own = wave / share, turn = wave - own * share, per_block = waves / share;
+    const int col0 = (blockIdx.x * per_block + own) * 16;  // past the end: the last rows again, nothing is stored
+    const int s1 = a.steps;
+    const uint8_t *pa[kM], *qa[kM];
+#pragma unroll
+    for (int f = 0; f < kM; ++f) {
+        const int r = min(f * 16 + (lane & 15), a.m - 1);
+        pa[f] = a.a + (int64_t)r * a.lda + (lane >> 4) * 16;
+        qa[f] = a.as + (int64_t)(r >> a.sha) * a.lsa;
+    }
+    const int rb = min(col0 + (lane & 15), a.n - 1);
+    const uint8_t *const pb = a.b + (int64_t)rb * a.ldb + (lane >> 4) * 16, *const qb = a.bs + (int64_t)(rb >> a.shb) * a.lsb;
+    struct Piece {
+        v4i32 a[kSteps][kM][2], b[kSteps][2];
+        unsigned wa[kM], wb;
+    };
+    auto load = [&](Piece& p, int step) {
+        p.wb = *reinterpret_cast<const unsigned*>(qb + (step & ~3));
+#pragma unroll
+        for (int f = 0; f < kM; ++f) p.wa[f] = *reinterpret_cast<const unsigned*>(qa[f] + (step & ~3));
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t at = (int64_t)min(step + i, a.steps - 1) * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                p.b[i][h] = *reinterpret_cast<const v4i32*>(pb + at + h * 64);
+#pragma unroll
+                for (int f = 0; f < kM; ++f) p.a[i][f][h] = *reinterpret_cast<const v4i32*>(pa[f] + at + h * 64);
+            }
+        }
+    };
+    floatx4 acc[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) acc[m] = floatx4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Piece& p, int step) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if (step + i >= a.steps) break;
+            const int sh = 8 * (kSteps == 4 ? i : ((step & 3) + i));
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+                if constexpr (!kWide) {
+                    acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        __builtin_shufflevector(p.b[i][0], p.b[i][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                        __builtin_shufflevector(p.a[i][m][0], p.a[i][m][1], 0, 1, 2, 3, 4, 5, 6, 7), acc[m], 0, 0, 0, (int)(p.wb >> sh), 0,
+                        (int)(p.wa[m] >> sh));
+                } else {
+                    const float sb = power_value((p.wb >> sh) & 255u), sa = power_value((p.wa[m] >> sh) & 255u);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            widen(p.b[i][q >> 1][2 * (q & 1)], p.b[i][q >> 1][2 * (q & 1) + 1], sb),
+                            widen(p.a[i][m][q >> 1][2 * (q & 1)], p.a[i][m][q >> 1][2 * (q & 1) + 1], sa), acc[m], 0, 0, 0);
+                }
+            }
+        }
+    };
+    const int jump = share * kSteps;
+    int step = turn * kSteps;
+    if (step < s1) {
+        // Always a next piece (the last one again at the end): a branch around its loads would
+        // make the compiler wait for all loads where the two ways meet.
+        const int last = s1 - 1 - (s1 - 1 - step) % jump;
+        Piece now, next;
+        load(now, step);
+        while (true) {
+            load(next, min(step + jump, last));
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(now, step);
+            if ((step += jump) >= s1) break;
+            load(now, min(step + jump, last));
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(next, step);
+            if ((step += jump) >= s1) break;
+        }
+    }
+    // a lane holds columns 4 (l / 16) .. + 3 of row l % 16 of every pair of fragments
+#pragma unroll
+    for (int m = 0; m < kM; ++m) *reinterpret_cast<floatx4*>(red + ((wave * kM + m) * 64 + lane) * 4) = acc[m];
+    __syncthreads();
+    // the waves of a group write its result, columns next to each other by threads next to each other
+    for (int i = turn * 64 + lane; i < kM * 256; i += share * 64) {
+        const int c = i & 15, row = i >> 4;
+        const int at = ((row >> 4) * 64 + (c >> 2) * 16 + (row & 15)) * 4 + (c & 3);
+        float f = 0.f;
+        for (int w = 0; w < share; ++w) f += red[(own * share + w) * kM * 256 + at];
+        if (row < a.m && col0 + c < a.n) put1(a, row, col0 + c, f);
+    }
+}
+
+template <int kM, bool kWide>
+__global__ __launch_bounds__(64 * kFewWaves) void k_matmul8_few(Mat8Args a) {
+    extern __shared__ float red[];
+    matmul8_few<kM, kWide>(a, red);
+}
+
+// Few rows of A and many of B: B's bytes bound the product, and a load has to bring whole cache
+// lines (8 rows of 128 bytes; 16 rows of 64 bytes straight to registers reach three quarters of
+// the rate). A block of eight waves takes 128 rows of B, a wave 16 of them, and streams along k
+// through a ring of kStages steps in LDS; A's rows come with them, an eighth by each wave, and are
+// what the one barrier a step is for. The powers of the block's part of k are brought to LDS first.
+constexpr int kStreamSteps = 128;  // steps of a part, at most
+
+template <int kM>
+struct StreamCfg {
+    static constexpr int kStages = kM == 1 ? 7 : kM == 2 ? 6 : 5;
+    static constexpr int kStage = 128 * 128 + kM * 16 * 128;
+    static constexpr int kPowerRow = kStreamSteps + 4;
+    static constexpr int kBytes = kStages * kStage + (128 + kM * 16) * kPowerRow;
+    static_assert(kBytes <= 160 * 1024, "LDS");
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int kM, bool kWide>
+__device__ __forceinline__ void matmul8_stream(const Mat8Args& a, uint8_t* smem) {
+    typedef StreamCfg<kM> Cfg;
+    constexpr int kStages = Cfg::kStages;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int blocks = (a.n + 127) / 128, part = blockIdx.x / blocks, col0 = (blockIdx.x - part * blocks) * 128;
+    const int fours = (a.steps + 3) >> 2;
+    const int s0 = 4 * (int)((int64_t)part * fours / a.splits);
+    const int s1 = min(a.steps, 4 * (int)((int64_t)(part + 1) * fours / a.splits));
+    const int nk = s1 - s0;
+    const __amdgpu_buffer_rsrc_t ra = resource(a.a + (int64_t)s0 * 128);
+    const __amdgpu_buffer_rsrc_t rb = resource(a.b + (int64_t)col0 * a.ldb + (int64_t)s0 * 128);
+    uint32_t offb[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = wave * 16 + q * 8 + (lane >> 3);
+        offb[q] = (uint32_t)min(r, a.n - 1 - col0) * (uint32_t)a.ldb + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    }
+    const int rowa = wave * 2 * kM + (lane >> 3);
+    const uint32_t offa = (uint32_t)min(rowa, a.m - 1) * (uint32_t)a.lda + ((lane & 7) ^ ((rowa >> 1) & 7)) * 16;
+    auto load = [&](int step) {
+        uint8_t* to = smem + step % kStages * Cfg::kStage;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + (wave * 2 + q) * 1024), 16, offb[q], step * 128, 0, 0);
+        if (lane < 16 * kM)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(to + 128 * 128 + wave * 256 * kM), 16, offa, step * 128, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        if (i < nk) load(i);
+    // powers, four steps a dword: B's 128 rows, then A's
+    uint8_t* const powers = smem + kStages * Cfg::kStage;
+    const int words = (nk + 3) >> 2;
+    for (int i = threadIdx.x; i < (128 + kM * 16) * words; i += 512) {
+        const int r = i / words, w = i - r * words;
+        const uint8_t* from = r < 128 ? a.bs + (int64_t)(min(col0 + r, a.n - 1) >> a.shb) * a.lsb
+                                      : a.as + (int64_t)(min(r - 128, a.m - 1) >> a.sha) * a.lsa;
+        *reinterpret_cast<unsigned*>(powers + r * Cfg::kPowerRow + w * 4) = *reinterpret_cast<const unsigned*>(from + s0 + w * 4);
+    }
+    floatx4 acc[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) acc[m] = floatx4{0.f, 0.f, 0.f, 0.f};
+    const int lr = lane & 15, lg = lane >> 4, sw = (lr >> 1) & 7;
+    const uint8_t *const powb = powers + (wave * 16 + lr) * Cfg::kPowerRow, *const powa = powers + (128 + lr) * Cfg::kPowerRow;
+    for (int k = 0; k < nk; ++k) {
+        // this wave's loads of the step, then everyone's; the step before has been read by all
+        if (k + kStages - 2 < nk) wait_loads_but<3 * (kStages - 2)>();
+        else wait_loads();
+        wait_lds();
+        barrier_no_fence();
+        if (k + kStages - 1 < nk) load(k + kStages - 1);
+        const uint8_t* st = smem + k % kStages * Cfg::kStage;
+        auto frag = [&](int row, int c) { return *reinterpret_cast<const v4i32*>(st + row * 128 + ((c ^ sw) << 4)); };
+        v4i32 fb[2], fa[kM][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            fb[h] = frag(wave * 16 + lr, lg + 4 * h);
+#pragma unroll
+            for (int m = 0; m < kM; ++m) fa[m][h] = frag(128 + m * 16 + lr, lg + 4 * h);
+        }
+        const unsigned eb = powb[k];
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            const unsigned ea = powa[m * 16 * Cfg::kPowerRow + k];
+            if constexpr (!kWide) {
+                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    __builtin_shufflevector(fb[0], fb[1], 0, 1, 2, 3, 4, 5, 6, 7),
+                    __builtin_shufflevector(fa[m][0], fa[m][1], 0, 1, 2, 3, 4, 5, 6, 7), acc[m], 0, 0, 0, (int)eb, 0, (int)ea);
+            } else {
+                const float sb = power_value(eb), sa = power_value(ea);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fb[q >> 1][2 * (q & 1)], fb[q >> 1][2 * (q & 1) + 1], sb),
+                                                                     widen(fa[m][q >> 1][2 * (q & 1)], fa[m][q >> 1][2 * (q & 1) + 1], sa),
+                                                                     acc[m], 0, 0, 0);
+            }
+        }
+    }
+    Mat8Args o = a;
+    if (a.splits > 1) {
+        o.c = a.partial + (int64_t)part * a.m * a.n;
+        o.ldc = a.n;
+        o.dtype = kF32;
+        o.accumulate = 0;
+    }
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+        const int row = m * 16 + lr, col = col0 + wave * 16 + lg * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (row < a.m && col + e < a.n) put1(o, row, col + e, acc[m][e]);
+    }
+}
+
+template <int kM, bool kWide>
+__global__ __launch_bounds__(512) void k_matmul8_stream(Mat8Args a) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[StreamCfg<kM>::kBytes];
+    matmul8_stream<kM, kWide>(a, smem);
+}
+
 // Adds the parts of k in order.
 __global__ __launch_bounds__(256) void k_matmul8_join(Mat8Args a, int chunks) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -388,28 +640,86 @@ __global__ __launch_bounds__(256) void k_matmul8_join(Mat8Args a, int chunks) {
 
 }  // namespace
 
+// Few rows of A: where one piece of k is all that a wave of the small form has to do and B is
+// 16 MiB at most, its one launch wins ([1, 4096] x [4096, 4096] 9.2 us; 12.5 through LDS with the
+// parts' sum), elsewhere B goes through LDS ([8, 5120] x [30720, 5120] 31 us; 44 to 63 us in the
+// small form, [16, 5120] x [5120, 5120] 12.9; 19.1).
+// Tiles: the cut with the least estimated time. A block's step of 128 takes as many microseconds
+// as below with a block a compute unit (two blocks of 128 on one take twice as long each), its
+// start and end a few (two blocks of 128 share theirs), and parts of k are written, read and added
+// at 8 TB/s (they are still in the caches) in a launch of their own.
+// Measured on MI355X: [2048, 2048, 2048] 16.6 us in one part of 128-tiles, 29.6 in two, 33 as
+// 256-tiles; [4096, 4096, 4096] 65 us as 256-tiles, 76 as 128-tiles; [512, 5120, 5120] 30 us
+// in three parts of 128-tiles, 36 as 256-tiles; fp32 [2048, 2048, 65536] 410 us in four parts of
+// 256-tiles, 471 in two of 128-tiles and 539 in one.
 Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide) {
     Mat8Plan p{};
-    auto tiles = [&](int64_t side) { return ((m + side - 1) / side) * ((n + side - 1) / side); };
-    p.tile = tiles(256) >= 128 ? 256 : 128;
     p.splits = 1;
-    const int64_t room = p.tile == 256 ? 256 : 512, fours = (k + 511) / 512;
-    if (tiles(p.tile) < room) p.splits = (int)std::max<int64_t>(1, std::min(room / tiles(p.tile), fours / 2));
+    const int64_t steps = std::max<int64_t>(1, (k + 127) / 128), fours = (steps + 3) / 4;
+    if (m <= 64) {
+        p.few = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+        const int64_t groups = (n + 15) / 16, pieces = (steps + (p.few == 1 ? 3 : 1)) / (p.few == 1 ? 4 : 2);
+        p.share = (int)std::max<int64_t>(1, std::min({4096 / groups, int64_t(kFewWaves), pieces}));
+        if (n * k > (int64_t(16) << 20) || pieces > p.share) {
+            p.stream = 1;
+            const int64_t blocks = (n + 127) / 128;
+            // a part's powers fit LDS (parts are cut at multiples of four steps)
+            p.splits = (int)std::max((steps + kStreamSteps - 4) / (kStreamSteps - 3),
+                                     std::min(std::max<int64_t>(1, kUnits / blocks), fours / 2));
+        } else {
+            p.waves = p.share * (int)std::max<int64_t>(1, std::min<int64_t>(kFewWaves / p.share, groups / kUnits));
+        }
+    } else {
+        double best = 0;
+        for (int tile = 128; tile <= 256; tile *= 2) {
+            const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+            const double step = tile == 128 ? (wide ? 1.0 : 0.56) : (wide ? 3.1 : 1.75), ends = tile == 128 ? 4 : 8;
+            for (int64_t s = 1; s <= std::min<int64_t>(fours, 16) && (s == 1 || tiles * (s - 1) < kUnits); ++s) {
+                const double rounds = double((tiles * s + kUnits - 1) / kUnits);
+                const double turns = tile == 128 ? double((tiles * s + 2 * kUnits - 1) / (2 * kUnits)) : rounds;
+                double t = rounds * double(std::min(steps, 4 * ((fours + s - 1) / s))) * step + turns * ends;
+                if (s > 1) t += 5 + double(s) * double(m) * double(n) * 8 / 8e6;
+                if (p.tile == 0 || t < best) {
+                    best = t;
+                    p.tile = tile;
+                    p.splits = (int)s;
+                }
+            }
+        }
+    }
     if (p.splits > 1) p.partial_bytes = size_t(p.splits) * size_t(m) * size_t(n) * 4;
     return p;
 }
 
-hipError_t launch_matmul8(const Mat8Plan& p, bool wide, const Mat8Args& a, hipStream_t s) {
+template <bool kWide>
+hipError_t launch_width(const Mat8Plan& p, const Mat8Args& args, hipStream_t s) {
+    Mat8Args a = args;
+    if (p.few) {
+        if (p.stream) {
+            const dim3 grid((unsigned)((a.n + 127) / 128 * a.splits)), block(512);
+            if (p.few == 1) hipLaunchKernelGGL((k_matmul8_stream<1, kWide>), grid, block, 0, s, a);
+            else if (p.few == 2) hipLaunchKernelGGL((k_matmul8_stream<2, kWide>), grid, block, 0, s, a);
+            else hipLaunchKernelGGL((k_matmul8_stream<4, kWide>), grid, block, 0, s, a);
+            return hipGetLastError();
+        }
+        a.share = p.share;
+        const int per_block = p.waves / p.share;
+        const dim3 grid((unsigned)(((a.n + 15) / 16 + per_block - 1) / per_block)), block(64 * p.waves);
+        const size_t lds = size_t(p.waves) * p.few * 1024;
+        if (p.few == 1) hipLaunchKernelGGL((k_matmul8_few<1, kWide>), grid, block, lds, s, a);
+        else if (p.few == 2) hipLaunchKernelGGL((k_matmul8_few<2, kWide>), grid, block, lds, s, a);
+        else hipLaunchKernelGGL((k_matmul8_few<4, kWide>), grid, block, lds, s, a);
+        return hipGetLastError();
+    }
     const int64_t total = int64_t(a.tiles_m) * a.tiles_n * a.splits;
     const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(256);
-    if (p.tile == 256) {
-        if (wide) hipLaunchKernelGGL((k_matmul8<256, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_matmul8<256, false>), grid, block, 0, s, a);
-    } else {
-        if (wide) hipLaunchKernelGGL((k_matmul8<128, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_matmul8<128, false>), grid, block, 0, s, a);
-    }
+    if (p.tile == 256) hipLaunchKernelGGL((k_matmul8<256, kWide>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_matmul8<128, kWide>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+hipError_t launch_matmul8(const Mat8Plan& p, bool wide, const Mat8Args& a, hipStream_t s) {
+    return wide ? launch_width<true>(p, a, s) : launch_width<false>(p, a, s);
 }
 
 hipError_t launch_matmul8_join(const Mat8Args& a, hipStream_t s) {

@@ -14,6 +14,7 @@ namespace muon {
 namespace {
 
 constexpr int kRotThreads = 256;
+constexpr int kHeads = 4;  // heads of a thread whose loads are in flight together
 
 // kPairs pairs a lane: 32 bytes. Halves: pairs (i, i + pairs), two 16-byte vectors; adjacent:
 // pairs (2 i, 2 i + 1), one stretch.
@@ -42,25 +43,44 @@ __global__ __launch_bounds__(kRotThreads) void k_rotary(RotaryArgs a) {
     const int turned = (a.pairs + kVec - 1) / kVec, rest = a.dim - 2 * a.pairs;
     const bool copies = a.x.data != a.y.data;  // in place, what is not turned stays
     const int items = turned + (copies ? (rest + kVec - 1) / kVec : 0);
-    for (unsigned i = threadIdx.x >> a.lane_bits; i < (unsigned)rows * a.heads; i += step) {
+    struct Head {
+        const elem* x;
+        elem* y;
+        const float2* cs;
+    };
+    auto head = [&](unsigned i) {
         unsigned r = i;
         if (a.heads > 1) r = (unsigned)(((uint64_t)__umulhi(i, a.heads_mul) + i) >> a.heads_shift);
         const unsigned h = i - r * a.heads;
         const uint32_t at = first + r, b = at / a.tokens, t = at - b * a.tokens;
-        const elem* x = reinterpret_cast<const elem*>(a.x.data) + (int64_t)b * a.x.sb + (int64_t)t * a.x.st + (int64_t)h * a.x.sh;
-        elem* y = reinterpret_cast<elem*>(a.y.data) + (int64_t)b * a.y.sb + (int64_t)t * a.y.st + (int64_t)h * a.y.sh;
-        for (int j = j0; j < items; j += lanes) {
-            if (j < turned) {
-                const int p0 = j * kVec;
-                const float2* cs = table + r * a.pairs + p0;
-                const int e0 = kAdjacent ? 2 * p0 : p0, e1 = kAdjacent ? e0 + kVec : a.pairs + p0;
-                if (p0 + kVec <= a.pairs) {
+        return Head{reinterpret_cast<const elem*>(a.x.data) + (int64_t)b * a.x.sb + (int64_t)t * a.x.st + (int64_t)h * a.x.sh,
+                    reinterpret_cast<elem*>(a.y.data) + (int64_t)b * a.y.sb + (int64_t)t * a.y.st + (int64_t)h * a.y.sh,
+                    table + r * a.pairs};
+    };
+    const unsigned end = (unsigned)rows * a.heads;
+    for (int j = j0; j < items; j += lanes) {
+        const int p0 = j * kVec, e0 = kAdjacent ? 2 * p0 : p0, e1 = kAdjacent ? e0 + kVec : a.pairs + p0;
+        if (p0 + kVec <= a.pairs) {
+            // kHeads heads at a time: their loads are in flight together
+            for (unsigned i = threadIdx.x >> a.lane_bits; i < end; i += kHeads * step) {
+                Head hd[kHeads];
+                u32x4 raw[kHeads][2];
+#pragma unroll
+                for (int u = 0; u < kHeads; ++u)
+                    if (i + u * step < end) {
+                        hd[u] = head(i + u * step);
+                        raw[u][0] = load16(hd[u].x + e0);
+                        raw[u][1] = load16(hd[u].x + e1);
+                    }
+#pragma unroll
+                for (int u = 0; u < kHeads; ++u) {
+                    if (i + u * step >= end) break;
                     float f[2][kVec], o[2][kVec];
-                    E::unpack(load16(x + e0), f[0]);
-                    E::unpack(load16(x + e1), f[1]);
+                    E::unpack(raw[u][0], f[0]);
+                    E::unpack(raw[u][1], f[1]);
 #pragma unroll
                     for (int k = 0; k < kVec; ++k) {
-                        const float2 w = cs[k];
+                        const float2 w = hd[u].cs[p0 + k];
                         if constexpr (kAdjacent) {
                             const int v = 2 * k / kVec, e = 2 * k % kVec;
                             o[v][e] = f[v][e] * w.x - f[v][e + 1] * w.y;
@@ -70,22 +90,27 @@ __global__ __launch_bounds__(kRotThreads) void k_rotary(RotaryArgs a) {
                             o[1][k] = f[0][k] * w.y + f[1][k] * w.x;
                         }
                     }
-                    put_stream16(y + e0, E::pack(o[0]));
-                    put_stream16(y + e1, E::pack(o[1]));
-                } else {
-                    for (int k = 0; p0 + k < a.pairs; ++k) {
-                        const float2 w = cs[k];
-                        const int ep = kAdjacent ? e0 + 2 * k : e0 + k, eq = kAdjacent ? ep + 1 : e1 + k;
-                        const float p = (float)x[ep], q = (float)x[eq];
-                        y[ep] = (elem)(p * w.x - q * w.y);
-                        y[eq] = (elem)(p * w.y + q * w.x);
-                    }
+                    put_stream16(hd[u].y + e0, E::pack(o[0]));
+                    put_stream16(hd[u].y + e1, E::pack(o[1]));
                 }
-            } else {
-                const int e = 2 * a.pairs + (j - turned) * kVec;
-                if (e + kVec <= a.dim) put_stream16(y + e, load16(x + e));
-                else
-                    for (int k = e; k < a.dim; ++k) y[k] = x[k];
+            }
+        } else {
+            for (unsigned i = threadIdx.x >> a.lane_bits; i < end; i += step) {
+                const Head hd = head(i);
+                if (j < turned) {  // the pairs that are left over
+                    for (int k = 0; p0 + k < a.pairs; ++k) {
+                        const float2 w = hd.cs[p0 + k];
+                        const int ep = kAdjacent ? e0 + 2 * k : e0 + k, eq = kAdjacent ? ep + 1 : e1 + k;
+                        const float p = (float)hd.x[ep], q = (float)hd.x[eq];
+                        hd.y[ep] = (elem)(p * w.x - q * w.y);
+                        hd.y[eq] = (elem)(p * w.y + q * w.x);
+                    }
+                } else {
+                    const int e = 2 * a.pairs + (j - turned) * kVec;
+                    if (e + kVec <= a.dim) put_stream16(hd.y + e, load16(hd.x + e));
+                    else
+                        for (int k = e; k < a.dim; ++k) hd.y[k] = hd.x[k];
+                }
             }
         }
     }
