@@ -42,6 +42,8 @@ from .add_norm import (  # noqa: F401
 )
 from .blocks8 import (  # noqa: F401
     Blocks8,
+    Weight8,
+    linear8,
     matmul8,
     matmul8_workspace_bytes,
     quantise8,
@@ -57,7 +59,7 @@ from .norms import (  # noqa: F401
     norm_forward,
     rms_norm,
 )
-from .rotary import (  # noqa: F401
+from .rotary_positions import (  # noqa: F401
     RotaryAxes,
     rotary,
     rotary_apply,

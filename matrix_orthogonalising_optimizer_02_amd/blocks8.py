@@ -213,9 +213,10 @@ def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = 
 
     With quantise8's results of a layer's x, weight and dy: y = (x, weight), dx = (dy, weight
     transposed), dweight = (dy transposed, x transposed). products 8: by the 8-bit matrix
-    instructions, which round inside (2^-16 of the result on normally distributed values); 16:
-    widened to bfloat16, exactly, with sums as of fp32 additions, at half the rate; None: 16 for
-    a float32 result, 8 for others. workspace: optional uint8 buffer of
+    instructions, which drop bits below 2^-13 of the largest in every eight products (the result
+    is off by 2^-16 of it on normally distributed values); 16: widened to bfloat16, exactly, with
+    sums as of fp32 additions, at half the rate; None: 16 for a float32 result, 8 for others.
+    workspace: optional uint8 buffer of
     matmul8_workspace_bytes().
     """
     torch = B._torch()
@@ -256,3 +257,89 @@ def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = 
     if rc:
         B._check(rc, "matmul8")
     return out
+
+
+class Weight8:
+    """A layer's weight [out, in] in 8 bits, as both products that read it want it: `direct`
+    for y = x w^T and `transposed` for dx = dy w, a power of two for every 128 x 128 elements.
+    Kept between steps; `update` follows the weight after one (HybridOptimizer does it for the
+    weights that it is told of)."""
+
+    def __init__(self, weight, stream=None):
+        if not isinstance(weight, B._torch().Tensor) or weight.dim() != 2:
+            raise ValueError("weight must be a 2-D torch.Tensor")
+        self.direct, self.transposed = quantise8(weight.detach(), tiles=True, transposed=True, stream=stream)
+        self.version = 0
+
+    @property
+    def shape(self):
+        return self.direct.shape
+
+    def update(self, weight, stream=None):
+        """Takes the weight's present values, into the same memory."""
+        if tuple(weight.shape) != self.shape:
+            raise ValueError(f"weight must have shape {self.shape}")
+        quantise8(weight.detach(), tiles=True, out=self.direct, out_transposed=self.transposed, stream=stream)
+        self.version += 1
+
+
+_function = None
+
+
+def _autograd_function():
+    """The autograd function, made at its first use: torch is imported lazily."""
+    global _function
+    if _function is not None:
+        return _function
+    torch = B._torch()
+
+    class Linear8(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, weight8, products):
+            ctx.shape, ctx.dtype, ctx.weight_dtype = x.shape, x.dtype, weight.dtype
+            w8 = Weight8(weight) if weight8 is None else weight8
+            ctx.w8, ctx.version, ctx.products = w8, w8.version, products
+            x8, ctx.x8t = quantise8(x, transposed=ctx.needs_input_grad[1])
+            return matmul8(x8, w8.direct, dtype=x.dtype).view(*x.shape[:-1], w8.shape[0])
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            if ctx.w8.version != ctx.version:
+                raise RuntimeError("the weight's 8-bit form was updated after the forward pass")
+            want_x, want_w = ctx.needs_input_grad[:2]
+            try:
+                _rows_of(dy, "dy")
+            except ValueError:  # an expanded or transposed gradient
+                dy = dy.contiguous()
+            dy8, dy8t = quantise8(dy, direct=want_x, transposed=want_w) if want_x or want_w else (None, None)
+            dx = matmul8(dy8, ctx.w8.transposed, dtype=ctx.dtype).view(ctx.shape) if want_x else None
+            dw = matmul8(dy8t, ctx.x8t, dtype=ctx.weight_dtype, products=ctx.products) if want_w else None
+            return dx, dw, None, None
+
+    _function = Linear8
+    return Linear8
+
+
+def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
+    """x weight^T for torch.autograd with all three products in 8 bits: the output, x's gradient
+    (both in x's dtype) and the weight's (in the weight's dtype, fp32 as Muon takes it).
+
+    x [..., in], weight [out, in], each float32, bfloat16 or float16. x and the gradient are
+    quantised by 128 elements along what each product sums over; for the weight's gradient x is
+    kept in 8 bits. weight8: the weight's 8-bit form, kept up to date by the caller; made in the
+    call without one. weight_grad_products: matmul8's `products` for the weight's gradient
+    (8: twice the rate, 2^-16 rounding; default 16 for a float32 weight).
+    """
+    torch = B._torch()
+    for t, name in ((x, "x"), (weight, "weight")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"weight must be 2-D with x's {x.shape[-1] if x.dim() else 0} elements a row")
+    if weight8 is not None:
+        if not isinstance(weight8, Weight8):
+            raise TypeError("weight8 must be a Weight8")
+        if weight8.shape != tuple(weight.shape) or weight8.direct.device != x.device:
+            raise ValueError(f"weight8 must have shape {tuple(weight.shape)} and live on {x.device}")
+    return _autograd_function().apply(x, weight, weight8, weight_grad_products)

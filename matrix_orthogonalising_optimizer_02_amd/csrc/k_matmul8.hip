@@ -41,11 +41,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* q) {
     return __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(q), (short)0, 0x7FFFFFFF, 0x00020000);
 }
 
-// Two ways to multiply. Narrow: the scaled 8-bit instructions. They round inside (the sum of 64
-// products is off by 2^-16 of it on gaussian codes, 2^-12 of the sum of magnitudes at most on
-// codes of any size), which a 16-bit result does not show and an fp32 one does. Wide: eight codes
-// become bf16, exactly and with their powers, for bf16 instructions at half the rate, whose sums
-// are as good as a sequence of fp32 additions.
+// Two ways to multiply. Narrow: the scaled 8-bit instructions. They add products in groups of
+// eight, in which bits below 2^-13 of the largest product are dropped (found with one large and
+// one small product at every pair of places), and the groups in fp32: a sum is off by 2^-16 of
+// it, root mean square, on normally distributed values, and by 2^-10 of its magnitudes' sum at
+// most. A 16-bit result does not show that, an fp32 one does. Wide: eight codes become bf16,
+// exactly and with their powers, for bf16 instructions at half the rate, whose sums are as good
+// as a sequence of fp32 additions.
 __device__ __forceinline__ bf16x8 widen(unsigned lo, unsigned hi, float power) {
     const bf162 w[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false),
                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true),

@@ -17,6 +17,7 @@ from __future__ import annotations
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import binding as B
+from .blocks8 import Weight8
 from .multi import AdamWMulti, GradNorm
 
 BLOCK_PREFIX = "blocks."
@@ -111,14 +112,21 @@ class HybridOptimizer:
     factor stays on the device: Muon's gradients are scaled in place, AdamW's where they
     are read. `grad_norm` then holds the last step's norm and factor (float32 [2]).
 
+    weights8: names of 2-D parameters whose 8-bit forms (Weight8, for linear8 and matmul8) the
+    optimizer keeps: `weights8[name]` follows the parameter after every step, in one more
+    launch each. Who changes parameters otherwise calls update_weights8().
+
     With adamw_state_bits no gradient is kept after the step that it was given to; who
     captures a step into a graph keeps its gradients for the replays.
     """
 
     def __init__(self, named_params: Dict[str, "object"], muon_hp: Optional[B.MuonHParams] = None,
                  adamw_hp: Optional[B.AdamWHParams] = None, adamw_state_bits: Optional[int] = None,
-                 max_grad_norm: Optional[float] = None, seed: int = 0):
+                 max_grad_norm: Optional[float] = None, seed: int = 0, weights8: Sequence[str] = ()):
         import torch
+        for n in weights8:
+            if n not in named_params or named_params[n].dim() != 2:
+                raise ValueError(f"weights8 names {n!r}, which is no 2-D parameter")
         if adamw_state_bits not in (None, 8, 32):
             raise ValueError("adamw_state_bits must be None, 8 or 32")
         if max_grad_norm is not None and adamw_state_bits is None:
@@ -146,6 +154,7 @@ class HybridOptimizer:
         self._norm = self._muon_norm = None
         self.grad_norm = None
         self.step_count = 0
+        self.weights8 = {n: Weight8(named_params[n]) for n in weights8}
 
     def step(self, grads: Dict[str, "object"], stream=None, update_rms=None, counter=None, lr=None):
         """One step. What either half refuses is refused before anything is written: weights,
@@ -188,6 +197,12 @@ class HybridOptimizer:
                     if held is not None:
                         held.release_grads()
         self.step_count += 1
+        self.update_weights8(stream)
+
+    def update_weights8(self, stream=None):
+        """The 8-bit forms of `weights8` from the parameters' present values."""
+        for n, w in self.weights8.items():
+            w.update(self.params[n], stream)
 
     def _check_adamw(self, g, stream, at, lr):
         """Gives AdamW its gradients; all that its step refuses is refused here."""
