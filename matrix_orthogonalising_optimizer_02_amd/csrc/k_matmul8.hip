@@ -119,29 +119,41 @@ __device__ __forceinline__ void put8(const Mat8Args& a, int row, int col, float*
     }
 }
 
-// A block of four waves (2 x 2) computes kSide x kSide of C, a wave a quarter of it in 32 x 32
-// accumulators. A step is 128 of k: both operands' tiles come straight to LDS (a load of 1 KiB
-// brings 8 rows of 128 bytes, whole cache lines), two stages. The wave reads a half step's
-// fragments (64 of k) while the matrix instructions work on the half before, and once all waves
-// hold a step's second half in registers, one barrier a step, its stage is filled again: a load
-// has one and a half steps to arrive. Rows of LDS are 128 bytes; chunk c of row r (16 bytes)
-// sits at c ^ ((r / 2) & 7), so that 16 lanes that read the same chunk of 16 rows meet all banks.
-// Rows past the matrix's end are its last row again, and are not stored.
+// A block computes kSide x kSide of C in 32 x 32 accumulators, a wave a part of it: eight waves
+// (2 x 4, two a SIMD, each 128 x 64) for 256 x 256 in the 8-bit instructions, else four (2 x 2). A
+// step is 128 of k: both operands' tiles come straight to LDS (a load of 1 KiB brings 8 rows of 128
+// bytes, whole cache lines), two stages. The wave reads a half step's fragments (64 of k) while the
+// matrix instructions work on the half before, and once all waves hold a step's second half in
+// registers, one barrier a step, its stage is filled again. Rows of LDS are 128 bytes; chunk c of
+// row r (16 bytes) sits at c ^ ((r / 2) & 7), so that 16 lanes that read the same chunk of 16 rows
+// meet all banks. Rows past the matrix's end are its last row again, and are not stored.
+// What bounds 256 x 256: a step's matrix instructions take 1.0 us, its LDS reads hide behind them
+// in part, and 64 KiB a compute unit and step come from L2 at some 65 lines in flight; asking for
+// half of a step's loads a half step later, A's and B's in turn, took [8192, 20480, 5120] from 718
+// to 665 us (2.6 PFLOP/s; 3.9 with nothing but matrix instructions). Halves of lines (64 of k a
+// stage, four stages) took 759 us, k begun at another place by every block 735 to 939 us, four
+// waves of 128 x 128 a block 705 us.
 template <int kSide, bool kWide>
-struct Mat8Lds {
-    static constexpr int kEpi = 32 * (kSide / 2 + 4) * 4;                       // a wave's 32 staged rows of the result
-    static constexpr int kBytes = std::max(2 * 2 * kSide * 128, 4 * kEpi);
+struct Mat8Cfg {
+    static constexpr bool kDense = kSide == 256 && !kWide;                      // two waves a SIMD of 256 registers
+    static constexpr int kWavesN = kDense ? 4 : 2, kWaves = 2 * kWavesN;        // 2 waves along m
+    static constexpr int kM = kSide / 2, kN = kSide / kWavesN;                  // a wave's part
+    static constexpr int kEpi = 32 * (kN + 4) * 4;                              // its 32 staged rows of the result
+    static constexpr int kPowers = 2 * kSide * 4;                               // both operands' powers of four steps
+    static constexpr int kLds = std::max(2 * 2 * kSide * 128 + 2 * kPowers, kWaves * kEpi);
 };
 
 template <int kSide, bool kWide>
 __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
-    constexpr int kHalf = kSide / 2, T = kHalf / 32;    // a wave's side, and in fragments
-    constexpr int kLoads = kSide / 32;                  // 1 KiB loads of a wave, an operand and a step
-    constexpr int kTile = kSide * 128, kStage = 2 * kTile;
-    constexpr int kRowF = kHalf + 4;                    // floats of a staged row of the result
-    constexpr int kEpi = Mat8Lds<kSide, kWide>::kEpi;
+    typedef Mat8Cfg<kSide, kWide> Cfg;
+    constexpr int kM = Cfg::kM, kN = Cfg::kN, TM = kM / 32, TN = kN / 32;  // a wave's part, and in fragments
+    constexpr int kLoads = kSide / 8 / Cfg::kWaves;     // 1 KiB loads of a wave, an operand and a step
+    // A's two stages, then B's: a wave's reads of both are within an instruction's offset of one address
+    constexpr int kTile = kSide * 128;
+    constexpr int kRowF = kN + 4;                       // floats of a staged row of the result
+    constexpr int kEpi = Cfg::kEpi;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / Cfg::kWavesN, wn = wave % Cfg::kWavesN;
     TileAt t;
     if (!tile_of(a, t)) return;
     // this part's steps: cut at multiples of four, whose powers are one dword of a row
@@ -155,124 +167,173 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
     const __amdgpu_buffer_rsrc_t rb = resource(a.b + (int64_t)col0 * a.ldb + (int64_t)s0 * 128);
     const __amdgpu_buffer_rsrc_t rsa = resource(a.as + (int64_t)(row0 >> a.sha) * a.lsa + s0);
     const __amdgpu_buffer_rsrc_t rsb = resource(a.bs + (int64_t)(col0 >> a.shb) * a.lsb + s0);
-    uint32_t offa[kLoads], offb[kLoads], offsa[T], offsb[T];
+    uint32_t offa[kLoads], offb[kLoads];
+    // Eight tiles next to each other along m run at the same time on one XCD and read the same rows
+    // of B, and four along n the same of A. Each begins with other rows (the wave's loads in another
+    // turn): the rows that a block asks for first come from memory, and the other blocks find them in
+    // L2 when their turn comes (718 to 680 us by itself; tiles of 128, of few steps, show nothing).
+    const int turn_a = kSide == 256 ? t.tj * (kLoads / 4) : 0, turn_b = kSide == 256 ? t.ti * kLoads / 8 : 0;
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-        const int r = (wave * kLoads + q) * 8 + (lane >> 3);
-        const uint32_t chunk = (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16;
-        offa[q] = (uint32_t)min(r, a.m - 1 - row0) * (uint32_t)a.lda + chunk;
-        offb[q] = (uint32_t)min(r, a.n - 1 - col0) * (uint32_t)a.ldb + chunk;
+        const int r = (wave * kLoads + (q + turn_a) % kLoads) * 8 + (lane >> 3);
+        offa[q] = (uint32_t)min(r, a.m - 1 - row0) * (uint32_t)a.lda + (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16;
+        const int s = (wave * kLoads + (q + turn_b) % kLoads) * 8 + (lane >> 3);
+        offb[q] = (uint32_t)min(s, a.n - 1 - col0) * (uint32_t)a.ldb + (uint32_t)((lane & 7) ^ ((s >> 1) & 7)) * 16;
     }
+    // The powers of four steps, a dword a row, come to LDS as well: 64 rows a load, A's 256 (128)
+    // first, in two places in turn.
+    constexpr int kPowerLoads = 2 * kSide / 64 / Cfg::kWaves;
+    uint8_t* const powers = smem + 4 * kTile;
+    uint32_t offp[kPowerLoads];
 #pragma unroll
-    for (int f = 0; f < T; ++f) {
-        const int r = f * 32 + (lane & 31);
-        offsa[f] = (uint32_t)((min(row0 + wm * kHalf + r, a.m - 1) >> a.sha) - (row0 >> a.sha)) * (uint32_t)a.lsa;
-        offsb[f] = (uint32_t)((min(col0 + wn * kHalf + r, a.n - 1) >> a.shb) - (col0 >> a.shb)) * (uint32_t)a.lsb;
+    for (int q = 0; q < kPowerLoads; ++q) {
+        const int r = (wave * kPowerLoads + q) * 64 % kSide + lane;
+        const bool is_b = (wave * kPowerLoads + q) * 64 >= kSide;
+        offp[q] = is_b ? (uint32_t)((min(col0 + r, a.n - 1) >> a.shb) - (col0 >> a.shb)) * (uint32_t)a.lsb
+                       : (uint32_t)((min(row0 + r, a.m - 1) >> a.sha) - (row0 >> a.sha)) * (uint32_t)a.lsa;
     }
-    auto load = [&](int stage, int step, int q) {  // q < 2 kLoads
-        uint8_t* to = smem + stage * kStage + (q < kLoads ? 0 : kTile) + (wave * kLoads + q % kLoads) * 1024;
-        if (q < kLoads) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)to, 16, offa[q], step * 128, 0, 0);
-        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)to, 16, offb[q - kLoads], step * 128, 0, 0);
-    };
-    // powers of the present four steps and of the next four, a dword a fragment
-    unsigned pa[T], pb[T], na[T], nb[T];
     auto load_powers = [&](int four) {
+        const int from = min(four, (nk - 1) >> 2);  // past the end: once more, and not read
 #pragma unroll
-        for (int f = 0; f < T; ++f) {
-            na[f] = __builtin_amdgcn_raw_buffer_load_b32(rsa, offsa[f], four * 4, 0);
-            nb[f] = __builtin_amdgcn_raw_buffer_load_b32(rsb, offsb[f], four * 4, 0);
+        for (int q = 0; q < kPowerLoads; ++q) {
+            const int at = wave * kPowerLoads + q;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(at * 64 >= kSide ? rsb : rsa, (lds_ptr_t)(powers + (four & 1) * Cfg::kPowers + at * 256),
+                                                     4, offp[q], from * 4, 0, 0);
+        }
+    };
+    unsigned pa[TM], pb[TN];
+    auto read_powers = [&](int four) {
+        const unsigned* p = reinterpret_cast<const unsigned*>(powers + (four & 1) * Cfg::kPowers);
+#pragma unroll
+        for (int f = 0; f < TM; ++f) pa[f] = p[wm * kM + f * 32 + (lane & 31)];
+#pragma unroll
+        for (int f = 0; f < TN; ++f) pb[f] = p[kSide + wn * kN + f * 32 + (lane & 31)];
+    };
+    auto load = [&](int stage, int step, int i) {  // i < 2 kLoads
+        const int q = Cfg::kDense ? i >> 1 : i % kLoads;
+        if (Cfg::kDense ? i & 1 : i >= kLoads) {
+            uint8_t* to = smem + (stage + 2) * kTile + (wave * kLoads + (q + turn_b) % kLoads) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)to, 16, offb[q], step * 128, 0, 0);
+        } else {
+            uint8_t* to = smem + stage * kTile + (wave * kLoads + (q + turn_a) % kLoads) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)to, 16, offa[q], step * 128, 0, 0);
         }
     };
     // fragments of a half step: lane l holds row l % 32, 32 bytes: chunks 4 half + 2 (l / 32), + 1
-    v4i32 fa[2][T][2], fb[2][T][2];
+    // (Dense: A's have one set of registers, and are read again once both of a fragment's products
+    // are under way; a second set does not fit)
+    constexpr int kSetsA = Cfg::kDense ? 1 : 2;
+    v4i32 fa[kSetsA][TM][2], fb[2][TN][2];
+    constexpr int kFrags = 2 * (TM + TN);  // 16-byte reads of a half step
     const int sw = (lane >> 1) & 7, lrow = (lane & 31) * 128;
-    auto frag = [&](int half, int stage, int i) {  // i < 4 T: one 16-byte read
-        const int j = i & 1, f = (i >> 1) % T;
-        const bool is_b = i >= 2 * T;
+    auto frag = [&](int half, int stage, int i) {  // i < kFrags
+        const bool is_b = i >= 2 * TM;
+        const int j = i & 1, f = is_b ? (i >> 1) - TM : i >> 1;
         const int chunk = ((half * 4 + (lane >> 5) * 2 + j) ^ sw) * 16;
-        const uint8_t* p = smem + stage * kStage + (is_b ? kTile + wn * kHalf * 128 : wm * kHalf * 128) + f * 4096 + lrow + chunk;
+        const uint8_t* p = smem + (is_b ? 2 * kTile + wn * kN * 128 : wm * kM * 128) + lrow + chunk + stage * kTile + f * 4096;
         const v4i32 v = *reinterpret_cast<const v4i32*>(p);
         if (is_b) fb[half][f][j] = v;
-        else fa[half][f][j] = v;
+        else fa[half % kSetsA][f][j] = v;
     };
-    floatx16 acc[T][T];  // [n][m]: a lane holds four consecutive columns of one row of C
+    floatx16 acc[TN][TM];  // [n][m]: a lane holds four consecutive columns of one row of C
 #pragma unroll
-    for (int b = 0; b < T; ++b)
+    for (int b = 0; b < TN; ++b)
 #pragma unroll
-        for (int m = 0; m < T; ++m)
+        for (int m = 0; m < TM; ++m)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[b][m][r] = 0.f;
 
     auto whole = [](const v4i32 (&h)[2]) { return __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7); };
     // i-th fragment pair, snake order: two in a row differ in one operand only
     auto pair = [](int i, int& b, int& m) {
-        b = i / T;
-        m = b & 1 ? T - 1 - i % T : i % T;
+        if constexpr (Cfg::kDense) {
+            m = i / TN;
+            b = m & 1 ? TN - 1 - i % TN : i % TN;
+        } else {
+            b = i / TM;
+            m = b & 1 ? TM - 1 - i % TM : i % TM;
+        }
     };
-    // `between(slot)`, slot < T T: what is issued after the slot's matrix instructions
+    // `between(slot)`, slot < TM TN: what is issued after the slot's matrix instructions
     auto multiply = [&](int half, auto phase_c, int phase, auto between) {
         constexpr int PH = decltype(phase_c)::value;
         if constexpr (!kWide) {
 #pragma unroll
-            for (int i = 0; i < T * T; ++i) {
+            for (int i = 0; i < TM * TN; ++i) {
                 int b, m;
                 pair(i, b, m);
                 // PH < 0: the byte was moved down already
-                acc[b][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(whole(fb[half][b]), whole(fa[half][m]), acc[b][m], 0, 0,
+                acc[b][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(whole(fb[half][b]), whole(fa[half % kSetsA][m]), acc[b][m], 0, 0,
                                                                            PH < 0 ? 0 : PH, (int)pb[b], PH < 0 ? 0 : PH,
                                                                            (int)pa[m]);
                 between(i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
-            float sa[T], sb[T];
+            float sa[TM], sb[TN];
             const int sh = PH < 0 ? 0 : 8 * PH;
 #pragma unroll
-            for (int f = 0; f < T; ++f) {
-                sa[f] = power_value((pa[f] >> sh) & 255u);
-                sb[f] = power_value((pb[f] >> sh) & 255u);
-            }
+            for (int f = 0; f < TM; ++f) sa[f] = power_value((pa[f] >> sh) & 255u);
+#pragma unroll
+            for (int f = 0; f < TN; ++f) sb[f] = power_value((pb[f] >> sh) & 255u);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                bf16x8 wa[T], wb[T];
+                bf16x8 wa[TM], wb[TN];
 #pragma unroll
-                for (int f = 0; f < T; ++f) {
-                    wa[f] = widen(fa[half][f][s >> 1][2 * (s & 1)], fa[half][f][s >> 1][2 * (s & 1) + 1], sa[f]);
+                for (int f = 0; f < TM; ++f)
+                    wa[f] = widen(fa[half % kSetsA][f][s >> 1][2 * (s & 1)], fa[half % kSetsA][f][s >> 1][2 * (s & 1) + 1], sa[f]);
+#pragma unroll
+                for (int f = 0; f < TN; ++f)
                     wb[f] = widen(fb[half][f][s >> 1][2 * (s & 1)], fb[half][f][s >> 1][2 * (s & 1) + 1], sb[f]);
-                }
 #pragma unroll
-                for (int i = 0; i < T * T; ++i) {
+                for (int i = 0; i < TM * TN; ++i) {
                     int b, m;
                     pair(i, b, m);
                     acc[b][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[b], wa[m], acc[b][m], 0, 0, 0);
                 }
                 // a quarter of the slots
 #pragma unroll
-                for (int i = 0; i < (T * T) / 4; ++i) between(s * ((T * T) / 4) + i);
+                for (int i = 0; i < (TM * TN) / 4; ++i) between(s * ((TM * TN) / 4) + i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    constexpr int kSlots = T * T, kReads = (4 * T + kSlots / 2 - 1) / (kSlots / 2), kPuts = (2 * kLoads + kSlots / 2 - 1) / (kSlots / 2);
+    constexpr int kSlots = TM * TN, kReads = (kFrags + kSlots / 2 - 1) / (kSlots / 2), kPuts = 2;
+    // loads of a step that are asked for in the second half of the step two before; the others
+    // follow in the first half of the step between
+    constexpr int kEarly = kSide == 256 ? kLoads : 2 * kLoads;
+    // what slot i reads of the next half: a share of all fragments, or (dense) the one of A whose
+    // products are done, and one piece of B's
+    auto read = [&](int half, int stage, int i) {
+        if constexpr (Cfg::kDense) {
+            static_assert(TN == 2 && TM == 4, "two slots a fragment of A, four pieces of B");
+            if (i & 1) {
+                frag(half, stage, 2 * (i >> 1));
+                frag(half, stage, 2 * (i >> 1) + 1);
+            } else {
+                frag(half, stage, 2 * TM + (i >> 1));
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < kReads; ++q)
+                if (i * kReads + q < kFrags) frag(half, stage, i * kReads + q);
+        }
+    };
     // one step of 128. MORE: step kt + 2 is loaded; NEXT: step kt + 1 exists. PH: kt % 4, -1
     // where it is known at run time only.
     auto step = [&](int kt, auto more_c, auto next_c, auto phase_c) {
         constexpr bool MORE = decltype(more_c)::value, NEXT = decltype(next_c)::value;
         constexpr int PH = decltype(phase_c)::value;
         const int cur = PH >= 0 ? PH & 1 : kt & 1;
-        if (PH == 0 || (PH < 0 && (kt & 3) == 0)) {
-#pragma unroll
-            for (int f = 0; f < T; ++f) {
-                pa[f] = na[f];
-                pb[f] = nb[f];
-            }
-            load_powers(min((kt >> 2) + 1, (nk - 1) >> 2));
-        }
+        if (PH == 0 || (PH < 0 && (kt & 3) == 0)) read_powers(kt >> 2);
         // without a phase the dwords move down a byte a step: byte 0 is always this step's
         multiply(0, phase_c, kt, [&](int i) {
+            if (NEXT) {
 #pragma unroll
-            for (int q = 0; q < kReads; ++q)
-                if (i * kReads + q < 4 * T) frag(1, cur, i * kReads + q);
+                for (int q = 0; q < kPuts; ++q)
+                    if (kEarly + i * kPuts + q < 2 * kLoads) load(cur ^ 1, kt + 1, kEarly + i * kPuts + q);
+            }
+            read(1, cur, i);
         });
         if (NEXT) {
             wait_lds();
@@ -280,23 +341,19 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
             barrier_no_fence();
         }
         multiply(1, phase_c, kt, [&](int i) {
+            if (i == 0 && MORE && (PH == 0 || (PH < 0 && (kt & 3) == 0))) load_powers((kt >> 2) + 1);
             if (MORE) {
 #pragma unroll
                 for (int q = 0; q < kPuts; ++q)
-                    if (i * kPuts + q < 2 * kLoads) load(cur, kt + 2, i * kPuts + q);
+                    if (i * kPuts + q < kEarly) load(cur, kt + 2, i * kPuts + q);
             }
-            if (NEXT) {
-#pragma unroll
-                for (int q = 0; q < kReads; ++q)
-                    if (i * kReads + q < 4 * T) frag(0, cur ^ 1, i * kReads + q);
-            }
+            if (NEXT) read(0, cur ^ 1, i);
         });
         if constexpr (PH < 0) {
 #pragma unroll
-            for (int f = 0; f < T; ++f) {
-                pa[f] >>= 8;
-                pb[f] >>= 8;
-            }
+            for (int f = 0; f < TM; ++f) pa[f] >>= 8;
+#pragma unroll
+            for (int f = 0; f < TN; ++f) pb[f] >>= 8;
         }
     };
     constexpr BoolC<true> Y{};
@@ -307,11 +364,11 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
         for (int q = 0; q < 2 * kLoads; ++q) load(0, 0, q);
         if (nk > 1)
 #pragma unroll
-            for (int q = 0; q < 2 * kLoads; ++q) load(1, 1, q);
+            for (int q = 0; q < kEarly; ++q) load(1, 1, q);
         wait_loads();
         barrier_no_fence();
 #pragma unroll
-        for (int i = 0; i < 4 * T; ++i) frag(0, 0, i);
+        for (int i = 0; i < kFrags; ++i) frag(0, 0, i);
         int kt = 0;
         for (; kt + 5 < nk; kt += 4) {
             step(kt, Y, Y, IntC<0>{});
@@ -336,18 +393,18 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
         o.dtype = kF32;
         o.accumulate = 0;
     }
-    const int rbase = row0 + wm * kHalf, cbase = col0 + wn * kHalf;
+    const int rbase = row0 + wm * kM, cbase = col0 + wn * kN;
 #pragma unroll
-    for (int m = 0; m < T; ++m) {
+    for (int m = 0; m < TM; ++m) {
 #pragma unroll
-        for (int b = 0; b < T; ++b)
+        for (int b = 0; b < TN; ++b)
 #pragma unroll
             for (int rg = 0; rg < 4; ++rg) {
                 const floatx4 v = {acc[b][m][4 * rg], acc[b][m][4 * rg + 1], acc[b][m][4 * rg + 2], acc[b][m][4 * rg + 3]};
                 *reinterpret_cast<floatx4*>(st + (lane & 31) * kRowF + b * 32 + rg * 8 + (lane >> 5) * 4) = v;
             }
         wait_lds();
-        constexpr int kPer = kHalf / 8;  // 8 columns a lane
+        constexpr int kPer = kN / 8;  // 8 columns a lane
 #pragma unroll
         for (int it = 0; it < 32 * kPer / 64; ++it) {
             const int c = it * 64 + lane, r = c / kPer, k = c % kPer;
@@ -362,8 +419,8 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
 }
 
 template <int kSide, bool kWide>
-__global__ __launch_bounds__(256, kSide == 256 ? 1 : 2) void k_matmul8(Mat8Args a) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[Mat8Lds<kSide, kWide>::kBytes];
+__global__ __launch_bounds__(kSide == 256 && !kWide ? 512 : 256, kSide == 256 && kWide ? 1 : 2) void k_matmul8(Mat8Args a) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Mat8Cfg<kSide, kWide>::kLds];
     matmul8_tile<kSide, kWide>(a, smem);
 }
 
@@ -714,9 +771,9 @@ hipError_t launch_width(const Mat8Plan& p, const Mat8Args& args, hipStream_t s) 
         return hipGetLastError();
     }
     const int64_t total = int64_t(a.tiles_m) * a.tiles_n * a.splits;
-    const dim3 grid((unsigned)(8 * ((total + 7) / 8))), block(256);
-    if (p.tile == 256) hipLaunchKernelGGL((k_matmul8<256, kWide>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_matmul8<128, kWide>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)(8 * ((total + 7) / 8)));
+    if (p.tile == 256) hipLaunchKernelGGL((k_matmul8<256, kWide>), grid, dim3(64 * Mat8Cfg<256, kWide>::kWaves), 0, s, a);
+    else hipLaunchKernelGGL((k_matmul8<128, kWide>), grid, dim3(64 * Mat8Cfg<128, kWide>::kWaves), 0, s, a);
     return hipGetLastError();
 }
 
