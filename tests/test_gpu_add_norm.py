@@ -284,6 +284,20 @@ def test_rotary_views_and_in_place(torch_dev, name, dim, sections):  # noqa: F81
     assert empty.shape == (batch, 0, 3 * heads, dim)
 
 
+@pytest.mark.parametrize("layout", ["halves", "adjacent"])
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+def test_rotary_in_place_of_odd_heads(torch_dev, name, layout):  # noqa: F811
+    """Heads that vectors do not divide, of fewer elements than a vector and of more vectors than
+    a wave has lanes."""
+    torch, dev = torch_dev
+    for i, (pairs, dim) in enumerate(((3, 7), (1, 2), (9, 19), (61, 125), (300, 601), (509, 1019))):
+        x = draw(torch, dev, 735 + i, 0, (40, 5, dim), dtype_of(torch, name))
+        pos = torch.arange(40, device=dev)[:, None]
+        want = check_rotary(torch, name, x, pos, (pairs,), layout)
+        assert torch.equal(check_rotary(torch, name, x, pos, (pairs,), layout, out=x), want)
+        log(f"{name} {layout} {pairs} pairs of {dim}")
+
+
 def test_rotary_own_frequencies(torch_dev):  # noqa: F811
     """Axes dealt out pair by pair."""
     torch, dev = torch_dev
