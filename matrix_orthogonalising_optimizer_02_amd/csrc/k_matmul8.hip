@@ -130,9 +130,10 @@ __device__ __forceinline__ void put8(const Mat8Args& a, int row, int col, float*
 // What bounds 256 x 256: a step's matrix instructions take 1.0 us, its LDS reads hide behind them
 // in part, and 64 KiB a compute unit and step come from L2 at some 65 lines in flight; asking for
 // half of a step's loads a half step later, A's and B's in turn, took [8192, 20480, 5120] from 718
-// to 665 us (2.6 PFLOP/s; 3.9 with nothing but matrix instructions). Halves of lines (64 of k a
+// to 655 us (2.6 PFLOP/s; 3.9 with nothing but matrix instructions). Halves of lines (64 of k a
 // stage, four stages) took 759 us, k begun at another place by every block 735 to 939 us, four
-// waves of 128 x 128 a block 705 us.
+// waves of 128 x 128 a block 705 us, blocks that stay for further tiles and load the next one's
+// first step while a result leaves 676 us (alike blocks then store at the same time).
 template <int kSide, bool kWide>
 struct Mat8Cfg {
     static constexpr bool kDense = kSide == 256 && !kWide;                      // two waves a SIMD of 256 registers
@@ -707,10 +708,10 @@ __global__ __launch_bounds__(256) void k_matmul8_join(Mat8Args a, int chunks) {
 // as below with a block a compute unit (two blocks of 128 on one take twice as long each), its
 // start and end a few (two blocks of 128 share theirs), and parts of k are written, read and added
 // at 8 TB/s (they are still in the caches) in a launch of their own.
-// Measured on MI355X: [2048, 2048, 2048] 16.6 us in one part of 128-tiles, 29.6 in two, 33 as
-// 256-tiles; [4096, 4096, 4096] 65 us as 256-tiles, 76 as 128-tiles; [512, 5120, 5120] 30 us
-// in three parts of 128-tiles, 36 as 256-tiles; fp32 [2048, 2048, 65536] 410 us in four parts of
-// 256-tiles, 471 in two of 128-tiles and 539 in one.
+// Measured on MI355X: [2048, 2048, 2048] 16 us as 128-tiles, 28 as 256-tiles; [4096, 4096, 4096]
+// 58 us as 256-tiles, 68 as 128-tiles; [2048, 5120, 20480] 212 and 285; [512, 5120, 5120] 31 us in
+// three parts of 128-tiles, 36 as 256-tiles; fp32 [2048, 2048, 65536] 408 us in four parts of
+// 256-tiles, 532 as 128-tiles.
 Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide) {
     Mat8Plan p{};
     p.splits = 1;
@@ -732,7 +733,7 @@ Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide) {
         double best = 0;
         for (int tile = 128; tile <= 256; tile *= 2) {
             const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
-            const double step = tile == 128 ? (wide ? 1.0 : 0.56) : (wide ? 3.1 : 1.75), ends = tile == 128 ? 4 : 8;
+            const double step = tile == 128 ? (wide ? 1.0 : 0.56) : (wide ? 3.1 : 1.45), ends = tile == 128 ? 4 : 8;
             for (int64_t s = 1; s <= std::min<int64_t>(fours, 16) && (s == 1 || tiles * (s - 1) < kUnits); ++s) {
                 const double rounds = double((tiles * s + kUnits - 1) / kUnits);
                 const double turns = tile == 128 ? double((tiles * s + 2 * kUnits - 1) / (2 * kUnits)) : rounds;
