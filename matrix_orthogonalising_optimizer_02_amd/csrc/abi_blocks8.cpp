@@ -130,8 +130,8 @@ MUON_API int dequantise8(const blocks8* q, void* y, int64_t stride, int32_t dtyp
         if (rc || (rc = check_matrix(y, q->rows, q->cols, stride, dtype, "y", true, ranges)) || (rc = check_overlaps(ranges)))
             return rc;
         if (q->rows == 0 || q->cols == 0) return MUON_OK;
-        const int64_t per_row = (q->cols + 15) / 16;
-        if (__int128(per_row) * q->rows > kMaxThreads - 255) return fail(MUON_ERR_TOO_LARGE, "more elements than a launch takes");
+        const int64_t vec = dtype == MUON_DTYPE_F32 ? 4 : 8, per_row = (q->cols + vec - 1) / vec;
+        if (__int128(per_row) * q->rows > kMaxThreads - 2048) return fail(MUON_ERR_TOO_LARGE, "more elements than a launch takes");
         Dequant8Args a{};
         a.q = ptr_of(q);
         a.y = y;

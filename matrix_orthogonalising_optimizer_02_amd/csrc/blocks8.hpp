@@ -38,7 +38,7 @@ struct Dequant8Args {
     Blocks8Ptr q;
     void* y;
     int64_t stride;
-    uint32_t total;        // chunks of 16 codes
+    uint32_t total;        // chunks of 16 bytes of y
     int32_t cols;
     uint32_t per_row;      // chunks of a row
     uint32_t mul;          // i / per_row = (mulhi(i, mul) + i) >> shift, 33-bit sum, for per_row > 1

@@ -56,7 +56,8 @@ __device__ __forceinline__ void put_power(uint8_t* row, int at, int blocks, unsi
 // threads share a row (its largest magnitude is a reduction over 16 lanes, its codes leave as
 // 128 contiguous bytes), and the 8 rows of a thread are 8 contiguous bytes of the transposed
 // matrix, which is put together in 16 KB of LDS. So both forms cost one read of x.
-// HBM-bound: [8192, 5120] bf16 into both forms, see the launcher.
+// HBM-bound: [8192, 5120] bf16 into both forms 34 us (5.0 TB/s), [15360, 5120] fp32 in 128 x 128
+// blocks into both 78 us (6.1 TB/s).
 template <int T, bool kTiles, bool kDirect, bool kTransposed>
 __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     typedef Elem<T> E;
@@ -185,33 +186,42 @@ __global__ __launch_bounds__(256) void k_quantise8(Quant8Args a) {
     }
 }
 
-// kChunks times 16 codes a thread, all asked for before the first is written; HBM-bound.
-constexpr int kChunks = 1;
-template <int T>
+// A lane's store is 16 bytes next to its neighbours', kChunks of them a thread, all asked for before
+// the first is written. HBM-bound: [8192, 5120] into bf16 18.5 us (two stores of a lane next to
+// each other, half of what its neighbours fill, took 26).
+constexpr int kChunks = 2;
+template <int T, bool kStream>
 __global__ __launch_bounds__(256) void k_dequantise8(Dequant8Args a) {
     typedef Elem<T> E;
     typedef typename E::type elem;
-    u32x4 w[kChunks];
+    constexpr int kVec = E::kVec, kWords = kVec / 4;
+    unsigned w[kChunks][kWords], row[kChunks];
     float s[kChunks];
-    unsigned row[kChunks];
     int col[kChunks];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
         const unsigned i = blockIdx.x * (256u * kChunks) + k * 256u + threadIdx.x;
         row[k] = i;
         if (a.per_row > 1) row[k] = (unsigned)(((uint64_t)__umulhi(i, a.mul) + i) >> a.shift);
-        col[k] = i < a.total ? (int)(i - row[k] * a.per_row) * 16 : a.cols;
+        col[k] = i < a.total ? (int)(i - row[k] * a.per_row) * kVec : a.cols;
         if (i < a.total) {
-            w[k] = *reinterpret_cast<const u32x4*>(a.q.codes + (int64_t)row[k] * a.q.ld + col[k]);
+            const unsigned* p = reinterpret_cast<const unsigned*>(a.q.codes + (int64_t)row[k] * a.q.ld + col[k]);
+            if constexpr (kWords == 2) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+                w[k][0] = v.x;
+                w[k][1] = v.y;
+            } else {
+                w[k][0] = *p;
+            }
             s[k] = power_value(a.q.scales[(int64_t)(row[k] >> a.row_shift) * a.q.scale_ld + col[k] / kBlock8]);
         }
     }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
         if (col[k] >= a.cols) break;
-        float f[16];
+        float f[kVec];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kWords; ++q) {
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k][q], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k][q], true);
             f[4 * q] = lo[0] * s[k];
             f[4 * q + 1] = lo[1] * s[k];
@@ -219,12 +229,12 @@ __global__ __launch_bounds__(256) void k_dequantise8(Dequant8Args a) {
             f[4 * q + 3] = hi[1] * s[k];
         }
         elem* y = reinterpret_cast<elem*>(a.y) + (int64_t)row[k] * a.stride + col[k];
-        if (col[k] + 16 <= a.cols) {
-#pragma unroll
-            for (int q = 0; q < 16 / E::kVec; ++q) put_stream16(y + q * E::kVec, E::pack(f + q * E::kVec));
+        if (col[k] + kVec <= a.cols) {
+            if constexpr (kStream) put_stream16(y, E::pack(f));
+            else store16(y, E::pack(f));
         } else {
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
+            for (int q = 0; q < kVec; ++q)
                 if (col[k] + q < a.cols) y[q] = (elem)f[q];
         }
     }
@@ -248,12 +258,20 @@ hipError_t launch_quantise8(int dtype, bool tiles, const Quant8Args& a, hipStrea
     return tiles ? launch_sides<kF16, true>(a, s) : launch_sides<kF16, false>(a, s);
 }
 
-hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s) {
+template <int T>
+static hipError_t launch_back(const Dequant8Args& a, hipStream_t s) {
     const dim3 grid((a.total + (256 * kChunks - 1)) / (256 * kChunks)), block(256);
-    if (a.dtype == kF32) hipLaunchKernelGGL(k_dequantise8<kF32>, grid, block, 0, s, a);
-    else if (a.dtype == kBF16) hipLaunchKernelGGL(k_dequantise8<kBF16>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_dequantise8<kF16>, grid, block, 0, s, a);
+    // streaming stores where they fill whole pieces of 64 bytes
+    const int64_t size = sizeof(typename Elem<T>::type);
+    if (((reinterpret_cast<uintptr_t>(a.y) | uintptr_t((a.stride | a.cols) * size)) & 63) == 0)
+        hipLaunchKernelGGL((k_dequantise8<T, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_dequantise8<T, false>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+hipError_t launch_dequantise8(const Dequant8Args& a, hipStream_t s) {
+    return a.dtype == kF32 ? launch_back<kF32>(a, s) : a.dtype == kBF16 ? launch_back<kBF16>(a, s) : launch_back<kF16>(a, s);
 }
 
 }  // namespace muon
