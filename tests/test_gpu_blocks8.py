@@ -144,6 +144,24 @@ def test_strides_and_what_lies_beside(torch_dev, tiles):
     assert bool((y == 7.0).all())
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tiles", [False, True])
+def test_reading_back_to_any_place(torch_dev, name, tiles):
+    """Into rows that fill whole lines and rows that do not, from every offset, beside what stays."""
+    torch, dev = torch_dev
+    for i, (rows, cols) in enumerate(((1, 1), (3, 7), (5, 130), (200, 256), (131, 1001), (40, 4096))):
+        q, _ = muon.quantise8(draw(torch, dev, 60 + i, (rows, cols), torch.float32), tiles=tiles)
+        want = q.dequantise(torch.float32).to(dtype_of(torch, name))  # float32 holds the values exactly
+        assert torch.equal(q.dequantise(dtype_of(torch, name)), want)
+        for lead, beside in ((0, 0), (0, 64), (1, 0), (3, 6), (8, 24)):
+            full = torch.full((rows + 2, lead + cols + beside), 7.0, dtype=dtype_of(torch, name), device=dev)
+            q.dequantise(out=full[1:-1, lead:lead + cols])
+            torch.cuda.synchronize()
+            assert torch.equal(full[1:-1, lead:lead + cols], want), (rows, cols, lead, beside)
+            full[1:-1, lead:lead + cols] = 7.0
+            assert bool((full == 7.0).all()), (rows, cols, lead, beside)
+
+
 def test_nothing_to_quantise(torch_dev):
     torch, dev = torch_dev
     for shape in ((0, 5), (5, 0), (0, 0)):
