@@ -426,8 +426,19 @@ hipError_t launch_type(int dtype, bool res32, const NormPlan& p, const AddNormAr
 NormPlan plan_add_norm(bool forward, int dtype, int64_t cols, int64_t rows) {
     // rows shorter than a vector are spread as those of one vector
     const int64_t least = dtype == kF32 ? 4 : 8;
-    return forward ? plan_norm_forward(dtype, std::max(cols, least), rows, 1)
-                   : plan_norm_backward(dtype, std::max(cols, least), rows, 1);
+    if (forward) return plan_norm_forward(dtype, std::max(cols, least), rows, 1);
+    NormPlan p = plan_norm_backward(dtype, std::max(cols, least), rows, 1);
+    // Backward asks for more waves of fp32 rows on a compute unit than the norms' rule, which cuts
+    // its 10 to whole blocks: one block of 7 or 8 waves takes [21897, 1629] in 165 us and
+    // [8000, 2000] in 69, two take 112 and 54. 16-bit rows, of twice the elements a lane, gain
+    // nothing ([20000, 2048] 123 us, with 14 waves 127).
+    if (dtype == kF32) {
+        constexpr int64_t kUnits = 256, kWaves = 14;
+        const int64_t blocks = kUnits * std::max<int64_t>(1, (kWaves * 64 + p.threads / 2) / p.threads);
+        p.chunks = int(std::max<int64_t>(p.chunks, std::min<int64_t>(blocks, rows / (4 * p.teams))));
+        p.chunk_rows = int((rows + p.chunks - 1) / p.chunks);
+    }
+    return p;
 }
 
 hipError_t launch_add_norm_forward(int dtype, bool res32, const NormPlan& p, const AddNormArgs& a, hipStream_t s) {
