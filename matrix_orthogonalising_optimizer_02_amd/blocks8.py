@@ -119,11 +119,15 @@ def _check_out(out, shape, dtype, device):
 def _new(like, rows, cols, tiles):
     """Memory for a matrix [rows, cols] in 8 bits, beside the tensor `like`."""
     torch = B._torch()
-    q = Blocks8.__new__(Blocks8)
     blocks = -(-cols // BLOCK)
-    q.codes = like.new_empty((rows, blocks * BLOCK), dtype=torch.float8_e4m3fn)
-    q.scales = like.new_empty((-(-rows // BLOCK) if tiles else rows, _up(blocks, 4)), dtype=torch.uint8)
-    q.rows, q.cols, q.tiles = rows, cols, tiles
+    return _made(like.new_empty((rows, blocks * BLOCK), dtype=torch.float8_e4m3fn),
+                 like.new_empty((-(-rows // BLOCK) if tiles else rows, _up(blocks, 4)), dtype=torch.uint8), rows, cols, tiles)
+
+
+def _made(codes, scales, rows, cols, tiles):
+    """The Blocks8 of memory that is known to fit it."""
+    q = Blocks8.__new__(Blocks8)
+    q.codes, q.scales, q.rows, q.cols, q.tiles = codes, scales, rows, cols, tiles
     return q
 
 
@@ -296,25 +300,38 @@ def _autograd_function():
     class Linear8(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, weight, weight8, products):
-            ctx.shape, ctx.dtype, ctx.weight_dtype = x.shape, x.dtype, weight.dtype
-            w8 = Weight8(weight) if weight8 is None else weight8
-            ctx.w8, ctx.version, ctx.products = w8, w8.version, products
-            x8, ctx.x8t = quantise8(x, transposed=ctx.needs_input_grad[1])
-            return matmul8(x8, w8.direct, dtype=x.dtype).view(*x.shape[:-1], w8.shape[0])
+            ctx.shape, ctx.dtype, ctx.weight_dtype, ctx.products = x.shape, x.dtype, weight.dtype, products
+            # the caller's Weight8 is the caller's to keep; what is made here is autograd's, which
+            # frees it after the backward pass and shows it to saved_tensors_hooks
+            ctx.weight8, ctx.version = weight8, weight8 and weight8.version
+            if weight8 is None:
+                w8, w8t = quantise8(weight, tiles=True, transposed=True)
+            else:
+                w8, w8t = weight8.direct, None
+            x8, x8t = quantise8(x, transposed=ctx.needs_input_grad[1])
+            ctx.rows = x8.rows
+            ctx.save_for_backward(x8t and x8t.codes, x8t and x8t.scales, w8t and w8t.codes, w8t and w8t.scales)
+            return matmul8(x8, w8, dtype=x.dtype).view(*x.shape[:-1], w8.rows)
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
-            if ctx.w8.version != ctx.version:
+            x_codes, x_scales, w_codes, w_scales = ctx.saved_tensors
+            if ctx.weight8 is not None and ctx.weight8.version != ctx.version:
                 raise RuntimeError("the weight's 8-bit form was updated after the forward pass")
             want_x, want_w = ctx.needs_input_grad[:2]
+            cols = ctx.shape[-1]
             try:
                 _rows_of(dy, "dy")
             except ValueError:  # an expanded or transposed gradient
                 dy = dy.contiguous()
             dy8, dy8t = quantise8(dy, direct=want_x, transposed=want_w) if want_x or want_w else (None, None)
-            dx = matmul8(dy8, ctx.w8.transposed, dtype=ctx.dtype).view(ctx.shape) if want_x else None
-            dw = matmul8(dy8t, ctx.x8t, dtype=ctx.weight_dtype, products=ctx.products) if want_w else None
+            dx = dw = None
+            if want_x:
+                w8t = _made(w_codes, w_scales, cols, dy8.cols, True) if ctx.weight8 is None else ctx.weight8.transposed
+                dx = matmul8(dy8, w8t, dtype=ctx.dtype).view(ctx.shape)
+            if want_w:
+                dw = matmul8(dy8t, _made(x_codes, x_scales, cols, ctx.rows, False), dtype=ctx.weight_dtype, products=ctx.products)
             return dx, dw, None, None
 
     _function = Linear8

@@ -1,0 +1,52 @@
+"""linear8 on the GPU: what stays allocated, and the same gradients through offloading and
+checkpointing."""
+import pytest
+
+import matrix_orthogonalising_optimizer_02_amd as muon
+from test_gpu_blocks8 import draw, torch_dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def layer(torch, dev, rows=300, cols=520, out=260):
+    x = draw(torch, dev, 510, (rows, cols), torch.bfloat16).requires_grad_()
+    w = draw(torch, dev, 511, (out, cols), torch.float32, 0.02).requires_grad_()
+    return x, w, draw(torch, dev, 512, (rows, out), torch.bfloat16)
+
+
+def test_memory_after_the_backward_pass(torch_dev):  # noqa: F811
+    torch, dev = torch_dev
+    x, w, g = layer(torch, dev, 1024, 1024, 1024)
+    muon.linear8(x, w).backward(g)  # x.grad and w.grad have their memory
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y = muon.linear8(x, w)
+    assert torch.cuda.memory_allocated() - before >= y.numel() * 2 + x.numel() + w.numel()
+    y.backward(g)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before == y.numel() * 2
+    with pytest.raises(RuntimeError, match="second time"):
+        y.backward(g)
+
+
+def test_offloaded_and_checkpointed(torch_dev):  # noqa: F811
+    torch, dev = torch_dev
+    x, w, g = layer(torch, dev)
+    kept = muon.Weight8(w)
+
+    def gradients(call):
+        x.grad = w.grad = None
+        y = call()
+        y.backward(g)
+        torch.cuda.synchronize()
+        return y.detach(), x.grad, w.grad
+
+    def offloaded(w8):
+        with torch.autograd.graph.save_on_cpu():
+            return muon.linear8(x, w, w8)
+
+    for w8 in (None, kept):
+        want = gradients(lambda: muon.linear8(x, w, w8))
+        for call in (lambda: offloaded(w8),
+                     lambda: torch.utils.checkpoint.checkpoint(lambda a, b: muon.linear8(a, b, w8), x, w, use_reentrant=False)):
+            assert all(torch.equal(a, b) for a, b in zip(want, gradients(call)))

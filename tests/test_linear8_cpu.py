@@ -1,0 +1,129 @@
+"""linear8 under torch.autograd: what it keeps for its backward pass, and for how long.
+
+The kernels' places are taken by plain products on the CPU; inputs are small whole numbers,
+which e4m3 holds, so that every result is exact.
+"""
+import numpy as np
+import pytest
+
+from matrix_orthogonalising_optimizer_02_amd import blocks8
+import matrix_orthogonalising_optimizer_02_amd as muon
+
+torch = pytest.importorskip("torch")
+
+
+class Recorder:
+    """quantise8 and matmul8 on the CPU, all powers 1, and a note of each call."""
+
+    def __init__(self):
+        self.made, self.forms, self.products = [], [], []
+
+    def quantise8(self, x, *, tiles=False, direct=True, transposed=False, out=None, out_transposed=None, stream=None):
+        flat = x.detach().reshape(-1, x.shape[-1])
+        self.forms.append((tuple(flat.shape), direct or out is not None, transposed or out_transposed is not None))
+        q = self.one(flat, tiles, out) if direct or out is not None else None
+        qt = self.one(flat.t(), tiles, out_transposed) if transposed or out_transposed is not None else None
+        return q, qt
+
+    def one(self, m, tiles, out):
+        q = blocks8._new(torch.empty(0), m.shape[0], m.shape[1], tiles) if out is None else out
+        q.codes.copy_(torch.nn.functional.pad(m.float(), (0, q.codes.shape[1] - m.shape[1])).to(torch.float8_e4m3fn))
+        q.scales.fill_(127)
+        self.made.append(q)
+        return q
+
+    def matmul8(self, a, b, *, dtype=None, products=None, **kw):
+        assert a.cols == b.cols and a.codes.shape[0] == a.rows and b.codes.shape[0] == b.rows
+        assert a.tiles is False
+        self.products.append(products)
+        return (a.codes.float()[:, :a.cols] @ b.codes.float()[:, :b.cols].t()).to(dtype)
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(blocks8, "quantise8", r.quantise8)
+    monkeypatch.setattr(blocks8, "matmul8", r.matmul8)
+    return r
+
+
+def whole(seed, *shape, grad=True):
+    gen = np.random.default_rng(seed)
+    return torch.from_numpy(gen.integers(-3, 4, shape).astype(np.float32)).requires_grad_(grad)
+
+
+def storages(quantised):
+    from torch.multiprocessing.reductions import StorageWeakRef
+    return [StorageWeakRef(t.untyped_storage()) for q in quantised for t in (q.codes, q.scales)]
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_gradients(fake, kept):
+    x, w, g = whole(1, 2, 5, 7), whole(2, 6, 7), whole(3, 2, 5, 6, grad=False)
+    muon.linear8(x, w, muon.Weight8(w) if kept else None).backward(g)
+    assert torch.equal(x.grad, g @ w.detach()) and torch.equal(w.grad, g.reshape(-1, 6).t() @ x.detach().reshape(-1, 7))
+
+
+def test_operands_go_with_the_backward_pass(fake):
+    """The output lives on; what the backward pass read does not."""
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    y = muon.linear8(x, w)
+    held = storages(fake.made)
+    fake.made.clear()
+    assert sum(not s.expired() for s in held) == 4  # the transposed x and weight
+    y.backward(g)
+    fake.made.clear()
+    assert all(s.expired() for s in held)
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_a_second_backward_pass_is_refused(fake, kept):
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    y = muon.linear8(x, w, muon.Weight8(w) if kept else None)
+    y.backward(g, retain_graph=True)
+    y.backward(g)
+    assert torch.equal(w.grad, 2 * (g.t() @ x.detach()))
+    with pytest.raises(RuntimeError, match="second time"):
+        y.backward(g)
+
+
+def test_hooks_see_what_is_kept(fake):
+    """saved_tensors_hooks get the 8-bit operands, and the backward pass takes what they give back."""
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    packed, unpacked = [], []
+
+    def pack(t):
+        packed.append(t.dtype)
+        return t.clone()
+
+    def unpack(t):
+        unpacked.append(t.dtype)
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, unpack):
+        y = muon.linear8(x, w)
+    held = storages(fake.made)
+    fake.made.clear()
+    assert all(s.expired() for s in held)  # the clones alone are kept
+    y.backward(g)
+    assert sorted(map(str, packed)) == sorted(map(str, unpacked)) == ["torch.float8_e4m3fn"] * 2 + ["torch.uint8"] * 2
+    assert torch.equal(x.grad, g @ w.detach()) and torch.equal(w.grad, g.t() @ x.detach())
+
+
+def test_checkpointing_keeps_no_operand(fake):
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    y = torch.utils.checkpoint.checkpoint(lambda a, b: muon.linear8(a, b), x, w, use_reentrant=False)
+    held = storages(fake.made)
+    fake.made.clear()
+    assert all(s.expired() for s in held)
+    y.backward(g)
+    assert torch.equal(x.grad, g @ w.detach()) and torch.equal(w.grad, g.t() @ x.detach())
+
+
+def test_a_form_that_moved_on_is_refused(fake):
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    w8 = muon.Weight8(w)
+    y = muon.linear8(x, w, w8)
+    w8.update(w)
+    with pytest.raises(RuntimeError, match="updated after"):
+        y.backward(g)
