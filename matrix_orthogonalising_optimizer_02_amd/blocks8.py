@@ -299,16 +299,18 @@ def _autograd_function():
 
     class Linear8(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, weight, weight8, products):
+        def forward(ctx, x, weight, weight8, products, grads):
+            # needs_input_grad tells of the leaves alone; grads: whether autograd records this call
+            need_x, need_w = (grads and need for need in ctx.needs_input_grad[:2])
             ctx.shape, ctx.dtype, ctx.weight_dtype, ctx.products = x.shape, x.dtype, weight.dtype, products
             # the caller's Weight8 is the caller's to keep; what is made here is autograd's, which
             # frees it after the backward pass and shows it to saved_tensors_hooks
             ctx.weight8, ctx.version = weight8, weight8 and weight8.version
             if weight8 is None:
-                w8, w8t = quantise8(weight, tiles=True, transposed=True)
+                w8, w8t = quantise8(weight, tiles=True, transposed=need_x)
             else:
                 w8, w8t = weight8.direct, None
-            x8, x8t = quantise8(x, transposed=ctx.needs_input_grad[1])
+            x8, x8t = quantise8(x, transposed=need_w)
             ctx.rows = x8.rows
             ctx.save_for_backward(x8t and x8t.codes, x8t and x8t.scales, w8t and w8t.codes, w8t and w8t.scales)
             return matmul8(x8, w8, dtype=x.dtype).view(*x.shape[:-1], w8.rows)
@@ -332,7 +334,7 @@ def _autograd_function():
                 dx = matmul8(dy8, w8t, dtype=ctx.dtype).view(ctx.shape)
             if want_w:
                 dw = matmul8(dy8t, _made(x_codes, x_scales, cols, ctx.rows, False), dtype=ctx.weight_dtype, products=ctx.products)
-            return dx, dw, None, None
+            return dx, dw, None, None, None
 
     _function = Linear8
     return Linear8
@@ -345,7 +347,7 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
     x [..., in], weight [out, in], each float32, bfloat16 or float16. x and the gradient are
     quantised by 128 elements along what each product sums over; for the weight's gradient x is
     kept in 8 bits. weight8: the weight's 8-bit form, kept up to date by the caller; made in the
-    call without one. weight_grad_products: matmul8's `products` for the weight's gradient
+    call without one, transposed too only where x's gradient will need it. weight_grad_products: matmul8's `products` for the weight's gradient
     (8: twice the rate, 2^-16 rounding; default 16 for a float32 weight).
     """
     torch = B._torch()
@@ -359,4 +361,4 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
             raise TypeError("weight8 must be a Weight8")
         if weight8.shape != tuple(weight.shape) or weight8.direct.device != x.device:
             raise ValueError(f"weight8 must have shape {tuple(weight.shape)} and live on {x.device}")
-    return _autograd_function().apply(x, weight, weight8, weight_grad_products)
+    return _autograd_function().apply(x, weight, weight8, weight_grad_products, torch.is_grad_enabled())

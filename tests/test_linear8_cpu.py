@@ -127,3 +127,24 @@ def test_a_form_that_moved_on_is_refused(fake):
     w8.update(w)
     with pytest.raises(RuntimeError, match="updated after"):
         y.backward(g)
+
+
+@pytest.mark.parametrize("grads", ["no_grad", "inference", "frozen"])
+def test_no_form_that_no_gradient_reads(fake, grads):
+    """Without gradients x and the weight are quantised in the form that the output reads alone."""
+    frozen = grads == "frozen"
+    x, w = whole(1, 5, 7, grad=not frozen), whole(2, 6, 7, grad=not frozen)
+    with {"no_grad": torch.no_grad, "inference": torch.inference_mode, "frozen": torch.enable_grad}[grads]():
+        y = muon.linear8(x, w)
+    assert not y.requires_grad and torch.equal(y, x.detach() @ w.detach().t())
+    assert sorted(fake.forms) == [((5, 7), True, False), ((6, 7), True, False)]
+
+
+def test_forms_of_one_gradient(fake):
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    muon.linear8(x, w.detach()).backward(g)
+    assert sorted(fake.forms) == [((5, 6), True, False), ((5, 7), True, False), ((6, 7), True, True)]
+    fake.forms.clear()
+    muon.linear8(x.detach(), w).backward(g)
+    assert sorted(fake.forms) == [((5, 6), False, True), ((5, 7), True, True), ((6, 7), True, False)]
+    assert torch.equal(x.grad, g @ w.detach()) and torch.equal(w.grad, g.t() @ x.detach())
