@@ -202,6 +202,11 @@ def quantise8(x, *, tiles: bool = False, direct: bool = True, transposed: bool =
     return q, qt
 
 
+def _check_products(products):
+    if products not in (None, 8, 16):
+        raise ValueError("products must be None, 8 or 16")
+
+
 def matmul8_workspace_bytes(m: int, n: int, k: int, dtype=None, products=None) -> int:
     """Bytes of matmul8's workspace for [m, k] times [n, k] into dtype (default bfloat16)."""
     size = ctypes.c_size_t(0)
@@ -232,8 +237,7 @@ def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = 
         raise ValueError(f"b must live on {device}")
     if a.cols != b.cols:
         raise ValueError(f"a and b must have the same number of columns, {a.cols} and {b.cols}")
-    if products not in (None, 8, 16):
-        raise ValueError("products must be None, 8 or 16")
+    _check_products(products)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is not None:
@@ -347,8 +351,9 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
     x [..., in], weight [out, in], each float32, bfloat16 or float16. x and the gradient are
     quantised by 128 elements along what each product sums over; for the weight's gradient x is
     kept in 8 bits. weight8: the weight's 8-bit form, kept up to date by the caller; made in the
-    call without one, transposed too only where x's gradient will need it. weight_grad_products: matmul8's `products` for the weight's gradient
-    (8: twice the rate, 2^-16 rounding; default 16 for a float32 weight).
+    call without one, transposed too only where x's gradient will need it.
+    weight_grad_products: matmul8's `products` for the weight's gradient (8: twice the rate,
+    2^-16 rounding; default 16 for a float32 weight).
     """
     torch = B._torch()
     for t, name in ((x, "x"), (weight, "weight")):
@@ -356,6 +361,12 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
             raise TypeError(f"{name} must be a torch.Tensor")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError(f"weight must be 2-D with x's {x.shape[-1] if x.dim() else 0} elements a row")
+    for t, name in ((x, "x"), (weight, "weight")):
+        if t.dtype not in B.dtype_codes():
+            raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if weight.device != x.device:
+        raise ValueError(f"weight must live on {x.device}")
+    _check_products(weight_grad_products)
     if weight8 is not None:
         if not isinstance(weight8, Weight8):
             raise TypeError("weight8 must be a Weight8")

@@ -148,3 +148,17 @@ def test_forms_of_one_gradient(fake):
     muon.linear8(x.detach(), w).backward(g)
     assert sorted(fake.forms) == [((5, 6), False, True), ((5, 7), True, True), ((6, 7), True, False)]
     assert torch.equal(x.grad, g @ w.detach()) and torch.equal(w.grad, g.t() @ x.detach())
+
+
+def test_refused_at_the_call(fake):
+    """What the backward pass could not do is refused by the forward call."""
+    x, w = whole(1, 5, 8), whole(2, 6, 8)
+    w8 = muon.Weight8(w)
+    for call, text in ((lambda: muon.linear8(x, w.detach().double(), w8), "weight must be float32"),
+                       (lambda: muon.linear8(x.detach().double(), w, w8), "x must be float32"),
+                       (lambda: muon.linear8(x, w.detach().to("meta"), w8), "weight must live on cpu"),
+                       (lambda: muon.linear8(x, w, w8, weight_grad_products=4), "products must be None, 8 or 16")):
+        fake.forms.clear()
+        with pytest.raises(ValueError, match=text):
+            call()
+        assert not fake.forms
