@@ -581,8 +581,9 @@ int dequantise8(const blocks8* q, void* y, int64_t stride, int32_t dtype, void* 
  * products: 8 = by the 8-bit matrix instructions, which drop, in every eight products that
  *   follow each other along k, bits below 2^-13 of the largest: the result is off by 2^-16 of
  *   it, root mean square, on normally distributed values, and by 2^-10 of the sum of
- *   magnitudes at most; 16 = the codes are widened to bf16, exactly, and the sums are those of
- *   fp32 additions, at half the rate; 0 = 16 for an fp32 c, 8 for others.
+ *   magnitudes at most (above a 16-bit c's own rounding where sums cancel); 16 = the codes are
+ *   widened to bf16, exactly, and the sums are those of fp32 additions, at half the rate; 0 = 16
+ *   for an fp32 c, 8 for others.
  * Workspace (matmul8_workspace_bytes, 256-byte aligned; none needed where that gives 0): the
  * partial sums of products with few tiles.
  * Errors: INVALID_ARG (and a->cols != b->cols), ALIGN, ALIAS (c or the workspace overlaps

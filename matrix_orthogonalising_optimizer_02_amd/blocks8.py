@@ -222,11 +222,11 @@ def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = 
 
     With quantise8's results of a layer's x, weight and dy: y = (x, weight), dx = (dy, weight
     transposed), dweight = (dy transposed, x transposed). products 8: by the 8-bit matrix
-    instructions, which drop bits below 2^-13 of the largest in every eight products (the result
-    is off by 2^-16 of it on normally distributed values); 16: widened to bfloat16, exactly, with
-    sums as of fp32 additions, at half the rate; None: 16 for a float32 result, 8 for others.
-    workspace: optional uint8 buffer of
-    matmul8_workspace_bytes().
+    instructions, which drop bits below 2^-13 of the largest in every eight products. The result
+    is off by 2^-16 of it on normally distributed values, but by up to 2^-10 of the products'
+    magnitudes: more than a 16-bit result's own rounding where sums cancel. 16: widened to
+    bfloat16, exactly, with sums as of fp32 additions, at half the rate. None: 16 for a float32
+    result, 8 for others. workspace: optional uint8 buffer of matmul8_workspace_bytes().
     """
     torch = B._torch()
     for q, name in ((a, "a"), (b, "b")):
@@ -303,10 +303,10 @@ def _autograd_function():
 
     class Linear8(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, weight, weight8, products, grads):
+        def forward(ctx, x, weight, weight8, products, weight_products, grads):
             # needs_input_grad tells of the leaves alone; grads: whether autograd records this call
             need_x, need_w = (grads and need for need in ctx.needs_input_grad[:2])
-            ctx.shape, ctx.dtype, ctx.weight_dtype, ctx.products = x.shape, x.dtype, weight.dtype, products
+            ctx.shape, ctx.dtype, ctx.weight_dtype, ctx.products = x.shape, x.dtype, weight.dtype, (products, weight_products)
             # the caller's Weight8 is the caller's to keep; what is made here is autograd's, which
             # frees it after the backward pass and shows it to saved_tensors_hooks
             ctx.weight8, ctx.version = weight8, weight8 and weight8.version
@@ -317,7 +317,7 @@ def _autograd_function():
             x8, x8t = quantise8(x, transposed=need_w)
             ctx.rows = x8.rows
             ctx.save_for_backward(x8t and x8t.codes, x8t and x8t.scales, w8t and w8t.codes, w8t and w8t.scales)
-            return matmul8(x8, w8, dtype=x.dtype).view(*x.shape[:-1], w8.rows)
+            return matmul8(x8, w8, dtype=x.dtype, products=products).view(*x.shape[:-1], w8.rows)
 
         @staticmethod
         @torch.autograd.function.once_differentiable
@@ -335,16 +335,17 @@ def _autograd_function():
             dx = dw = None
             if want_x:
                 w8t = _made(w_codes, w_scales, cols, dy8.cols, True) if ctx.weight8 is None else ctx.weight8.transposed
-                dx = matmul8(dy8, w8t, dtype=ctx.dtype).view(ctx.shape)
+                dx = matmul8(dy8, w8t, dtype=ctx.dtype, products=ctx.products[0]).view(ctx.shape)
             if want_w:
-                dw = matmul8(dy8t, _made(x_codes, x_scales, cols, ctx.rows, False), dtype=ctx.weight_dtype, products=ctx.products)
-            return dx, dw, None, None, None
+                x8t = _made(x_codes, x_scales, cols, ctx.rows, False)
+                dw = matmul8(dy8t, x8t, dtype=ctx.weight_dtype, products=ctx.products[1])
+            return dx, dw, None, None, None, None
 
     _function = Linear8
     return Linear8
 
 
-def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
+def linear8(x, weight, weight8: Weight8 = None, *, products=None, weight_grad_products=None):
     """x weight^T for torch.autograd with all three products in 8 bits: the output, x's gradient
     (both in x's dtype) and the weight's (in the weight's dtype, fp32 as Muon takes it).
 
@@ -352,8 +353,9 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
     quantised by 128 elements along what each product sums over; for the weight's gradient x is
     kept in 8 bits. weight8: the weight's 8-bit form, kept up to date by the caller; made in the
     call without one, transposed too only where x's gradient will need it.
-    weight_grad_products: matmul8's `products` for the weight's gradient (8: twice the rate,
-    2^-16 rounding; default 16 for a float32 weight).
+    products, weight_grad_products: matmul8's `products` for the output and x's gradient, and for
+    the weight's (8: twice the rate, fewer bits in the sums; None: 16 for a float32 result, 8 for
+    others; a 16-bit output whose sums cancel needs 16).
     """
     torch = B._torch()
     for t, name in ((x, "x"), (weight, "weight")):
@@ -366,10 +368,11 @@ def linear8(x, weight, weight8: Weight8 = None, *, weight_grad_products=None):
             raise ValueError(f"{name} must be float32, bfloat16 or float16")
     if weight.device != x.device:
         raise ValueError(f"weight must live on {x.device}")
+    _check_products(products)
     _check_products(weight_grad_products)
     if weight8 is not None:
         if not isinstance(weight8, Weight8):
             raise TypeError("weight8 must be a Weight8")
         if weight8.shape != tuple(weight.shape) or weight8.direct.device != x.device:
             raise ValueError(f"weight8 must have shape {tuple(weight.shape)} and live on {x.device}")
-    return _autograd_function().apply(x, weight, weight8, weight_grad_products, torch.is_grad_enabled())
+    return _autograd_function().apply(x, weight, weight8, products, weight_grad_products, torch.is_grad_enabled())

@@ -50,3 +50,23 @@ def test_offloaded_and_checkpointed(torch_dev):  # noqa: F811
         for call in (lambda: offloaded(w8),
                      lambda: torch.utils.checkpoint.checkpoint(lambda a, b: muon.linear8(a, b, w8), x, w, use_reentrant=False)):
             assert all(torch.equal(a, b) for a, b in zip(want, gradients(call)))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("kept", [False, True])
+def test_sums_that_cancel(torch_dev, dtype, kept):  # noqa: F811
+    """products=16: small products beside large ones that cancel each other. Every product and
+    partial sum is a multiple of 2^-16 below 2^17 in magnitude that eleven significant bits or a
+    few more hold, so that sums as of fp32 additions are exact; the 8-bit instructions drop what
+    lies 2^-13 below the largest of eight products."""
+    torch, dev = torch_dev
+    v = torch.ones(16, device=dev)
+    v[0] = v[8] = 256.0
+    s = v.clone()
+    s[8] = -256.0
+    w = (v[:, None] * v[None, :] / 256.0).requires_grad_()
+    x = s[None, :].repeat(3, 1).to(getattr(torch, dtype)).requires_grad_()
+    y = muon.linear8(x, w, muon.Weight8(w) if kept else None, products=16)
+    y.backward(x.detach())
+    want = (v * 14.0 / 256.0)[None, :].repeat(3, 1)  # v . s = 14
+    assert torch.equal(y.detach().float(), want) and torch.equal(x.grad.float(), want)

@@ -162,3 +162,14 @@ def test_refused_at_the_call(fake):
         with pytest.raises(ValueError, match=text):
             call()
         assert not fake.forms
+
+
+def test_products_of_each_result(fake):
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7), whole(3, 5, 6, grad=False)
+    for more, want in (({}, [None, None, None]), (dict(products=16), [16, 16, None]), (dict(products=8, weight_grad_products=16), [8, 8, 16]),
+                       (dict(weight_grad_products=8), [None, None, 8])):
+        fake.products.clear()
+        muon.linear8(x, w, **more).backward(g)
+        assert fake.products == want
+    with pytest.raises(ValueError, match="products must be None, 8 or 16"):
+        muon.linear8(x, w, products=0)
