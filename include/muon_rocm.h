@@ -539,7 +539,7 @@ int norm_backward(const norm_desc* desc, const norm_rows* dy, const norm_rows* x
  * least 2^e with max |x| <= 448 2^e over its finite elements (e >= -127), kept as the byte
  * e + 127 (255 stands for NaN and is never written); its codes are x 2^-e rounded to nearest,
  * ties to even. Infinities and NaN become NaN codes, each for itself. A value is
- * code 2^(byte - 127); in blocks below 2^-118 it may be taken for 0. */
+ * code 2^(byte - 127), for a byte of 0 as for the others. */
 #define MUON_BLOCK8 128
 #define MUON_BLOCKS8_MAX_COLS (1 << 22)
 
@@ -568,7 +568,7 @@ int quantise8(const void* x, int64_t rows, int64_t cols, int64_t stride, int32_t
               const blocks8* transposed, void* stream);
 
 /* y [rows, cols] of `dtype`, rows `stride` elements apart: the values of q, rounded to dtype
- * (exact in fp32 and bf16 but for the smallest blocks). Errors: as quantise8. */
+ * (exact in fp32, and in bf16 but for what has bits below 2^-133, in blocks below 2^-116). Errors: as quantise8. */
 int dequantise8(const blocks8* q, void* y, int64_t stride, int32_t dtype, void* stream);
 
 /* c[i][j] = sum_k a[i][k] b[j][k] for a [m, k], b [n, k], c [m, n] of `dtype`, rows ldc
@@ -582,8 +582,8 @@ int dequantise8(const blocks8* q, void* y, int64_t stride, int32_t dtype, void* 
  *   follow each other along k, bits below 2^-13 of the largest: the result is off by 2^-16 of
  *   it, root mean square, on normally distributed values, and by 2^-10 of the sum of
  *   magnitudes at most (above a 16-bit c's own rounding where sums cancel); 16 = the codes are
- *   widened to bf16, exactly, and the sums are those of fp32 additions, at half the rate; 0 = 16
- *   for an fp32 c, 8 for others.
+ *   widened to bf16 (as exactly as dequantise8 does) and the sums are those of fp32 additions,
+ *   at half the rate; 0 = 16 for an fp32 c, 8 for others.
  * Workspace (matmul8_workspace_bytes, 256-byte aligned; none needed where that gives 0): the
  * partial sums of products with few tiles.
  * Errors: INVALID_ARG (and a->cols != b->cols), ALIGN, ALIAS (c or the workspace overlaps

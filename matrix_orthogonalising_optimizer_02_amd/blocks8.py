@@ -44,7 +44,7 @@ class Blocks8:
     codes: float8_e4m3fn [rows, at least cols rounded up to 128], zeros from cols to there.
     scales: uint8 [rows, at least cols / 128 rounded up, to a multiple of 4], the power of
     each 1 x 128 elements as its exponent + 127; with `tiles` a row for each 128 rows, the
-    power of 128 x 128 elements. A value is code * 2^(scale - 127). Rows may lie further
+    power of 128 x 128 elements. A value is code * 2^(scale - 127), NaN for a scale of 255. Rows may lie further
     apart than they are long.
     """
 
@@ -87,7 +87,8 @@ class Blocks8:
         return _pack(self.rows, self.cols, c.data_ptr(), s.data_ptr(), ld, scale_ld, self.tiles, 0)
 
     def dequantise(self, dtype=None, out=None, stream=None):
-        """The values [rows, cols] in dtype (default float32; exact there and in bfloat16)."""
+        """The values [rows, cols] in dtype (default float32; exact there, and in bfloat16 but
+        for what has bits below 2^-133)."""
         torch = B._torch()
         device = self.device
         with B.device_and_stream(device, stream):

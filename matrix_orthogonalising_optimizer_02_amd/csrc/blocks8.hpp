@@ -120,10 +120,13 @@ __device__ __forceinline__ unsigned block_power(unsigned top) {
     return e > 8u ? e - 8u : 0u;
 }
 
-// 2^-e and 2^e of the byte (a byte of 0 gives 0 for the latter: its block holds zeros, or
-// magnitudes below 2^-118).
+// 2^-e and 2^e of the byte: 2^-127 (a byte of 0) is a subnormal, 255 is NaN.
 __device__ __forceinline__ float power_inverse(unsigned byte) { return __uint_as_float((254u - byte) << 23); }
-__device__ __forceinline__ float power_value(unsigned byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float power_value(unsigned byte) {
+    return __uint_as_float(byte == 255u ? 0x7FC00000u : max(byte << 23, 0x00400000u));
+}
+// 2^e as the instructions that widen codes take it: of a float they read the exponent alone.
+__device__ __forceinline__ float power_operand(unsigned byte) { return __uint_as_float(byte << 23); }
 
 // Four values of at most 448 to four codes, ties to even; an infinity or NaN gives NaN.
 __device__ __forceinline__ unsigned pack_codes(float a, float b, float c, float d) {

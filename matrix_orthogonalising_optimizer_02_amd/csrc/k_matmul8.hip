@@ -277,9 +277,9 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
             float sa[TM], sb[TN];
             const int sh = PH < 0 ? 0 : 8 * PH;
 #pragma unroll
-            for (int f = 0; f < TM; ++f) sa[f] = power_value((pa[f] >> sh) & 255u);
+            for (int f = 0; f < TM; ++f) sa[f] = power_operand((pa[f] >> sh) & 255u);
 #pragma unroll
-            for (int f = 0; f < TN; ++f) sb[f] = power_value((pb[f] >> sh) & 255u);
+            for (int f = 0; f < TN; ++f) sb[f] = power_operand((pb[f] >> sh) & 255u);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 bf16x8 wa[TM], wb[TN];
@@ -506,7 +506,7 @@ __device__ __forceinline__ void matmul8_few(const Mat8Args& a, float* red) {
                         __builtin_shufflevector(p.a[i][m][0], p.a[i][m][1], 0, 1, 2, 3, 4, 5, 6, 7), acc[m], 0, 0, 0, (int)(p.wb >> sh), 0,
                         (int)(p.wa[m] >> sh));
                 } else {
-                    const float sb = power_value((p.wb >> sh) & 255u), sa = power_value((p.wa[m] >> sh) & 255u);
+                    const float sb = power_operand((p.wb >> sh) & 255u), sa = power_operand((p.wa[m] >> sh) & 255u);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -646,7 +646,7 @@ __device__ __forceinline__ void matmul8_stream(const Mat8Args& a, uint8_t* smem)
                     __builtin_shufflevector(fb[0], fb[1], 0, 1, 2, 3, 4, 5, 6, 7),
                     __builtin_shufflevector(fa[m][0], fa[m][1], 0, 1, 2, 3, 4, 5, 6, 7), acc[m], 0, 0, 0, (int)eb, 0, (int)ea);
             } else {
-                const float sb = power_value(eb), sa = power_value(ea);
+                const float sb = power_operand(eb), sa = power_operand(ea);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(fb[q >> 1][2 * (q & 1)], fb[q >> 1][2 * (q & 1) + 1], sb),

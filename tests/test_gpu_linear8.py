@@ -1,9 +1,11 @@
-"""linear8 on the GPU: what stays allocated, and the same gradients through offloading and
-checkpointing."""
+"""linear8 on the GPU: what stays allocated, the same gradients through offloading and
+checkpointing, sums that cancel; and the ends of the powers' range."""
+import numpy as np
 import pytest
 
+from oracle import blocks8_oracle as Q
 import matrix_orthogonalising_optimizer_02_amd as muon
-from test_gpu_blocks8 import draw, torch_dev  # noqa: F401
+from test_gpu_blocks8 import VALUES, draw, torch_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +72,51 @@ def test_sums_that_cancel(torch_dev, dtype, kept):  # noqa: F811
     y.backward(x.detach())
     want = (v * 14.0 / 256.0)[None, :].repeat(3, 1)  # v . s = 14
     assert torch.equal(y.detach().float(), want) and torch.equal(x.grad.float(), want)
+
+
+def every_code(torch, dev, byte, rows):
+    """A Blocks8 [rows, 256] of all codes by turns under one power, and its values in float64."""
+    codes = (torch.arange(256, device=dev, dtype=torch.uint8)[None, :] + torch.arange(rows, device=dev, dtype=torch.uint8)[:, None])
+    q = muon.Blocks8(codes.view(torch.float8_e4m3fn), torch.full((rows, 4), byte, dtype=torch.uint8, device=dev), 256)
+    return q, torch.from_numpy(VALUES).to(dev)[codes.long()] * (2.0 ** (byte - 127) if byte < 255 else float("nan"))
+
+
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 8, 127, 247, 254, 255])
+def test_one_meaning_of_a_power(torch_dev, byte):  # noqa: F811
+    """code 2^(byte - 127), from the smallest byte to the largest, 255 a NaN: read back, and
+    multiplied by the identity at 1 in both widths. fp32 holds all of it that is below its
+    largest; bf16, and the products through it, round what has bits below 2^-133."""
+    torch, dev = torch_dev
+    q, want = every_code(torch, dev, byte, 40)
+    assert torch.equal(q.dequantise().cpu().nan_to_num(7.0), want.cpu().float().nan_to_num(7.0))
+    assert torch.equal(q.dequantise(torch.bfloat16).cpu().nan_to_num(7.0), want.cpu().float().to(torch.bfloat16).nan_to_num(7.0))
+    clean = want.isfinite() & (want.abs() < 2.0 ** 119)  # times 2^(130 - 127), within bf16
+    codes = q.codes.view(torch.uint8).clone()
+    codes[~clean] = 0
+    if byte == 255:
+        codes[:] = 0x38
+    unit = torch.zeros(256, 256, dtype=torch.uint8, device=dev)
+    unit.fill_diagonal_(0x38)  # 1
+    for m in (40, 140):  # few rows, and tiles
+        a = muon.Blocks8(codes.repeat(4, 1)[:m].view(torch.float8_e4m3fn), q.scales.repeat(4, 1)[:m], 256)
+        b = muon.Blocks8(unit.view(torch.float8_e4m3fn), torch.full((256, 4), 130, dtype=torch.uint8, device=dev), 256)
+        exact = torch.where(clean, want, 0.0 * want.nan_to_num()).repeat(4, 1)[:m] * 8.0
+        for products in (8, 16):
+            got = muon.matmul8(a, b, dtype=torch.float32, products=products)
+            torch.cuda.synchronize()
+            if byte == 255:
+                assert bool(got.isnan().all()), (m, products)
+            else:
+                # eight times half a step of bf16's subnormals
+                assert bool(((got.double() - exact).abs() <= (8.0 * 2.0 ** -134 if products == 16 and byte < 3 else 0.0)).all()), (m, products)
+
+
+def test_blocks_of_subnormals(torch_dev):  # noqa: F811
+    """Blocks below 2^-118 are read back as they were rounded."""
+    torch, dev = torch_dev
+    x = draw(torch, dev, 513, (20, 300), torch.float32).clamp(-50, 50) * 2.0 ** -126
+    for tiles in (False, True):
+        q, qt = muon.quantise8(x, tiles=tiles, transposed=True)
+        for got, ref in ((q, x.double().cpu().numpy()), (qt, x.double().cpu().numpy().T)):
+            want, e = Q.quantise(ref, tiles)
+            assert (e == -127).any() and np.array_equal(got.dequantise().double().cpu().numpy(), want)
