@@ -225,7 +225,12 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_add_norm_forwar
                 o.pack(y);
                 o.store(reinterpret_cast<elem*>(a.y) + row * a.y_stride, sp.col, a.cols);
             }
-            if (a.q.codes) put_codes<kVec, kGroup>(a, row, index, sp.skip, y, mine);
+            if (a.q.codes) {
+                if (a.cols < kVec)  // behind the end of a row that is shorter than a vector: 0 times a NaN rstd
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) y[e] = e < a.cols ? y[e] : 0.f;
+                put_codes<kVec, kGroup>(a, row, index, sp.skip, y, mine);
+            }
         }
         if (a.q.codes && mine)  // rows shorter than their team's lanes: the rest of the last block
             for (int c = (kN * t.lanes + t.lane) * kVec; c < (a.cols + kBlock8 - 1) / kBlock8 * kBlock8; c += t.lanes * kVec)
