@@ -316,6 +316,15 @@ __global__ __launch_bounds__(kLanes ? kSubThreads : 1024) void k_add_norm_backwa
             }
         }
         float sum[1] = {s};
+        // In place over dh the last vector's lane reads what the lane before it writes, which may be
+        // another wave's. dh is in no sum, and the barrier inside row_sums waits for LDS alone: so dh
+        // is brought to its registers here. (It was asked for with the rest of the row: no cost.)
+        if constexpr (kLanes == 0) {
+#pragma unroll
+            for (int k = 0; k < kN; ++k)
+#pragma unroll
+                for (int q = 0; q < Piece<R, kVec>::kParts; ++q) asm volatile("" ::"v"(dh[k].raw[q]));
+        }
         row_sums<kLanes, 1>(sum, red[flip], t, a.team_waves);
         flip ^= 1;
         if (!mine) return;
