@@ -593,6 +593,19 @@ int matmul8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dtype, int3
 int matmul8(const blocks8* a, const blocks8* b, void* c, int64_t ldc, int32_t dtype, int32_t products,
             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
+/* How matmul8 cuts a product [m, k] x [n, k]. Host only, touches no device; for tests and
+ * capacity planning. `out` (host array of MUON_MATMUL8_PLAN_INTS) receives
+ *   [0] the side of a block's tile of c, 128 or 256; 0 with m <= 64
+ *   [1] the parts of k, one after another in the workspace where there are several
+ * and with m <= 64 (else 0)
+ *   [2] the groups of 16 rows of a that a wave takes: 1, 2 or 4
+ *   [3] 1 = b streams through LDS, 128 of its rows a block; 0 = straight to registers, then
+ *   [4] the waves of a block, and
+ *   [5] those of them that take turns along k at the same 16 rows of b.
+ * All are 0 where m == 0 or n == 0. Errors: INVALID_ARG, TOO_LARGE, as matmul8_workspace_bytes. */
+#define MUON_MATMUL8_PLAN_INTS 6
+int matmul8_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t products, int32_t* out);
+
 /* ---- Residual addition with RMS norm ----------------------------------------------------
  * The step between two layers of a pre-norm block. For rows of `cols` elements:
  *   h = x + residual, rounded to the residual's type;  rstd = 1 / sqrt((1/cols) sum h^2 + eps)

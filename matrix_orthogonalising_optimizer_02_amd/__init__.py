@@ -45,6 +45,7 @@ from .blocks8 import (  # noqa: F401
     Weight8,
     linear8,
     matmul8,
+    matmul8_plan,
     matmul8_workspace_bytes,
     quantise8,
 )

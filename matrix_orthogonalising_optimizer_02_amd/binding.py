@@ -42,7 +42,7 @@ EXPORTED = ("muon_abi_version", "muon_status_str", "muon_last_error", "muon_defa
             "norm_forward", "norm_backward_workspace_bytes", "norm_backward",
             "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step", "adamw_multi_step_device",
             "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
-            "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
+            "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8_plan", "matmul8",
             "add_rms_norm_forward", "add_rms_norm_backward_workspace_bytes", "add_rms_norm_backward", "rotary_apply",
             "muon_ceiling_copy", "muon_ceiling_mfma", "muon_timing_enable", "muon_timing_read")
 
@@ -206,6 +206,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.quantise8.argtypes = [vp, i64, i64, i64, i32, blocks, blocks, vp]
     lib.dequantise8.argtypes = [blocks, vp, i64, i32, vp]
     lib.matmul8_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, size]
+    lib.matmul8_plan.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i32)]
     lib.matmul8.argtypes = [blocks, blocks, vp, i64, i32, i32, i32, vp, sz, vp]
     add = ctypes.POINTER(AddNormDesc)
     lib.add_rms_norm_forward.argtypes = [add, rows, rows, param, rows, rows, blocks, vp, vp]
@@ -222,7 +223,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "rownorm_shard_colsq", "rownorm_shard_apply", "norm_forward", "norm_backward_workspace_bytes",
                  "norm_backward", "adamw_multi_plan_bytes", "adamw_multi_plan", "adamw_multi_step",
                  "adamw_multi_step_device", "grad_norm_plan_bytes", "grad_norm_plan", "grad_norm", "grad_scale",
-                 "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8",
+                 "quantise8", "dequantise8", "matmul8_workspace_bytes", "matmul8_plan", "matmul8",
                  "add_rms_norm_forward", "add_rms_norm_backward_workspace_bytes", "add_rms_norm_backward", "rotary_apply",
                  "muon_ceiling_copy", "muon_ceiling_mfma",
                  "muon_timing_enable", "muon_timing_read"):

@@ -216,6 +216,16 @@ def matmul8_workspace_bytes(m: int, n: int, k: int, dtype=None, products=None) -
     return size.value
 
 
+def matmul8_plan(m: int, n: int, k: int, dtype=None, products=None):
+    """How matmul8 cuts [m, k] times [n, k] into dtype (default bfloat16), host only: a dict of
+    `tile` (a block's side of the result, 0 up to 64 rows), `parts` of k, and up to 64 rows the
+    `groups` of 16 rows of a, whether b goes through LDS (`stream`), else the `waves` of a block
+    and how many `share` the same rows of b."""
+    out = (ctypes.c_int32 * 6)()
+    B._check(B.load_library().matmul8_plan(m, n, k, B.dtype_codes()[dtype or B._torch().bfloat16], products or 0, out), "matmul8_plan")
+    return dict(zip(("tile", "parts", "groups", "stream", "waves", "share"), out))
+
+
 def matmul8(a: Blocks8, b: Blocks8, *, dtype=None, out=None, accumulate: bool = False, products=None, workspace=None,
             stream=None):
     """out[i, j] = sum_k a[i, k] b[j, k] (plus the old out with accumulate), fp32 sums rounded

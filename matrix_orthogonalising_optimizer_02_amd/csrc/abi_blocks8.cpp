@@ -2,6 +2,8 @@
 // include/muon_rocm.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <iterator>
 #include <string>
 #include <vector>
 
@@ -157,6 +159,18 @@ MUON_API int matmul8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dt
         const int rc = check_product(m, n, k, dtype, products);
         if (rc) return rc;
         *bytes = m == 0 || n == 0 ? 0 : plan_matmul8(m, n, k, wide(dtype, products)).partial_bytes;
+        return MUON_OK;
+    });
+}
+
+MUON_API int matmul8_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t products, int32_t* out) {
+    return guarded([&]() -> int {
+        if (!out) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
+        const int rc = check_product(m, n, k, dtype, products);
+        if (rc) return rc;
+        const Mat8Plan p = m == 0 || n == 0 ? Mat8Plan{} : plan_matmul8(m, n, k, wide(dtype, products));
+        const int32_t record[MUON_MATMUL8_PLAN_INTS] = {p.tile, p.splits, p.few, p.stream, p.waves, p.stream ? 0 : p.share};
+        std::copy(std::begin(record), std::end(record), out);
         return MUON_OK;
     });
 }

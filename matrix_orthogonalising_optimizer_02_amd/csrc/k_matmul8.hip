@@ -711,10 +711,12 @@ __global__ __launch_bounds__(256) void k_matmul8_join(Mat8Args a, int chunks) {
 // as below with a block a compute unit (two blocks of 128 on one take twice as long each), its
 // start and end a few (two blocks of 128 share theirs), and parts of k are written, read and added
 // at 8 TB/s (they are still in the caches) in a launch of their own.
-// Measured on MI355X: [2048, 2048, 2048] 16 us as 128-tiles, 28 as 256-tiles; [4096, 4096, 4096]
-// 58 us as 256-tiles, 68 as 128-tiles; [2048, 5120, 20480] 212 and 285; [512, 5120, 5120] 31 us in
-// three parts of 128-tiles, 36 as 256-tiles; fp32 [2048, 2048, 65536] 408 us in four parts of
-// 256-tiles, 532 as 128-tiles.
+// Measured on MI355X, us: [2048, 2048, 2048] 15 as 128-tiles, 27 as 256-tiles; [4096, 4096, 4096] 55
+// as 256-tiles, 63 as 128-tiles; [2048, 5120, 20480] 226 and 292; [256, 5120, 5120] 23 in three parts
+// of 128-tiles, 31 in one, 30 in six of 256-tiles; [128, 5120, 20480] 40 in six parts of 128-tiles, 141
+// in one; fp32 [2048, 2048, 65536] 410 in four parts of 256-tiles, 441 in two of 128-tiles. Of 18 sizes
+// timed with every cut the estimate takes the fastest or one within 4%, but for [512, 5120, 5120]: 31 in
+// one part of 128-tiles, 29 in two or three.
 Mat8Plan plan_matmul8(int64_t m, int64_t n, int64_t k, bool wide) {
     Mat8Plan p{};
     p.splits = 1;
