@@ -443,9 +443,13 @@ NormPlan plan_add_norm(bool forward, int dtype, int64_t cols, int64_t rows) {
     if (forward) return plan_norm_forward(dtype, std::max(cols, least), rows, 1);
     NormPlan p = plan_norm_backward(dtype, std::max(cols, least), rows, 1);
     // Backward asks for more waves of fp32 rows on a compute unit than the norms' rule, which cuts
-    // its 10 to whole blocks: one block of 7 or 8 waves takes [21897, 1629] in 165 us and
-    // [8000, 2000] in 69, two take 112 and 54. 16-bit rows, of twice the elements a lane, gain
-    // nothing ([20000, 2048] 123 us, with 14 waves 127).
+    // its 10 to whole blocks: one block of 7 or 8 waves takes [21897, 1629] in 151 us and [8000, 2000]
+    // in 64, two take 107 and 53. Over 40 million elements two blocks take 0.62 (16 columns) to 0.79
+    // (4096) of one's time at every width up to 4096, floor 102 us: 64 columns 155 and 108 us, 200 190
+    // and 123, 512 156 and 111, 1024 142 and 109, 4096 139 and 110. Wider rows' blocks and inputs of 4
+    // million elements are cut alike by both. 20 waves take 108 us at 200 and 384 columns, but 123 at
+    // 1024 and 140 at 1629. 16-bit rows, of twice the elements a lane, lose: [20000, 2048] bf16 57 us,
+    // with 14 waves 61 (with an fp32 residual 123 and 127).
     if (dtype == kF32) {
         constexpr int64_t kUnits = 256, kWaves = 14;
         const int64_t blocks = kUnits * std::max<int64_t>(1, (kWaves * 64 + p.threads / 2) / p.threads);
