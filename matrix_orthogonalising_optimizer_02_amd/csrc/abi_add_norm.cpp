@@ -152,19 +152,7 @@ MUON_API int add_rms_norm_forward(const add_norm_desc* desc, const norm_rows* x,
         if (codes) {
             if (codes->rows != d.rows || codes->cols != d.cols || codes->tiles)
                 return fail(MUON_ERR_INVALID_ARG, "codes is not [rows, cols] in blocks of 1 x 128");
-            if (d.rows && d.cols) {
-                const int64_t kb = (d.cols + kBlock8 - 1) / kBlock8, width = kb * kBlock8, powers = (kb + 3) / 4 * 4;
-                if (!codes->codes || !codes->scales) return fail(MUON_ERR_INVALID_ARG, "codes: codes or scales is NULL");
-                if (codes->ld < width || codes->ld % 16 || codes->scale_ld < powers || codes->scale_ld % 4)
-                    return fail(MUON_ERR_INVALID_ARG, "codes: ld or scale_ld does not fit");
-                if (codes->ld > MUON_BLOCKS8_MAX_COLS || codes->scale_ld > MUON_BLOCKS8_MAX_COLS)
-                    return fail(MUON_ERR_TOO_LARGE, "codes: ld above 2^22");
-                if (reinterpret_cast<uintptr_t>(codes->codes) % 16 || reinterpret_cast<uintptr_t>(codes->scales) % 4)
-                    return fail(MUON_ERR_ALIGN, "codes not 16-byte or scales not 4-byte aligned");
-                if ((rc = check_vector(codes->codes, (d.rows - 1) * codes->ld + width, 1, "codes", true, ranges)) ||
-                    (rc = check_vector(codes->scales, (d.rows - 1) * codes->scale_ld + powers, 1, "scales", true, ranges)))
-                    return rc;
-            }
+            if ((rc = check_blocks(codes, "codes", true, ranges))) return rc;
         }
         if (present(w) && (rc = check_vector(w->data, d.cols, elem_size(d.wdtype), "w", false, ranges))) return rc;
         if ((rc = check_vector(rstd, d.rows, 4, "rstd", true, ranges)) || (rc = check_overlaps(ranges))) return rc;

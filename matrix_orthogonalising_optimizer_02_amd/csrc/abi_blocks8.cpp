@@ -27,27 +27,6 @@ int fail(int code, const std::string& what) { return set_last_error(code, what);
 
 int64_t blocks_of(int64_t n) { return (n + kBlock8 - 1) / kBlock8; }
 
-int check_blocks(const blocks8* b, const char* name, bool write, std::vector<Range>& ranges) {
-    const std::string who(name);
-    if (!b) return fail(MUON_ERR_INVALID_ARG, who + " is NULL");
-    if (b->rows < 0 || b->cols < 0) return fail(MUON_ERR_INVALID_ARG, who + " has a negative dimension");
-    if (b->tiles != 0 && b->tiles != 1) return fail(MUON_ERR_INVALID_ARG, who + "->tiles must be 0 or 1");
-    if (b->rows > kMaxRows || b->cols > kMaxCols) return fail(MUON_ERR_TOO_LARGE, who + ": rows above 2^30 or cols above 2^22");
-    if (b->rows == 0 || b->cols == 0) return MUON_OK;
-    if (!b->codes || !b->scales) return fail(MUON_ERR_INVALID_ARG, who + ": codes or scales is NULL");
-    const int64_t kb = blocks_of(b->cols), width = kb * kBlock8, powers = (kb + 3) / 4 * 4;
-    if (b->ld < width || b->ld % 16) return fail(MUON_ERR_INVALID_ARG, who + "->ld must be a multiple of 16, cols rounded up to 128 at least");
-    if (b->scale_ld < powers || b->scale_ld % 4)
-        return fail(MUON_ERR_INVALID_ARG, who + "->scale_ld must be a multiple of 4, cols / 128 rounded up at least");
-    if (b->ld > kMaxCols || b->scale_ld > kMaxCols) return fail(MUON_ERR_TOO_LARGE, who + ": ld above 2^22");
-    const uintptr_t c = reinterpret_cast<uintptr_t>(b->codes), s = reinterpret_cast<uintptr_t>(b->scales);
-    if (c % 16 || s % 4) return fail(MUON_ERR_ALIGN, who + ": codes not 16-byte or scales not 4-byte aligned");
-    const int64_t srows = b->tiles ? blocks_of(b->rows) : b->rows;
-    ranges.push_back({c, c + uintptr_t((b->rows - 1) * b->ld + width), write});
-    ranges.push_back({s, s + uintptr_t((srows - 1) * b->scale_ld + powers), write});
-    return MUON_OK;
-}
-
 // A [rows, cols] matrix of `dtype` with adjacent elements in a row.
 int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t stride, int dtype, const char* name, bool write,
                  std::vector<Range>& ranges) {
@@ -83,6 +62,28 @@ int check_product(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t produc
 bool wide(int32_t dtype, int32_t products) { return products ? products == 16 : dtype == MUON_DTYPE_F32; }
 
 }  // namespace
+
+int check_blocks(const blocks8* b, const char* name, bool write, std::vector<Range>& ranges) {
+    const std::string who(name);
+    if (!b) return fail(MUON_ERR_INVALID_ARG, who + " is NULL");
+    if (b->rows < 0 || b->cols < 0) return fail(MUON_ERR_INVALID_ARG, who + " has a negative dimension");
+    if (b->tiles != 0 && b->tiles != 1) return fail(MUON_ERR_INVALID_ARG, who + "->tiles must be 0 or 1");
+    if (b->rows > kMaxRows || b->cols > kMaxCols) return fail(MUON_ERR_TOO_LARGE, who + ": rows above 2^30 or cols above 2^22");
+    if (b->rows == 0 || b->cols == 0) return MUON_OK;
+    if (!b->codes || !b->scales) return fail(MUON_ERR_INVALID_ARG, who + ": codes or scales is NULL");
+    const int64_t kb = blocks_of(b->cols), width = kb * kBlock8, powers = (kb + 3) / 4 * 4;
+    if (b->ld < width || b->ld % 16) return fail(MUON_ERR_INVALID_ARG, who + "->ld must be a multiple of 16, cols rounded up to 128 at least");
+    if (b->scale_ld < powers || b->scale_ld % 4)
+        return fail(MUON_ERR_INVALID_ARG, who + "->scale_ld must be a multiple of 4, cols / 128 rounded up at least");
+    if (b->ld > kMaxCols || b->scale_ld > kMaxCols) return fail(MUON_ERR_TOO_LARGE, who + ": ld above 2^22");
+    const uintptr_t c = reinterpret_cast<uintptr_t>(b->codes), s = reinterpret_cast<uintptr_t>(b->scales);
+    if (c % 16 || s % 4) return fail(MUON_ERR_ALIGN, who + ": codes not 16-byte or scales not 4-byte aligned");
+    const int64_t srows = b->tiles ? blocks_of(b->rows) : b->rows;
+    ranges.push_back({c, c + uintptr_t((b->rows - 1) * b->ld + width), write});
+    ranges.push_back({s, s + uintptr_t((srows - 1) * b->scale_ld + powers), write});
+    return MUON_OK;
+}
+
 }  // namespace muon
 
 using namespace muon;

@@ -28,6 +28,10 @@ struct Range {
 // Sorts the ranges.
 int check_overlaps(std::vector<Range>& ranges);
 
+// The descriptor of a matrix in 8 bits: its sizes, strides, pointers and limits; the spans of its
+// codes and powers join `ranges`.
+int check_blocks(const blocks8* b, const char* name, bool write, std::vector<Range>& ranges);
+
 // Runs `launch`, bracketed by events of kernel class `cls` while timing is enabled;
 // MUON_ERR_HIP (with the error text set) when it fails.
 int run_timed(int cls, hipStream_t stream, const char* name, const std::function<hipError_t()>& launch);

@@ -12,7 +12,6 @@ namespace {
 
 typedef int v8i32 __attribute__((ext_vector_type(8)));
 typedef int v4i32 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf162 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 template <bool B>
@@ -52,7 +51,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* q) {
 // form. Wide: eight codes become bf16, exactly and with their powers, for bf16 instructions at
 // half the rate, whose sums are as good as a sequence of fp32 additions; fp32 results take it.
 __device__ __forceinline__ bf16x8 widen(unsigned lo, unsigned hi, float power) {
-    const bf162 w[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false),
+    const bf162_t w[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false),
                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true),
                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false),
                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true)};
@@ -259,7 +258,7 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
         }
     };
     // `between(slot)`, slot < TM TN: what is issued after the slot's matrix instructions
-    auto multiply = [&](int half, auto phase_c, int phase, auto between) {
+    auto multiply = [&](int half, auto phase_c, auto between) {
         constexpr int PH = decltype(phase_c)::value;
         if constexpr (!kWide) {
 #pragma unroll
@@ -331,7 +330,7 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
         const int cur = PH >= 0 ? PH & 1 : kt & 1;
         if (PH == 0 || (PH < 0 && (kt & 3) == 0)) read_powers(kt >> 2);
         // without a phase the dwords move down a byte a step: byte 0 is always this step's
-        multiply(0, phase_c, kt, [&](int i) {
+        multiply(0, phase_c, [&](int i) {
             if (NEXT) {
 #pragma unroll
                 for (int q = 0; q < kPuts; ++q)
@@ -344,7 +343,7 @@ __device__ __forceinline__ void matmul8_tile(const Mat8Args& a, uint8_t* smem) {
             wait_loads();
             barrier_no_fence();
         }
-        multiply(1, phase_c, kt, [&](int i) {
+        multiply(1, phase_c, [&](int i) {
             if (i == 0 && MORE && (PH == 0 || (PH < 0 && (kt & 3) == 0))) load_powers((kt >> 2) + 1);
             if (MORE) {
 #pragma unroll
