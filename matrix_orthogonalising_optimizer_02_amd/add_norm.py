@@ -233,5 +233,7 @@ def _rows_or_copy(t):
 
 def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """(y, h) of add_rms_norm_forward for torch.autograd: the norm's output, and the residual
-    stream for the next addition (None without a residual)."""
+    stream for the next addition (None without a residual). To capture a backward pass into a HIP
+    graph, call add_rms_norm_forward and add_rms_norm_backward themselves: while an eager graph of
+    the same leaves lives, torch ends a process that captures autograd's backward pass."""
     return _autograd_function().apply(x, residual, weight, eps, weight_offset)

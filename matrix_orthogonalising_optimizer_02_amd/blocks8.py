@@ -282,7 +282,12 @@ class Weight8:
     """A layer's weight [out, in] in 8 bits, as both products that read it want it: `direct`
     for y = x w^T and `transposed` for dx = dy w, a power of two for every 128 x 128 elements.
     Kept between steps; `update` follows the weight after one (HybridOptimizer does it for the
-    weights that it is told of)."""
+    weights that it is told of).
+
+    `version` counts the updates that the host made: linear8's backward pass refuses a form that
+    was updated after its forward pass. An update in a captured graph counts once, at the capture:
+    its replays write new codes and are not seen there, so a step is replayed after the backward
+    passes of the forward passes before it."""
 
     def __init__(self, weight, stream=None):
         if not isinstance(weight, B._torch().Tensor) or weight.dim() != 2:
@@ -367,6 +372,10 @@ def linear8(x, weight, weight8: Weight8 = None, *, products=None, weight_grad_pr
     products, weight_grad_products: matmul8's `products` for the output and x's gradient, and for
     the weight's (8: twice the rate, fewer bits in the sums; None: 16 for a float32 result, 8 for
     others; a 16-bit output whose sums cancel needs 16).
+
+    To capture a backward pass into a HIP graph, call quantise8 and matmul8 themselves: while an
+    eager graph of the same leaves lives, a capture of autograd's backward pass waits for that
+    graph's stream, which a capture does not allow, and torch ends the process.
     """
     torch = B._torch()
     for t, name in ((x, "x"), (weight, "weight")):

@@ -114,7 +114,8 @@ class HybridOptimizer:
 
     weights8: names of 2-D parameters whose 8-bit forms (Weight8, for linear8 and matmul8) the
     optimizer keeps: `weights8[name]` follows the parameter after every step, in one more
-    launch each. Who changes parameters otherwise calls update_weights8().
+    launch each, replayed steps too (Weight8 says what its version does not see of those). Who
+    changes parameters otherwise calls update_weights8().
 
     With adamw_state_bits no gradient is kept after the step that it was given to; who
     captures a step into a graph keeps its gradients for the replays.

@@ -183,7 +183,9 @@ def _autograd_function():
 
 
 def rotary(x, positions, axes: RotaryAxes):
-    """rotary_apply for torch.autograd; positions have no gradient."""
+    """rotary_apply for torch.autograd; positions have no gradient. To capture a backward pass into
+    a HIP graph, call rotary_apply itself, inverse for the gradient: while an eager graph of the
+    same leaves lives, torch ends a process that captures autograd's backward pass."""
     if positions.requires_grad:
         raise ValueError("positions have no gradient")
     return _autograd_function().apply(x, positions, axes)
