@@ -165,9 +165,10 @@ def _autograd_function():
     class Rotary(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, positions, axes):
+            y = rotary_apply(x, positions, axes)  # checks its arguments
             ctx.save_for_backward(positions)
             ctx.axes = axes
-            return rotary_apply(x, positions, axes)
+            return y
 
         @staticmethod
         @torch.autograd.function.once_differentiable
@@ -186,6 +187,6 @@ def rotary(x, positions, axes: RotaryAxes):
     """rotary_apply for torch.autograd; positions have no gradient. To capture a backward pass into
     a HIP graph, call rotary_apply itself, inverse for the gradient: while an eager graph of the
     same leaves lives, torch ends a process that captures autograd's backward pass."""
-    if positions.requires_grad:
+    if getattr(positions, "requires_grad", False):
         raise ValueError("positions have no gradient")
     return _autograd_function().apply(x, positions, axes)

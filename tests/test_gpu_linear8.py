@@ -120,3 +120,29 @@ def test_blocks_of_subnormals(torch_dev):  # noqa: F811
         for got, ref in ((q, x.double().cpu().numpy()), (qt, x.double().cpu().numpy().T)):
             want, e = Q.quantise(ref, tiles)
             assert (e == -127).any() and np.array_equal(got.dequantise().double().cpu().numpy(), want)
+
+
+def test_no_rows_and_one_row(torch_dev):  # noqa: F811
+    """Empty batches through the autograd forms, and inputs that are a single row."""
+    torch, dev = torch_dev
+    w = draw(torch, dev, 514, (30, 40), torch.float32, 0.02).requires_grad_()
+    n = torch.ones(40, device=dev, requires_grad=True)
+    axes = muon.RotaryAxes((2, 3), device=dev)
+    for lead in ((0,), (2, 0)):
+        x = torch.zeros(lead + (40,), device=dev, dtype=torch.bfloat16, requires_grad=True)
+        y, h = muon.add_rms_norm(x, torch.zeros_like(x), n)
+        z = muon.linear8(y, w)
+        q = muon.rotary(z.view(lead + (3, 10)), torch.zeros(lead + (2,), device=dev, dtype=torch.int32), axes)
+        (q.float().sum() + h.float().sum()).backward()
+        torch.cuda.synchronize()
+        assert x.grad.shape == x.shape and z.shape == lead + (30,)
+        assert not w.grad.any() and not n.grad.any() and w.grad.shape == w.shape
+        w.grad = n.grad = None
+    x, w8 = draw(torch, dev, 515, (1, 40), torch.bfloat16), muon.Weight8(w)
+    flat = x[0].clone().requires_grad_()
+    y = muon.linear8(flat, w, w8)
+    y.backward(torch.ones_like(y))
+    want = x.clone().requires_grad_()
+    z = muon.linear8(want, w, w8)
+    z.backward(torch.ones_like(z))
+    assert y.shape == (30,) and torch.equal(y, z[0]) and torch.equal(flat.grad, want.grad[0])
