@@ -2,11 +2,14 @@
 // 2 pi pos[axis(i)] freq(i) of its token:
 //   p' = p cos - q sin,  q' = p sin + q cos
 // and the gradient is the same turned back. The angle's fraction of a turn is worked out in
-// fp64 (a position of 2^20 times a frequency leaves fp32 no digits of it) and the sine and
-// cosine of that fraction in fp32: once for a token and pair, by a block that then turns all
-// heads of its tokens from a table in LDS, the first of them read meanwhile. So the operator is
-// bound by reading and writing its rows once ([8192, 80, 128] bf16 in 66 us, 5.1 TB/s); strides
-// take it to the query and key views of a fused projection, in place too.
+// fp64 (a position of 2^20 times a frequency leaves fp32 no digits of it), the sine and cosine in
+// fp32, of the fraction as fp32 holds it and then of the rest, so that small ones keep their digits
+// ([8192, 80, 128] bf16 65 us with and without the rest, [60000, 1, 128] 14; all in fp64 65 and 18).
+// That is done once for a token and pair, by a block that then turns all heads of its tokens from
+// a table in LDS, the first of them read meanwhile. So the operator is bound by reading and writing
+// its rows once ([8192, 80, 128] bf16 in 65 us, 5.2 TB/s) where a token has many heads; with few, by
+// the table too ([60000, 8, 128] 51, 4.8 TB/s; [60000, 1, 128] 14, 2.1). Strides take it to the query
+// and key views of a fused projection, in place too.
 #include "rows.hpp"
 
 #include <algorithm>
@@ -157,7 +160,13 @@ __global__ __launch_bounds__(kRotThreads) void k_rotary(RotaryArgs a) {
                                              : (double)reinterpret_cast<const float*>(a.pos)[from];
         const double turns = pos * a.freq[p];
         float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        const double half = 2.0 * (turns - rint(turns));
+        const float near = (float)half;
+        sincospif(near, &s, &c);
+        // what the rounding to fp32 left of the angle, by the sine's and cosine's slopes
+        const float left = (float)(3.141592653589793 * (half - near)), slope = c;
+        c = fmaf(-s, left, c);
+        s = fmaf(slope, left, s);
         table[i] = make_float2(c, s * a.sign);
     }
     __syncthreads();
