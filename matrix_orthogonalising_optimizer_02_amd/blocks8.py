@@ -44,8 +44,8 @@ class Blocks8:
     codes: float8_e4m3fn [rows, at least cols rounded up to 128], zeros from cols to there.
     scales: uint8 [rows, at least cols / 128 rounded up, to a multiple of 4], the power of
     each 1 x 128 elements as its exponent + 127; with `tiles` a row for each 128 rows, the
-    power of 128 x 128 elements. A value is code * 2^(scale - 127), NaN for a scale of 255. Rows may lie further
-    apart than they are long.
+    power of 128 x 128 elements. A value is code * 2^(scale - 127), NaN for a scale of 255. Rows
+    may lie further apart than they are long.
     """
 
     __slots__ = ("codes", "scales", "rows", "cols", "tiles")
@@ -368,7 +368,8 @@ def linear8(x, weight, weight8: Weight8 = None, *, products=None, weight_grad_pr
     x [..., in], weight [out, in], each float32, bfloat16 or float16. x and the gradient are
     quantised by 128 elements along what each product sums over; for the weight's gradient x is
     kept in 8 bits. weight8: the weight's 8-bit form, kept up to date by the caller; made in the
-    call without one, transposed too only where x's gradient will need it.
+    call without one, transposed too only where x's gradient will need it. With a form of its own
+    and no gradient the weight's shape alone is used: it may be on another device.
     products, weight_grad_products: matmul8's `products` for the output and x's gradient, and for
     the weight's (8: twice the rate, fewer bits in the sums; None: 16 for a float32 result, 8 for
     others; a 16-bit output whose sums cancel needs 16).
@@ -383,11 +384,14 @@ def linear8(x, weight, weight8: Weight8 = None, *, products=None, weight_grad_pr
             raise TypeError(f"{name} must be a torch.Tensor")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError(f"weight must be 2-D with x's {x.shape[-1] if x.dim() else 0} elements a row")
-    for t, name in ((x, "x"), (weight, "weight")):
-        if t.dtype not in B.dtype_codes():
-            raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    if weight.device != x.device:
-        raise ValueError(f"weight must live on {x.device}")
+    if x.dtype not in B.dtype_codes():
+        raise ValueError("x must be float32, bfloat16 or float16")
+    grads = torch.is_grad_enabled()
+    if weight8 is None or (grads and weight.requires_grad):
+        if weight.dtype not in B.dtype_codes():
+            raise ValueError("weight must be float32, bfloat16 or float16")
+        if weight.device != x.device:
+            raise ValueError(f"weight must live on {x.device}")
     _check_products(products)
     _check_products(weight_grad_products)
     if weight8 is not None:
@@ -395,4 +399,4 @@ def linear8(x, weight, weight8: Weight8 = None, *, products=None, weight_grad_pr
             raise TypeError("weight8 must be a Weight8")
         if weight8.shape != tuple(weight.shape) or weight8.direct.device != x.device:
             raise ValueError(f"weight8 must have shape {tuple(weight.shape)} and live on {x.device}")
-    return _autograd_function().apply(x, weight, weight8, products, weight_grad_products, torch.is_grad_enabled())
+    return _autograd_function().apply(x, weight, weight8, products, weight_grad_products, grads)

@@ -154,9 +154,11 @@ def test_refused_at_the_call(fake):
     """What the backward pass could not do is refused by the forward call."""
     x, w = whole(1, 5, 8), whole(2, 6, 8)
     w8 = muon.Weight8(w)
-    for call, text in ((lambda: muon.linear8(x, w.detach().double(), w8), "weight must be float32"),
+    for call, text in ((lambda: muon.linear8(x, w.detach().double().requires_grad_(), w8), "weight must be float32"),
+                       (lambda: muon.linear8(x, w.detach().double()), "weight must be float32"),
                        (lambda: muon.linear8(x.detach().double(), w, w8), "x must be float32"),
-                       (lambda: muon.linear8(x, w.detach().to("meta"), w8), "weight must live on cpu"),
+                       (lambda: muon.linear8(x, w.detach().to("meta").requires_grad_(), w8), "weight must live on cpu"),
+                       (lambda: muon.linear8(x, w.detach().to("meta")), "weight must live on cpu"),
                        (lambda: muon.linear8(x, w, w8, weight_grad_products=4), "products must be None, 8 or 16")):
         fake.forms.clear()
         with pytest.raises(ValueError, match=text):
@@ -173,3 +175,16 @@ def test_products_of_each_result(fake):
         assert fake.products == want
     with pytest.raises(ValueError, match="products must be None, 8 or 16"):
         muon.linear8(x, w, products=0)
+
+
+def test_a_weight_that_is_its_8_bit_form_alone(fake):
+    """With a kept form and no gradient of its own, a weight lends its shape: the full one may be
+    elsewhere, in any type, or nowhere."""
+    x, w, g = whole(1, 5, 7), whole(2, 6, 7, grad=False), whole(3, 5, 6, grad=False)
+    w8 = muon.Weight8(w)
+    for other in (w.to("meta"), w.double()):
+        x.grad = None
+        muon.linear8(x, other, w8).backward(g)
+        assert torch.equal(x.grad, g @ w)
+    with torch.no_grad():
+        assert torch.equal(muon.linear8(x, w.to("meta").requires_grad_(), w8), x @ w.t())
